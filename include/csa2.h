@@ -352,6 +352,108 @@ csa2_status csa2_sparse_attn_fp4_noalloc(const uint16_t* q_bf16, const uint8_t* 
                                          float softmax_scale, float* out, float* lse,
                                          cudaStream_t stream);
 
+/*
+ * The 8-bit paged KV cache, and the step's batch: for a model's ordinary
+ * attention layers (full or sliding-window, K and V heads shared by groups of
+ * query heads) beside its CSA2 layers.  The pages have no counterpart.
+ *
+ * Cache.  Tokens live in pages of `page` tokens; K and V are E4M3 codes with
+ * one fp32 scale per block, a block being a page's tokens of one head: value =
+ * code * scale.  Scales must be positive and lie in [2^-100, 2^120]
+ * (csa2_kv8_append writes powers of two in that range).
+ *
+ * Batch.  S sequences with rows in this step.  Token j of sequence s is in page
+ * block_table[s][j / page], row j % page.  kv_len[s] counts its tokens, those
+ * of this step included.  Sequence s has rows cu_rows[s] .. cu_rows[s + 1] - 1
+ * of the step's T rows, or, with cu_rows NULL, an equal share (T % S == 0);
+ * row i of its n rows is token kv_len[s] - n + i.  A row whose token would be
+ * negative belongs to no token: it is not written to the cache, reads as
+ * zeros, and sees nothing (so kv_len[s] = 0 makes s an idle slot of a fixed
+ * batch).  Rows of no sequence (past cu_rows[S]) are left as they were.
+ *   Entries that make no sense are skipped and set CSA2_ERR_BAD_INDEX in the
+ * status: a block-table entry outside [0, n_pages) where a token is needed
+ * (nothing is written; reads as zeros; not seen), kv_len[s] < 0 or past
+ * max_pages * page (the tokens past it are skipped), cu_rows that decrease or
+ * leave [0, T] (the sequence has no rows).  Entries for tokens outside a
+ * sliding window are never read.
+ *   Sequences may share pages that the step does not write.
+ * Supported: D in {64, 128}, page in {16, 32, 64, 128}, max_pages * page <= 2^30,
+ * n_pages < 2^31, T <= 2^28, S <= 2^24, H_kv <= 2^14; else
+ * CSA2_ERR_UNSUPPORTED.
+ */
+typedef enum csa2_type { CSA2_BF16 = 0, CSA2_FP16 = 1, CSA2_FP32 = 2 } csa2_type;
+
+typedef struct csa2_kv8_cache {
+  uint8_t* k;        /* E4M3 [n_pages][H_kv][page][D], 16-byte aligned */
+  uint8_t* v;        /* the same */
+  float* k_scale;    /* [n_pages][H_kv] */
+  float* v_scale;    /* [n_pages][H_kv] */
+  int64_t n_pages;
+  int H_kv, page, D;
+} csa2_kv8_cache;
+
+typedef struct csa2_kv8_batch {
+  const int32_t* block_table;  /* [S][max_pages] */
+  const int32_t* kv_len;       /* [S] */
+  const int32_t* cu_rows;      /* [S + 1] or NULL */
+  int S, T, max_pages;
+} csa2_kv8_batch;
+
+/*
+ * csa2_kv8_append -- writes the step's K and V rows into the cache.
+ *   k, v     [T][H_kv][D] of `type` (csa2_type), tokens k_stride / v_stride
+ *            elements apart (>= H_kv * D, a multiple of 16 bytes; 16-byte
+ *            aligned): slices of a joint projection need no copy
+ *   Per block (page, head) the rows [a, b) of the page that this step writes:
+ *   need = 2^e, e the least integer with absmax <= 448 * 2^e, clamped to
+ *   [-100, 120]; the scale becomes max(old scale, need), or need where a = 0 (the
+ *   page starts).  If it grew, the rows [0, a) become E4M3(code * (old /
+ *   new)); the new rows are E4M3(x * (1 / scale)), both to nearest even.
+ *   Bit-exact.  Infinities saturate, a NaN is stored as the E4M3 NaN.  The
+ *   rows of the page past b are left as they were.
+ *   No two of the step's tokens may share a page row, and no two sequences a
+ *   page that the step writes: the contents would depend on timing.
+ *   ws       at least 256 bytes (the status word).
+ */
+csa2_status csa2_kv8_append(const csa2_kv8_cache* cache, const csa2_kv8_batch* batch,
+                            const void* k, const void* v, int type, int64_t k_stride,
+                            int64_t v_stride, void* ws, size_t ws_bytes, cudaStream_t stream);
+
+/*
+ * csa2_kv8_read -- reads the step's rows back: code * scale, formed in fp32
+ * and rounded once to `type`.  With n = kv_len[s] rows a sequence is read
+ * whole.
+ *   k, v     [T][H_kv][D] of `type`, dense, 16-byte aligned
+ *   ws       at least 256 bytes (the status word).
+ */
+csa2_status csa2_kv8_read(const csa2_kv8_cache* cache, const csa2_kv8_batch* batch, void* k,
+                          void* v, int type, void* ws, size_t ws_bytes, cudaStream_t stream);
+
+/*
+ * csa2_kv8_attn -- softmax attention of the step's query rows over their
+ * sequences' tokens in the cache (those of this step are appended before).
+ *   q        [T][H][D], CSA2_BF16 or CSA2_FP16, tokens q_stride elements apart
+ *            (as k_stride above); query head h reads KV head h / (H / H_kv)
+ *   causal   non-zero: row i sees tokens up to its own; zero: all kv_len[s]
+ *   window   0, or (causal only) a row sees its own token and the window - 1
+ *            before it
+ *   out      [T][H][D] of q's type, dense, 16-byte aligned
+ *   lse      fp32 [T][H] log-sum-exp of the scaled logits, or NULL
+ *   A row that sees nothing yields out = 0 and lse = -inf.  The result of a
+ *   call depends on its inputs alone (no atomics).
+ *   ws       at least csa2_kv8_workspace_size(cache, batch, H) bytes, 16-byte
+ *            aligned.
+ * H must be a multiple of H_kv with H / H_kv <= 16 (CSA2_ERR_UNSUPPORTED).
+ */
+csa2_status csa2_kv8_attn(const void* q, int type, int64_t q_stride, int H,
+                          const csa2_kv8_cache* cache, const csa2_kv8_batch* batch, int causal,
+                          int window, float softmax_scale, void* out, float* lse, void* ws,
+                          size_t ws_bytes, cudaStream_t stream);
+
+/* Workspace bytes of csa2_kv8_attn for these sizes (host only; H = 0: enough
+ * for the other two calls).  Depends on the current device's SM count. */
+size_t csa2_kv8_workspace_size(const csa2_kv8_cache* cache, const csa2_kv8_batch* batch, int H);
+
 /* One layer of a CSA2 layer group. */
 typedef struct csa2_layer {
   int mode;                /* csa2_mode */

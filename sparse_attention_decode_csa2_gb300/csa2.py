@@ -61,6 +61,17 @@ class Csa2GroupArgs(ctypes.Structure):
                 ("indexer_fmt", ctypes.c_int), ("q_ready", _vp)]
 
 
+class Csa2Kv8Cache(ctypes.Structure):
+    _fields_ = [("k", _vp), ("v", _vp), ("k_scale", _vp), ("v_scale", _vp),
+                ("n_pages", ctypes.c_int64), ("H_kv", ctypes.c_int), ("page", ctypes.c_int),
+                ("D", ctypes.c_int)]
+
+
+class Csa2Kv8Batch(ctypes.Structure):
+    _fields_ = [("block_table", _vp), ("kv_len", _vp), ("cu_rows", _vp), ("S", ctypes.c_int),
+                ("T", ctypes.c_int), ("max_pages", ctypes.c_int)]
+
+
 INDEXER_E4M3, INDEXER_MXFP4 = 0, 1
 UPLOAD_RAW, UPLOAD_KV_FP4 = 0, 1
 
@@ -106,6 +117,15 @@ _SIGS = {
                                         _vp, _i64, _i32, _vp, _f32, _vp, _vp, _vp, _sz, _vp]),
     "csa2_sparse_attn_fp4_noalloc": (_i32, [_vp, _vp, _i32, _i32, _i32, _i64, _i64, _i32, _vp,
                                             _i32, _f32, _vp, _vp, _vp]),
+    "csa2_kv8_append": (_i32, [ctypes.POINTER(Csa2Kv8Cache), ctypes.POINTER(Csa2Kv8Batch), _vp,
+                               _vp, _i32, _i64, _i64, _vp, _sz, _vp]),
+    "csa2_kv8_read": (_i32, [ctypes.POINTER(Csa2Kv8Cache), ctypes.POINTER(Csa2Kv8Batch), _vp,
+                             _vp, _i32, _vp, _sz, _vp]),
+    "csa2_kv8_attn": (_i32, [_vp, _i32, _i64, _i32, ctypes.POINTER(Csa2Kv8Cache),
+                             ctypes.POINTER(Csa2Kv8Batch), _i32, _i32, _f32, _vp, _vp, _vp, _sz,
+                             _vp]),
+    "csa2_kv8_workspace_size": (_sz, [ctypes.POINTER(Csa2Kv8Cache),
+                                      ctypes.POINTER(Csa2Kv8Batch), _i32]),
     "csa2_layer_group": (_i32, [ctypes.POINTER(Csa2Layer), _i32, ctypes.POINTER(Csa2GroupArgs),
                                 _vp, _sz, _vp]),
     "csa2_layer_group_launches": (_i32, [ctypes.POINTER(Csa2Layer), _i32,
@@ -515,3 +535,182 @@ def layer_group(modes, q_bf16, qi_fp8, kv_fp4, ki_fp8, N, kv_seq_stride, q_per_s
     return LayerGroup(modes, q_bf16, qi_fp8, kv_fp4, ki_fp8, N, kv_seq_stride, q_per_seq, q_pos,
                       ratio, k, pool_size, softmax_scale, pool_block=pool_block, swa_kv=swa_kv,
                       n_win=n_win, indexer_fmt=indexer_fmt)()
+
+
+# ---------------------------------------------------------------------------
+# the 8-bit paged KV cache
+# ---------------------------------------------------------------------------
+
+_KV8_TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+
+
+class Kv8Cache:
+    """A layer's paged cache: E4M3 codes k, v [n_pages][H_kv][page][D] (uint8 or
+    float8_e4m3fn) with fp32 scales [n_pages][H_kv].  Holds the tensors and the
+    prepared C struct; ``Kv8Cache.empty`` allocates them."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor,
+                 v_scale: torch.Tensor):
+        if k.dtype == torch.float8_e4m3fn:
+            k = k.view(torch.uint8)
+        if v.dtype == torch.float8_e4m3fn:
+            v = v.view(torch.uint8)
+        if k.dim() != 4:
+            raise ValueError("k must be [n_pages][H_kv][page][D]")
+        self.k, self.v = _dev(k, torch.uint8, "k"), _out(v, k.shape, torch.uint8, "v")
+        self.n_pages, self.kv_heads, self.page, self.dim = k.shape
+        self.k_scale = _out(k_scale, k.shape[:2], torch.float32, "k_scale")
+        self.v_scale = _out(v_scale, k.shape[:2], torch.float32, "v_scale")
+        self.device = k.device
+        _same_device(self.device, v=v, k_scale=k_scale, v_scale=v_scale)
+        self._c = Csa2Kv8Cache(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), self.n_pages,
+                               self.kv_heads, self.page, self.dim)
+        self._ref = ctypes.byref(self._c)
+
+    @classmethod
+    def empty(cls, n_pages: int, kv_heads: int, page: int, dim: int, device=None) -> "Kv8Cache":
+        shape, dev = (n_pages, kv_heads, page, dim), device or "cuda"
+        return cls(torch.empty(shape, dtype=torch.uint8, device=dev),
+                   torch.empty(shape, dtype=torch.uint8, device=dev),
+                   torch.ones(shape[:2], device=dev), torch.ones(shape[:2], device=dev))
+
+
+class Kv8Batch:
+    """A step's batch: int32 block_table [S][max_pages], kv_len [S] (this step's
+    tokens included), n_rows rows in all, and cu_rows [S + 1] (None: equal
+    shares).  Holds the tensors, whose contents may change between calls."""
+
+    def __init__(self, block_table: torch.Tensor, kv_len: torch.Tensor, n_rows: int,
+                 cu_rows: Optional[torch.Tensor] = None):
+        self.block_table = _dev(block_table, torch.int32, "block_table")
+        if block_table.dim() != 2:
+            raise ValueError("block_table must be [S][max_pages]")
+        S, W = block_table.shape
+        self.kv_len = _out(kv_len, (S,), torch.int32, "kv_len")
+        self.cu_rows = None if cu_rows is None else _out(cu_rows, (S + 1,), torch.int32, "cu_rows")
+        self.seqs, self.n_rows = S, int(n_rows)
+        if self.n_rows < 0 or (cu_rows is None and self.n_rows % max(1, S)):
+            raise ValueError(f"{n_rows} rows are no equal shares of {S} sequences")
+        self.device = block_table.device
+        _same_device(self.device, kv_len=kv_len, cu_rows=cu_rows)
+        self._c = Csa2Kv8Batch(_ptr(block_table), _ptr(kv_len), _ptr(cu_rows), S, self.n_rows, W)
+        self._ref = ctypes.byref(self._c)
+
+
+def _same_device(device, **tensors) -> None:
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} is on {t.device}, not on {device}")
+
+
+def _kv8_rows(t: torch.Tensor, rows: int, heads: Optional[int], dim: int, device, name: str) -> int:
+    """Checks [rows][heads][dim] whose tokens may be strided; returns the token stride."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (there is no CPU path)")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    sh = t.shape
+    if t.dim() != 3 or sh[0] != rows or sh[2] != dim or (heads is not None and sh[1] != heads):
+        raise ValueError(f"{name} must be [{rows}][{heads if heads is not None else 'H'}][{dim}], "
+                         f"got {tuple(sh)}")
+    s0, s1, s2 = t.stride()
+    dense = sh[1] * dim
+    if s2 != 1 or (s1 != dim and sh[1] > 1):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    if rows > 1 and s0 < dense:
+        raise ValueError(f"{name}: tokens must not overlap")
+    return s0 if rows > 1 else dense
+
+
+def _kv8_call(device, where: str, fn, *args) -> None:
+    # the kernels run on the tensors' device, on its current stream
+    if torch.cuda.current_device() == device.index:
+        code = fn(*args, _stream())
+    else:
+        with torch.cuda.device(device):
+            code = fn(*args, _stream())
+    if code:
+        _check(code, where)
+
+
+def make_kv8_workspace(cache: Kv8Cache, batch: Kv8Batch, heads: int = 0) -> torch.Tensor:
+    """Workspace of the kv8 calls (heads > 0: of kv8_attn with that many query heads)."""
+    with torch.cuda.device(cache.device):
+        n = int(lib.csa2_kv8_workspace_size(cache._ref, batch._ref, heads))
+        ws = torch.empty(n, dtype=torch.uint8, device=cache.device)
+        _check(lib.csa2_workspace_init(ws.data_ptr(), n, _stream()), "csa2_workspace_init")
+    return ws
+
+
+def _kv8_ws(cache: Kv8Cache, batch: Kv8Batch, heads: int,
+            ws: Optional[torch.Tensor]) -> torch.Tensor:
+    if batch.device != cache.device:
+        raise ValueError(f"the batch is on {batch.device}, the cache on {cache.device}")
+    if ws is None:
+        return make_kv8_workspace(cache, batch, heads)
+    _dev(ws, torch.uint8, "ws")
+    if ws.device != cache.device:
+        raise ValueError(f"ws is on {ws.device}, not on {cache.device}")
+    return ws
+
+
+def kv8_append(cache: Kv8Cache, batch: Kv8Batch, k: torch.Tensor, v: torch.Tensor,
+               ws: Optional[torch.Tensor] = None) -> None:
+    """Writes the step's K and V rows [n_rows][H_kv][D] (bf16, fp16 or fp32; tokens
+    may be strided) into the cache."""
+    ws = _kv8_ws(cache, batch, 0, ws)
+    if k.dtype not in _KV8_TYPES or v.dtype != k.dtype:
+        raise ValueError(f"k and v must both be bf16, fp16 or fp32, got {k.dtype} and {v.dtype}")
+    ks = _kv8_rows(k, batch.n_rows, cache.kv_heads, cache.dim, cache.device, "k")
+    vs = _kv8_rows(v, batch.n_rows, cache.kv_heads, cache.dim, cache.device, "v")
+    _kv8_call(cache.device, "csa2_kv8_append", lib.csa2_kv8_append, cache._ref, batch._ref,
+              k.data_ptr(), v.data_ptr(), _KV8_TYPES[k.dtype], ks, vs, ws.data_ptr(), ws.numel())
+
+
+def kv8_read(cache: Kv8Cache, batch: Kv8Batch, dtype: torch.dtype = torch.bfloat16,
+             out_k: Optional[torch.Tensor] = None, out_v: Optional[torch.Tensor] = None,
+             ws: Optional[torch.Tensor] = None):
+    """The step's rows read back: (k, v) [n_rows][H_kv][D] of dtype."""
+    ws = _kv8_ws(cache, batch, 0, ws)
+    if dtype not in _KV8_TYPES:
+        raise ValueError(f"dtype must be bf16, fp16 or fp32, got {dtype}")
+    shape = (batch.n_rows, cache.kv_heads, cache.dim)
+    if out_k is None:
+        out_k = torch.empty(shape, dtype=dtype, device=cache.device)
+    if out_v is None:
+        out_v = torch.empty(shape, dtype=dtype, device=cache.device)
+    _out(out_k, shape, dtype, "out_k")
+    _out(out_v, shape, dtype, "out_v")
+    _same_device(cache.device, out_k=out_k, out_v=out_v)
+    _kv8_call(cache.device, "csa2_kv8_read", lib.csa2_kv8_read, cache._ref, batch._ref,
+              out_k.data_ptr(), out_v.data_ptr(), _KV8_TYPES[dtype], ws.data_ptr(), ws.numel())
+    return out_k, out_v
+
+
+def kv8_attn(q: torch.Tensor, cache: Kv8Cache, batch: Kv8Batch, causal: bool = True,
+             window: int = 0, softmax_scale: Optional[float] = None,
+             out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+             ws: Optional[torch.Tensor] = None, want_lse: bool = True):
+    """bf16 or fp16 q [n_rows][H][D] (tokens may be strided) over the sequences'
+    tokens in the cache -> (out [n_rows][H][D] of q's type, fp32 lse [n_rows][H]).
+    Rows past the last sequence's are left as they were (undefined in an out
+    allocated here)."""
+    if q.dtype not in (torch.bfloat16, torch.float16):
+        raise ValueError(f"q must be bf16 or fp16, got {q.dtype}")
+    qs = _kv8_rows(q, batch.n_rows, None, cache.dim, cache.device, "q")
+    T, H, D = q.shape
+    ws = _kv8_ws(cache, batch, H, ws)
+    if softmax_scale is None:
+        softmax_scale = 1.0 / math.sqrt(D)
+    if out is None:
+        out = torch.empty((T, H, D), dtype=q.dtype, device=q.device)
+    else:
+        _same_device(q.device, out=_out(out, (T, H, D), q.dtype, "out"))
+    if lse is not None:
+        _same_device(q.device, lse=_out(lse, (T, H), torch.float32, "lse"))
+    elif want_lse:
+        lse = torch.empty((T, H), dtype=torch.float32, device=q.device)
+    _kv8_call(cache.device, "csa2_kv8_attn", lib.csa2_kv8_attn, q.data_ptr(), _KV8_TYPES[q.dtype],
+              qs, H, cache._ref, batch._ref, 1 if causal else 0, window, softmax_scale,
+              out.data_ptr(), _ptr(lse), ws.data_ptr(), ws.numel())
+    return out, lse

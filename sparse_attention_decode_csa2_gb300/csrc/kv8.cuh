@@ -1,0 +1,100 @@
+// The 8-bit paged KV cache: geometry shared by its kernels (append, read
+// back, attention) and the launchers' declarations.
+#pragma once
+
+#include "csa2_internal.cuh"
+
+namespace csa2 {
+
+// The cache and the step's batch as the kernels see them (validated by the C
+// ABI: page is 1 << page_shift in 16..128, max_pages << page_shift < 2^31).
+struct Kv8Args {
+  uint8_t* k;
+  uint8_t* v;
+  float* k_scale;
+  float* v_scale;
+  int64_t n_pages;
+  const int32_t* table;
+  const int32_t* kv_len;
+  const int32_t* cu;  // null: T / S rows for every sequence
+  int32_t* status;
+  int H_kv, D, page_shift, S, T, max_pages;
+};
+
+// A sequence's rows of the step.  Row i (of n) is token len - n + i; tokens
+// below zero do not exist (their rows belong to no token).  A sequence whose
+// entries make no sense has no rows (`bad`).
+struct Kv8Seq {
+  int row0, n, len;
+  bool bad;
+};
+
+__device__ __forceinline__ Kv8Seq kv8_seq(const Kv8Args& a, int s) {
+  Kv8Seq q;
+  if (a.cu) {
+    const int r0 = a.cu[s], r1 = a.cu[s + 1];
+    q.bad = r0 < 0 || r1 < r0 || r1 > a.T;
+    q.row0 = q.bad ? 0 : r0;
+    q.n = q.bad ? 0 : r1 - r0;
+  } else {
+    q.n = a.T / a.S;
+    q.row0 = s * q.n;
+    q.bad = false;
+  }
+  q.len = a.kv_len[s];
+  // a length past the block table: the tokens the table has no entry for are skipped
+  q.bad = q.bad || q.len < 0 || q.len > (int)((int64_t)a.max_pages << a.page_shift);
+  if (q.len < 0) q.len = 0;
+  return q;
+}
+
+// Raises the bad-index bit if any sequence's entries make no sense (one
+// block's threads look at all of them).
+__device__ __forceinline__ void kv8_check_batch(const Kv8Args& a) {
+  bool bad = false;
+  for (int s = threadIdx.x; s < a.S; s += blockDim.x) bad |= kv8_seq(a, s).bad;
+  if (bad) set_status(a.status, kStatusBadIndex);
+}
+
+// Page id of column `col` (< max_pages) of sequence s, or -1 (and the
+// bad-index bit) for an entry outside the cache.
+__device__ __forceinline__ int64_t kv8_page(const Kv8Args& a, int s, int col) {
+  const int32_t p = a.table[(int64_t)s * a.max_pages + col];
+  if (p >= 0 && p < a.n_pages) return p;
+  set_status(a.status, kStatusBadIndex);
+  return -1;
+}
+
+// 2^e for whole e in [-126, 127], and 1 / 2^e's exponent arithmetic from bits.
+__device__ __forceinline__ float pow2f(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+
+__device__ __forceinline__ float2 e4m3x2_to_float2(uint16_t v) {
+  return half2_bits_to_float2(e4m3x2_to_f16x2(v));
+}
+
+// Two floats -> two E4M3 bytes (low byte = lo), nearest even, saturating.
+__device__ __forceinline__ uint32_t f32x2_to_e4m3x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+cudaError_t launch_kv8_append(const Kv8Args& a, const void* k, const void* v, int type,
+                              int64_t k_stride, int64_t v_stride, cudaStream_t stream);
+cudaError_t launch_kv8_read(const Kv8Args& a, void* k, void* v, int type, cudaStream_t stream);
+
+struct Kv8AttnArgs {
+  Kv8Args c;
+  const void* q;       // [T][H][D], token stride q_stride elements
+  int64_t q_stride;
+  void* out;           // [T][H][D], q's type
+  float* lse;          // [T][H] or null
+  int H, G, causal, window;
+  float scale_log2;    // softmax scale * log2(e)
+  uint8_t* scratch;    // kv8_attn_scratch_bytes(...)
+};
+
+size_t kv8_attn_scratch_bytes(int S, int T, int H, int H_kv, int D);
+cudaError_t launch_kv8_attn(const Kv8AttnArgs& a, int type, cudaStream_t stream);
+
+}  // namespace csa2

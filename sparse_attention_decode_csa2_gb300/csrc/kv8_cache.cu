@@ -1,0 +1,404 @@
+// The 8-bit paged KV cache's writer and reader.
+//
+// Cache: E4M3 codes [n_pages][H_kv][page][D] for K and for V, one fp32 scale
+// per page and head.  The scale of a block (a page's tokens of one head) is
+// the power of two 2^e with the least e such that absmax <= 448 * 2^e.  E4M3
+// is a floating-point format, so any scale keeps the same relative precision
+// above its subnormals; a power of two makes x / scale and a later change of
+// scale exact, and the only rounding left is that to the 3-bit mantissa.
+//
+// A page fills over several steps.  Its scale only grows: when a step's rows
+// need a larger one, the rows that the page holds are decoded, divided and
+// rounded again (exact except where a code becomes subnormal).  A step that
+// writes a page's first token starts the scale anew, whatever the page held.
+//
+// One team of threads (a warp for a few rows per sequence, else a block of
+// 256) owns the rows of one (sequence, page, head) of K or V: it reads them
+// once into registers, reduces absmax, settles the scale and stores the codes.
+// No two teams touch the same block, so there are no atomics.
+#include <cuda_bf16.h>
+
+#include "kv8.cuh"
+
+namespace csa2 {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kEMin = -100, kEMax = 120;  // scale exponents
+
+template <typename T>
+struct Vec16;  // 16 consecutive values
+template <>
+struct Vec16<float> {
+  float4 r[4];
+  __device__ __forceinline__ void load(const float* p) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r[i] = __ldg(reinterpret_cast<const float4*>(p) + i);
+  }
+  __device__ __forceinline__ void get(float* x) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[4 * i] = r[i].x;
+      x[4 * i + 1] = r[i].y;
+      x[4 * i + 2] = r[i].z;
+      x[4 * i + 3] = r[i].w;
+    }
+  }
+};
+template <typename T>
+struct Vec16Half {
+  uint4 r[2];
+  __device__ __forceinline__ void load(const T* p) {
+    r[0] = __ldg(reinterpret_cast<const uint4*>(p));
+    r[1] = __ldg(reinterpret_cast<const uint4*>(p) + 1);
+  }
+  __device__ __forceinline__ void get(float* x) const;
+};
+template <>
+__device__ __forceinline__ void Vec16Half<__nv_bfloat16>::get(float* x) const {
+  const uint32_t w[8] = {r[0].x, r[0].y, r[0].z, r[0].w, r[1].x, r[1].y, r[1].z, r[1].w};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    x[2 * i] = __uint_as_float(w[i] << 16);
+    x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+  }
+}
+template <>
+__device__ __forceinline__ void Vec16Half<__half>::get(float* x) const {
+  const uint32_t w[8] = {r[0].x, r[0].y, r[0].z, r[0].w, r[1].x, r[1].y, r[1].z, r[1].w};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float2 f = half2_bits_to_float2(w[i]);
+    x[2 * i] = f.x;
+    x[2 * i + 1] = f.y;
+  }
+}
+template <>
+struct Vec16<__nv_bfloat16> : Vec16Half<__nv_bfloat16> {};
+template <>
+struct Vec16<__half> : Vec16Half<__half> {};
+
+// Least e with amax <= 448 * 2^e (448 = 1.75 * 2^8), clamped; infinity gives kEMax.
+__device__ __forceinline__ int scale_exponent(float amax) {
+  if (!(amax > 0.0f)) return kEMin;
+  int m_bits = (int)(__float_as_uint(amax) & 0x7FFFFFu);
+  const int E = (int)(__float_as_uint(amax) >> 23) - 127;  // -127: subnormal, far below kEMin
+  int e = E - 8 + (m_bits > 0x600000 ? 1 : 0);
+  return e < kEMin ? kEMin : (e > kEMax ? kEMax : e);
+}
+
+// 16 codes of the values x * inv.
+__device__ __forceinline__ uint4 encode16(const float* x, float inv) {
+  uint32_t o[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    o[i] = f32x2_to_e4m3x2(x[4 * i] * inv, x[4 * i + 1] * inv) |
+           (f32x2_to_e4m3x2(x[4 * i + 2] * inv, x[4 * i + 3] * inv) << 16);
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+__device__ __forceinline__ void decode16(uint4 c, float* x) {
+  const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 a = e4m3x2_to_float2((uint16_t)(w[i] & 0xFFFFu));
+    const float2 b = e4m3x2_to_float2((uint16_t)(w[i] >> 16));
+    x[4 * i] = a.x;
+    x[4 * i + 1] = a.y;
+    x[4 * i + 2] = b.x;
+    x[4 * i + 3] = b.y;
+  }
+}
+
+// Work items: (slot, head, K or V).  Each sequence has enough slots for the
+// pages its rows can touch: n rows touch at most (n + page - 2) / page + 1
+// pages.  With equal shares that is the count; with cu, sequence s owns slots
+// [cu[s] / page + 2 s, cu[s + 1] / page + 2 s + 2), which is at least as many
+// and needs no prefix sum, so a slot finds its sequence by bisection.
+__host__ __device__ inline int64_t slots_of(int S, int T, bool cu, int page_shift) {
+  const int64_t page = (int64_t)1 << page_shift;
+  if (cu) return ((int64_t)T >> page_shift) + 2 * (int64_t)S;
+  const int64_t n = T / S;
+  return (int64_t)S * ((n + page - 2) / page + 1);
+}
+
+// The rows of the step that a slot stands for: page column `col` of sequence
+// s, tokens [pos, pos + rows), the first of them row `row` of the step.
+// rows = 0: nothing to do.
+struct Slot {
+  int s, j, col, pos, rows, row;
+  Kv8Seq q;
+};
+
+__device__ __forceinline__ Slot find_slot(const Kv8Args& a, int64_t slot) {
+  Slot r;
+  if (a.cu) {
+    // last s with clamp(cu[s]) / page + 2 s <= slot, 32 candidates a round
+    // (every lane of a warp has the same slot)
+    const int lane = threadIdx.x & 31;
+    int lo = 0, hi = a.S;  // key(lo) <= slot (key(0) >= 0 is checked below)
+    while (hi - lo > 1) {
+      const int step = (hi - lo + 31) / 32;
+      const int c = lo + (lane + 1) * step;
+      bool le = false;
+      if (c < hi) {
+        const int cu = min(max(a.cu[c], 0), a.T);
+        le = ((int64_t)(cu >> a.page_shift) + 2 * (int64_t)c) <= slot;
+      }
+      const uint32_t m = __ballot_sync(0xffffffffu, le);
+      const int k = m == 0 ? 0 : 32 - __clz(m);  // highest candidate that is not past the slot
+      const int nlo = lo + k * step;
+      hi = min(hi, nlo + step);
+      lo = nlo;
+    }
+    r.s = lo;
+    const int cu = min(max(a.cu[lo], 0), a.T);
+    const int64_t j = slot - ((int64_t)(cu >> a.page_shift) + 2 * (int64_t)lo);
+    r.j = j < 0 || j > INT32_MAX ? INT32_MAX : (int)j;
+  } else {
+    const int64_t page = (int64_t)1 << a.page_shift;
+    const int64_t per = ((int64_t)(a.T / a.S) + page - 2) / page + 1;
+    r.s = (int)(slot / per);
+    r.j = (int)(slot % per);
+  }
+  r.q = kv8_seq(a, r.s);
+  const int cap = (int)min((int64_t)r.q.len, (int64_t)a.max_pages << a.page_shift);
+  const int64_t first = (int64_t)r.q.len - r.q.n;  // token of the sequence's row 0
+  const int p0 = first < 0 ? 0 : (int)first;
+  const int64_t col = (int64_t)(p0 >> a.page_shift) + r.j;
+  r.col = col >= a.max_pages ? a.max_pages : (int)col;
+  const int64_t start = col << a.page_shift, end = start + ((int64_t)1 << a.page_shift);
+  const int64_t lo = start > p0 ? start : p0, hi = end < cap ? end : cap;
+  r.pos = (int)(lo < cap ? lo : cap);
+  r.rows = r.q.n > 0 && r.col < a.max_pages && hi > lo ? (int)(hi - lo) : 0;
+  r.row = r.q.row0 + (int)(lo - first);
+  return r;
+}
+
+template <int kTeam>
+__device__ __forceinline__ float team_max(float x, float* red) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+  if (kTeam > 32) {
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = x;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kTeam / 32; ++i) x = fmaxf(x, red[i]);
+  }
+  return x;
+}
+
+template <typename T, int kTeam>
+__global__ void __launch_bounds__(kThreads)
+kv8_append_kernel(const __grid_constant__ Kv8Args a, const T* __restrict__ k,
+                  const T* __restrict__ v, int64_t k_stride, int64_t v_stride, int64_t items) {
+  __shared__ float red[kThreads / 32];
+  if (blockIdx.x == 0) kv8_check_batch(a);
+  const int64_t item = (int64_t)blockIdx.x * (kThreads / kTeam) + threadIdx.x / kTeam;
+  if (item >= items) return;
+  const int t = threadIdx.x % kTeam;
+  const bool is_v = item & 1;
+  const int h = (int)((item >> 1) % a.H_kv);
+  const Slot sl = find_slot(a, (item >> 1) / a.H_kv);
+  if (sl.rows == 0) return;
+  const int64_t page_id = kv8_page(a, sl.s, sl.col);
+  if (page_id < 0) return;
+  const int D = a.D, cpr = D / 16;  // 16-value chunks per row
+  const int off = sl.pos & ((1 << a.page_shift) - 1);
+  const int64_t stride = is_v ? v_stride : k_stride;
+  const T* src = (is_v ? v : k) + (int64_t)sl.row * stride + (int64_t)h * D;
+  uint8_t* blk = (is_v ? a.v : a.k) + ((page_id * a.H_kv + h) << a.page_shift) * D;
+  float* scale = (is_v ? a.v_scale : a.k_scale) + page_id * a.H_kv + h;
+
+  // one pass over the rows: the first kHold chunks of a thread stay in
+  // registers (a whole page at 256 threads), the rest are read again
+  constexpr int kHold = 4;
+  Vec16<T> held[kHold];
+  const int chunks = sl.rows * cpr;
+  const int shift = D == 128 ? 3 : 2;
+  auto at = [&](int c) { return src + (int64_t)(c >> shift) * stride + (c & (cpr - 1)) * 16; };
+  float amax = 0.0f;
+  auto take = [&](const Vec16<T>& w) {
+    float x[16];
+    w.get(x);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(x[i]));
+  };
+#pragma unroll
+  for (int i = 0; i < kHold; ++i)
+    if (t + i * kTeam < chunks) held[i].load(at(t + i * kTeam));
+  const float old = off > 0 ? *scale : 0.0f;  // a page that starts forgets its scale
+#pragma unroll
+  for (int i = 0; i < kHold; ++i)
+    if (t + i * kTeam < chunks) take(held[i]);
+  for (int c = t + kHold * kTeam; c < chunks; c += kTeam) {
+    Vec16<T> w;
+    w.load(at(c));
+    take(w);
+  }
+  amax = team_max<kTeam>(amax, red);  // every thread has read the old scale by here
+  const float need = pow2f(scale_exponent(amax));
+  const float sc = fmaxf(old, need), inv = 1.0f / sc;
+
+  uint8_t* dst = blk + (int64_t)off * D;
+  auto put = [&](int c, const Vec16<T>& w) {
+    float x[16];
+    w.get(x);
+    *reinterpret_cast<uint4*>(dst + (int64_t)c * 16) = encode16(x, inv);
+  };
+#pragma unroll
+  for (int i = 0; i < kHold; ++i)
+    if (t + i * kTeam < chunks) put(t + i * kTeam, held[i]);
+  for (int c = t + kHold * kTeam; c < chunks; c += kTeam) {
+    Vec16<T> w;
+    w.load(at(c));
+    put(c, w);
+  }
+  if (off > 0 && sc > old) {  // the rows that the page held
+    const float r = old * inv;
+    for (int c = t; c < off * cpr; c += kTeam) {
+      uint4* p = reinterpret_cast<uint4*>(blk) + c;
+      float x[16];
+      decode16(*p, x);
+      *p = encode16(x, r);
+    }
+  }
+  __syncwarp();
+  if (t == 0 && sc != old) *scale = sc;
+}
+
+template <typename T>
+__device__ __forceinline__ void store16(T* p, const float* x);
+template <>
+__device__ __forceinline__ void store16<float>(float* p, const float* x) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    reinterpret_cast<float4*>(p)[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+}
+template <>
+__device__ __forceinline__ void store16<__half>(__half* p, const float* x) {
+  uint32_t w[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const __half2 h = __floats2half2_rn(x[2 * i], x[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  reinterpret_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+  reinterpret_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+}
+template <>
+__device__ __forceinline__ void store16<__nv_bfloat16>(__nv_bfloat16* p, const float* x) {
+  uint32_t w[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  reinterpret_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+  reinterpret_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+}
+
+// Values of the step's rows: code * scale, rounded once to T.  Teams and
+// items as the writer's; rows of tokens below zero, and of pages outside the
+// cache, read as zeros.
+template <typename T, int kTeam>
+__global__ void __launch_bounds__(kThreads)
+kv8_read_kernel(const __grid_constant__ Kv8Args a, T* __restrict__ k, T* __restrict__ v,
+                int64_t items) {
+  if (blockIdx.x == 0) kv8_check_batch(a);
+  const int64_t item = (int64_t)blockIdx.x * (kThreads / kTeam) + threadIdx.x / kTeam;
+  if (item >= items) return;
+  const int t = threadIdx.x % kTeam;
+  const bool is_v = item & 1;
+  const int h = (int)((item >> 1) % a.H_kv);
+  const Slot sl = find_slot(a, (item >> 1) / a.H_kv);
+  const int D = a.D, cpr = D / 16, shift = D == 128 ? 3 : 2;
+  const int64_t stride = (int64_t)a.H_kv * D;
+  T* out = (is_v ? v : k) + (int64_t)h * D;
+  auto dst = [&](int row, int64_t c) {
+    return out + (row + (c >> shift)) * stride + (c & (cpr - 1)) * 16;
+  };
+  if (sl.j == 0) {  // rows without a token, or past the block table
+    const float zero[16] = {};
+    const int64_t cap = (int64_t)a.max_pages << a.page_shift;
+    const int before = min(sl.q.n, max(0, sl.q.n - sl.q.len));
+    for (int64_t c = t; c < (int64_t)before * cpr; c += kTeam) store16<T>(dst(sl.q.row0, c), zero);
+    const int past = (int)min((int64_t)sl.q.n, max((int64_t)0, (int64_t)sl.q.len - cap));
+    for (int64_t c = t; c < (int64_t)past * cpr; c += kTeam)
+      store16<T>(dst(sl.q.row0 + sl.q.n - past, c), zero);
+  }
+  if (sl.rows == 0) return;
+  const int64_t page_id = kv8_page(a, sl.s, sl.col);
+  const int off = sl.pos & ((1 << a.page_shift) - 1);
+  const int64_t b = (page_id < 0 ? 0 : page_id) * a.H_kv + h;
+  const uint8_t* src = (is_v ? a.v : a.k) + ((b << a.page_shift) + off) * D;
+  const float sc = page_id < 0 ? 0.0f : (is_v ? a.v_scale : a.k_scale)[b];
+  for (int c = t; c < sl.rows * cpr; c += kTeam) {
+    float x[16];
+    decode16(page_id < 0 ? make_uint4(0, 0, 0, 0)
+                         : __ldg(reinterpret_cast<const uint4*>(src) + c), x);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) x[i] *= sc;
+    store16<T>(dst(sl.row, c), x);
+  }
+}
+
+// A warp per item where the sequences have few rows on average, else a block.
+constexpr int kFewRows = 8;
+
+inline bool few_rows(const Kv8Args& a) { return (int64_t)a.T <= (int64_t)kFewRows * a.S; }
+
+template <typename T>
+cudaError_t append_t(const Kv8Args& a, const void* k, const void* v, int64_t ks, int64_t vs,
+                     cudaStream_t stream) {
+  const int64_t items = slots_of(a.S, a.T, a.cu != nullptr, a.page_shift) * a.H_kv * 2;
+  const T* kp = static_cast<const T*>(k);
+  const T* vp = static_cast<const T*>(v);
+  if (few_rows(a)) {
+    const int64_t blocks = (items + 7) / 8;
+    if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
+    kv8_append_kernel<T, 32><<<(unsigned)blocks, kThreads, 0, stream>>>(a, kp, vp, ks, vs, items);
+  } else {
+    if (items > INT32_MAX) return cudaErrorInvalidConfiguration;
+    kv8_append_kernel<T, kThreads><<<(unsigned)items, kThreads, 0, stream>>>(a, kp, vp, ks, vs,
+                                                                            items);
+  }
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t read_t(const Kv8Args& a, void* k, void* v, cudaStream_t stream) {
+  const int64_t items = slots_of(a.S, a.T, a.cu != nullptr, a.page_shift) * a.H_kv * 2;
+  T* kp = static_cast<T*>(k);
+  T* vp = static_cast<T*>(v);
+  if (few_rows(a)) {
+    const int64_t blocks = (items + 7) / 8;
+    if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
+    kv8_read_kernel<T, 32><<<(unsigned)blocks, kThreads, 0, stream>>>(a, kp, vp, items);
+  } else {
+    if (items > INT32_MAX) return cudaErrorInvalidConfiguration;
+    kv8_read_kernel<T, kThreads><<<(unsigned)items, kThreads, 0, stream>>>(a, kp, vp, items);
+  }
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_kv8_append(const Kv8Args& a, const void* k, const void* v, int type,
+                              int64_t k_stride, int64_t v_stride, cudaStream_t stream) {
+  switch (type) {
+    case CSA2_BF16: return append_t<__nv_bfloat16>(a, k, v, k_stride, v_stride, stream);
+    case CSA2_FP16: return append_t<__half>(a, k, v, k_stride, v_stride, stream);
+    default: return append_t<float>(a, k, v, k_stride, v_stride, stream);
+  }
+}
+
+cudaError_t launch_kv8_read(const Kv8Args& a, void* k, void* v, int type, cudaStream_t stream) {
+  switch (type) {
+    case CSA2_BF16: return read_t<__nv_bfloat16>(a, k, v, stream);
+    case CSA2_FP16: return read_t<__half>(a, k, v, stream);
+    default: return read_t<float>(a, k, v, stream);
+  }
+}
+
+}  // namespace csa2
