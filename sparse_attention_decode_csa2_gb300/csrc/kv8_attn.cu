@@ -32,185 +32,35 @@
 // contraction is permuted so that a lane's 16 bytes are its four k-steps), V
 // fragments come from transposing matrix loads of byte pairs, both converted in
 // registers (E4M3 -> fp16 is one instruction for two values).
-#include <cuda_bf16.h>
-
-#include "kv8.cuh"
+#include "kv8_sched.cuh"
 
 namespace csa2 {
 namespace {
 
-constexpr int kRows = 16;            // query rows of a unit
+using namespace kv8;
+
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-constexpr int kWarpKeys = 32;
-constexpr int kGranule = kWarps * kWarpKeys;  // keys
-constexpr float kHeadroom = 15.0f;            // log2 of the largest weight
+constexpr int kTileKeys = 32;
+constexpr float kHeadroom = 15.0f;  // log2 of the largest weight
 
-template <int D>
+// kRg warps share a tile's keys, 16 query rows each; 4 / kRg groups of warps
+// have rings of their own.  The ring of a CTA has the same size for every kRg.
+template <int D, int kRg>
 struct Cfg {
-  static constexpr int stages = D == 128 ? 3 : 4;
-  static constexpr int tile = kWarpKeys * D;               // bytes of K (or V) of a stage
+  static constexpr int unit = 16 * kRg;                    // query rows
+  static constexpr int kgs = kWarps / kRg;                 // key groups
+  static constexpr int granule = kgs * kTileKeys;          // keys
+  static constexpr int stages = (D == 128 ? 3 : 4) * kRg;
+  static constexpr int tile = kTileKeys * D;               // bytes of K (or V) of a stage
   static constexpr int stage = 2 * tile;
-  static constexpr int ring = kWarps * stages * stage;
-  static constexpr int scales = kWarps * stages * 16;      // ks, vs of two 16-key halves
+  static constexpr int ring = kgs * stages * stage;
+  static constexpr int scales = kgs * stages * 16;         // ks, vs of two 16-key halves
   static constexpr int smem = ring + scales;
   static constexpr int ctas = D == 128 ? 2 : 3;            // per SM
-  static_assert(ring >= kWarps * kRows * D * 4, "the merge of the warps reuses the ring");
+  static_assert(ring >= kWarps * 16 * D * 4, "the merge of the warps reuses the ring");
+  static_assert(stages <= 16, "two bits a stage in a word");
 };
-
-constexpr float kLn2 = 0.69314718055994530942f;
-
-// One part of a cut unit in scratch: O [16][D], max [16], sum [16].
-__host__ __device__ constexpr size_t part_floats(int D) { return (size_t)kRows * D + 2 * kRows; }
-
-struct Dims {
-  int n, row0, len, cap;   // the sequence's rows and tokens; tokens the table has room for
-  int tpm, nm;             // tokens per unit, units per KV head
-};
-
-__device__ __forceinline__ Dims seq_dims(const Kv8AttnArgs& a, int s) {
-  const Kv8Seq q = kv8_seq(a.c, s);
-  Dims d;
-  d.n = q.n;
-  d.row0 = q.row0;
-  d.len = q.len;
-  d.cap = (int)min((int64_t)q.len, (int64_t)a.c.max_pages << a.c.page_shift);
-  d.tpm = kRows / a.G;
-  d.nm = (q.n + d.tpm - 1) / d.tpm;
-  return d;
-}
-
-// Tokens [lo, hi) that some row of unit m sees, and the granules that cover them.
-struct Span {
-  int lo, hi, g0, ng;
-};
-
-__device__ __forceinline__ Span unit_span(const Kv8AttnArgs& a, const Dims& d, int m) {
-  Span u;
-  u.lo = 0;
-  u.hi = d.cap;
-  if (a.causal) {
-    const int i0 = m * d.tpm, i1 = min(d.n, i0 + d.tpm);
-    const int64_t p0 = (int64_t)d.len - d.n + i0, p1 = (int64_t)d.len - d.n + i1 - 1;
-    u.hi = (int)max((int64_t)0, min((int64_t)d.cap, p1 + 1));
-    if (a.window > 0) u.lo = (int)max((int64_t)0, p0 - a.window + 1);
-  }
-  if (u.lo > u.hi) u.lo = u.hi;
-  u.g0 = u.lo / kGranule;
-  u.ng = max(1, (u.hi + kGranule - 1) / kGranule - u.g0);  // one at least: it writes the rows
-  return u;
-}
-
-__device__ __forceinline__ int64_t seq_work(const Kv8AttnArgs& a, const Dims& d) {
-  if (!a.causal) return (int64_t)a.c.H_kv * d.nm * unit_span(a, d, 0).ng;
-  int64_t w = 0;
-  for (int m = 0; m < d.nm; ++m) w += unit_span(a, d, m).ng;
-  return w * a.c.H_kv;
-}
-
-// The CTA's range [w0, w1) of the batch's granules, and the sequence that
-// holds granule w0 with the offset inside it.
-struct Range {
-  int64_t w0, w1, rem, total;
-  int s, workers;  // workers that have a range (no more than there are granules)
-};
-
-struct RangeSmem {
-  int64_t warp_sum[kWarps];
-  int64_t rem;
-  int s;
-};
-
-__device__ Range find_range(const Kv8AttnArgs& a, int worker, int workers, RangeSmem& sm) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int per = (a.c.S + kThreads - 1) / kThreads;
-  const int s0 = min(a.c.S, tid * per), s1 = min(a.c.S, s0 + per);
-  int64_t mine = 0, first = 0;
-  for (int s = s0; s < s1; ++s) {
-    const int64_t w = seq_work(a, seq_dims(a, s));
-    if (s == s0) first = w;
-    mine += w;
-  }
-  int64_t inc = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t y = __shfl_up_sync(0xffffffffu, inc, o);
-    if (lane >= o) inc += y;
-  }
-  if (lane == 31) sm.warp_sum[warp] = inc;
-  if (tid == 0) sm.s = -1;
-  __syncthreads();
-  int64_t base = 0, total = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    if (w < warp) base += sm.warp_sum[w];
-    total += sm.warp_sum[w];
-  }
-  Range r;
-  r.total = total;
-  r.workers = (int)min((int64_t)workers, total);
-  r.w0 = r.w1 = 0;
-  if (worker < r.workers) {
-    r.w0 = total * worker / r.workers;
-    r.w1 = total * (worker + 1) / r.workers;
-  }
-  int64_t at = base + inc - mine;  // granules before this thread's sequences
-  if (r.w0 < r.w1 && r.w0 >= at && r.w0 < at + mine) {
-    for (int s = s0; s < s1; ++s) {
-      const int64_t w = s == s0 ? first : seq_work(a, seq_dims(a, s));
-      if (r.w0 < at + w) {
-        sm.s = s;
-        sm.rem = r.w0 - at;
-        break;
-      }
-      at += w;
-    }
-  }
-  __syncthreads();
-  r.s = sm.s;
-  r.rem = sm.rem;
-  return r;
-}
-
-// Walks the units of a range: unit m, head h of sequence s, granules
-// [t0, t1) of its span.
-struct Walk {
-  int s, m, h, t0, t1;
-  Dims d;
-  Span u;
-};
-
-// Places the walk at offset `rem` of sequence s.
-__device__ __forceinline__ void walk_to(const Kv8AttnArgs& a, Walk& w, int s, int64_t rem) {
-  w.s = s;
-  w.d = seq_dims(a, s);
-  for (w.m = 0;; ++w.m) {
-    w.u = unit_span(a, w.d, w.m);
-    const int64_t all = (int64_t)w.u.ng * a.c.H_kv;
-    if (rem < all || w.m + 1 >= w.d.nm) break;
-    rem -= all;
-  }
-  w.h = (int)(rem / w.u.ng);
-  w.t0 = (int)(rem % w.u.ng);
-}
-
-// To the unit after this one (false past the last sequence).
-__device__ __forceinline__ bool walk_next(const Kv8AttnArgs& a, Walk& w) {
-  w.t0 = 0;
-  if (++w.h < a.c.H_kv) return true;
-  w.h = 0;
-  if (++w.m < w.d.nm) {
-    w.u = unit_span(a, w.d, w.m);
-    return true;
-  }
-  w.m = 0;
-  do {
-    if (++w.s >= a.c.S) return false;
-    w.d = seq_dims(a, w.s);
-  } while (w.d.nm == 0);
-  w.u = unit_span(a, w.d, 0);
-  return true;
-}
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
   return (uint32_t)__cvta_generic_to_shared(p);
@@ -238,31 +88,6 @@ __device__ __forceinline__ void mma16816(float* c, const uint32_t* x, uint32_t b
       : "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(b0), "r"(b1));
 }
 
-// 2^x by the hardware's approximation (relative error about 2^-22).
-__device__ __forceinline__ float ex2(float x) {
-  float r;
-  asm("ex2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-  const __half2 h = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-
-template <bool kBf16>
-__device__ __forceinline__ float2 pair_to_float2(uint32_t w) {
-  if (kBf16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
-  return half2_bits_to_float2(w);
-}
-template <bool kBf16>
-__device__ __forceinline__ uint32_t pair_from_floats(float lo, float hi) {
-  if (kBf16) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&h);
-  }
-  return pack_f16(lo, hi);
-}
-
 // Byte offset of 16-byte chunk ch of key r in a tile: 128-byte lines, chunks
 // exclusive-or'ed with the line so that eight lanes reading one chunk of eight
 // keys, or all chunks of two keys, meet eight different banks.
@@ -279,32 +104,40 @@ __device__ __forceinline__ int key_of(int n) {
   return D == 128 ? (n >> 1) | ((n & 1) << 2) : n;
 }
 
-template <int D, bool kBf16>
-__global__ void __launch_bounds__(kThreads, Cfg<D>::ctas)
+// The warps of key group kg.
+template <int kRg>
+__device__ __forceinline__ void group_sync(int kg) {
+  if (kRg == 1)
+    __syncwarp();
+  else
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + kg), "n"(kRg * 32) : "memory");
+}
+
+template <int D, int kRg, bool kBf16>
+__global__ void __launch_bounds__(kThreads, Cfg<D, kRg>::ctas)
 kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a) {
-  using C = Cfg<D>;
+  using C = Cfg<D, kRg>;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ RangeSmem rsm;
-  __shared__ float row_max[kWarps][kRows], row_sum[kWarps][kRows];
+  __shared__ RangeSmem<kWarps> rsm;
+  __shared__ float row_max[C::kgs][C::unit], row_sum[C::kgs][C::unit];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, c = lane & 3;
+  const int kg = warp / kRg, rq = warp % kRg;  // key group, row group
   pdl_trigger();
   if (blockIdx.x == 0) kv8_check_batch(a.c);
-  const Range rg = find_range(a, blockIdx.x, gridDim.x, rsm);
+  const Range rg = find_range<C::unit, C::granule, kWarps>(a, blockIdx.x, gridDim.x, rsm);
   if (rg.s < 0) return;
 
-  uint8_t* ring = smem + warp * (C::stages * C::stage);
-  float* ring_scale = reinterpret_cast<float*>(smem + C::ring) + warp * (C::stages * 4);
+  uint8_t* ring = smem + kg * (C::stages * C::stage);
+  float* ring_scale = reinterpret_cast<float*>(smem + C::ring) + kg * (C::stages * 4);
   const uint32_t ring_u = smem_u32(ring), scale_u = smem_u32(ring_scale);
   const int page_mask = (1 << a.c.page_shift) - 1;
-  float* part = reinterpret_cast<float*>(a.scratch) + (size_t)blockIdx.x * 2 * part_floats(D);
+  float* part =
+      reinterpret_cast<float*>(a.scratch) + (size_t)blockIdx.x * 2 * part_floats(C::unit, D);
 
-  Walk w;
-  walk_to(a, w, rg.s, rg.rem);
-  for (int64_t pos = rg.w0; pos < rg.w1;) {
-    w.t1 = (int)min((int64_t)w.u.ng, w.t0 + (rg.w1 - pos));
-    const int i0 = w.m * w.d.tpm;
-    const int nrow = (min(w.d.n, i0 + w.d.tpm) - i0) * a.G;  // rows of the unit
+  Walk<C::unit, C::granule> w(a, rg);
+  do {
+    const int i0 = w.first_row(), nrow = w.rows(a.G);
 
     // ---- this lane's two rows of Q (g and g + 8) ----
     uint32_t qf[D / 16][4];
@@ -312,7 +145,7 @@ kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a) {
     int rlo[2], rhi[2];  // tokens the row sees
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      const int row = g + 8 * r;
+      const int row = rq * 16 + g + 8 * r;
       const bool ok = row < nrow;
       const int tok = i0 + (ok ? row : 0) / a.G, head = w.h * a.G + (ok ? row % a.G : 0);
       const uint32_t* src = reinterpret_cast<const uint32_t*>(
@@ -343,8 +176,7 @@ kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a) {
           }
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        int E = (int)(__float_as_uint(mx) >> 23) - 127;
-        E = mx > 0.0f ? max(-126, min(126, E)) : 0;
+        const int E = row_exponent(mx);
         const float down = pow2f(-E);
         crow[r] *= pow2f(E);
 #pragma unroll
@@ -381,7 +213,7 @@ kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a) {
     // page ids of a tile's two 16-key halves (one page where pages are longer);
     // -1: nothing of the half is seen, or the entry is outside the cache
     auto tile_page = [&](int t) -> int {
-      const int key = (w.u.g0 + t) * kGranule + warp * kWarpKeys + (lane & 16);
+      const int key = (w.u.g0 + t) * C::granule + kg * kTileKeys + (lane & 16);
       int p = -1;
       if (t < w.t1 && key < w.u.hi && key + 16 > w.u.lo) {
         p = table[key >> a.c.page_shift];
@@ -396,13 +228,14 @@ kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a) {
       const int st = (t - w.t0) % C::stages;
       const int p0 = __shfl_sync(0xffffffffu, pid, 0), p1 = __shfl_sync(0xffffffffu, pid, 16);
       if (t < w.t1) {
-        const int key0 = (w.u.g0 + t) * kGranule + warp * kWarpKeys;
+        const int key0 = (w.u.g0 + t) * C::granule + kg * kTileKeys;
         const uint32_t kd = ring_u + st * C::stage, vd = kd + C::tile;
         constexpr int kCh = D / 16;              // 16-byte chunks per key
         constexpr int kPerIt = 32 / kCh;         // keys per instruction
+        constexpr int kMine = kTileKeys / kRg;   // keys that this warp copies
 #pragma unroll
-        for (int it = 0; it < kWarpKeys / kPerIt; ++it) {
-          const int r = it * kPerIt + lane / kCh, ch = lane % kCh;
+        for (int it = 0; it < kMine / kPerIt; ++it) {
+          const int r = rq * kMine + it * kPerIt + lane / kCh, ch = lane % kCh;
           const int key = key0 + r;
           const int p = r < 16 ? p0 : p1;
           const bool ok = p >= 0 && key >= w.u.lo && key < w.u.hi;
@@ -413,7 +246,7 @@ kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a) {
           copy16(kd + so, a.c.k + off, ok);
           copy16(vd + so, a.c.v + off, ok);
         }
-        if (lane < 4) {  // ks of half 0, 1, vs of half 0, 1
+        if (rq == 0 && lane < 4) {  // ks of half 0, 1, vs of half 0, 1
           const int p = (lane & 1) ? p1 : p0;
           const bool ok = p >= 0;
           const int64_t off = ok ? (int64_t)p * a.c.H_kv + w.h : 0;
@@ -435,6 +268,10 @@ kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a) {
     }
     for (int t = w.t0; t < w.t1; ++t) {
       const int rel = t - w.t0, st = rel % C::stages;
+      copy_wait<C::stages - 2>();
+      // the group's copies of tile t are there, and it is done with tile t - 1,
+      // whose stage takes the next copies
+      group_sync<kRg>(kg);
       {
         const int pid = pid_next;
         pid_next = tile_page(t + C::stages);
@@ -443,13 +280,11 @@ kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a) {
         const uint32_t b = __ballot_sync(0xffffffffu, pid >= 0);
         live = (live & ~(3u << (2 * ns))) | (((b & 1u) | ((b >> 15) & 2u)) << (2 * ns));
       }
-      copy_wait<C::stages - 1>();
-      __syncwarp();
       const uint32_t halves = (live >> (2 * st)) & 3u;
       if (halves != 0) {
         const uint8_t* kt = ring + st * C::stage;
         const uint32_t vt = ring_u + st * C::stage + C::tile;
-        const int key0 = (w.u.g0 + t) * kGranule + warp * kWarpKeys;
+        const int key0 = (w.u.g0 + t) * C::granule + kg * kTileKeys;
         // ---- S = Q K^T ----
         float sc[4][4];
 #pragma unroll
@@ -473,7 +308,7 @@ kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a) {
         const float rv[2] = {(halves & 1u) ? 1.0f / bs.z : 0.0f, (halves & 2u) ? 1.0f / bs.w : 0.0f};
         float tmax[2] = {-INFINITY, -INFINITY};
         const bool whole = halves == 3u && key0 >= max(rlo[0], rlo[1]) &&
-                           key0 + kWarpKeys <= min(rhi[0], rhi[1]);
+                           key0 + kTileKeys <= min(rhi[0], rhi[1]);
 #pragma unroll
         for (int nt = 0; nt < 4; ++nt) {
           const int hf = nt >> 1;
@@ -551,29 +386,29 @@ kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a) {
           }
         }
       }
-      __syncwarp();  // the stage may be written again
     }
     copy_wait<0>();
 
-    // ---- join the warps ----
+    // ---- join the key groups ----
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       lrow[r] += __shfl_xor_sync(0xffffffffu, lrow[r], 1);
       lrow[r] += __shfl_xor_sync(0xffffffffu, lrow[r], 2);
       if (c == 0) {
-        row_max[warp][g + 8 * r] = mrow[r];
-        row_sum[warp][g + 8 * r] = lrow[r];
+        row_max[kg][rq * 16 + g + 8 * r] = mrow[r];
+        row_sum[kg][rq * 16 + g + 8 * r] = lrow[r];
       }
     }
     __syncthreads();  // every warp is done with its ring
-    float* obuf = reinterpret_cast<float*>(smem);  // [warp][row][D]
+    float* obuf = reinterpret_cast<float*>(smem);  // [key group][row][D]
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      float m = row_max[0][g + 8 * r];
+      const int row = rq * 16 + g + 8 * r;
+      float m = row_max[0][row];
 #pragma unroll
-      for (int i = 1; i < kWarps; ++i) m = fmaxf(m, row_max[i][g + 8 * r]);
+      for (int i = 1; i < C::kgs; ++i) m = fmaxf(m, row_max[i][row]);
       const float f = ex2(mrow[r] - (m == -INFINITY ? 0.0f : m));
-      float* dst = obuf + ((size_t)warp * kRows + g + 8 * r) * D;
+      float* dst = obuf + ((size_t)kg * C::unit + row) * D;
 #pragma unroll
       for (int cb = 0; cb < D / 16; ++cb)
         *reinterpret_cast<float4*>(dst + 16 * cb + 4 * c) =
@@ -581,140 +416,104 @@ kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a) {
                         o[2 * cb + 1][2 * r + 1] * f);
     }
     __syncthreads();
-    const bool full = w.t0 == 0 && w.t1 == w.u.ng;
-    float* pw = part + (w.t0 == 0 ? part_floats(D) : 0);  // a part that starts a unit is the last
-    constexpr int kTpr = D / 4;                            // threads per row
+    float* pw = part + (w.t0 == 0 ? part_floats(C::unit, D) : 0);
+    constexpr int kTpr = D / 4;  // threads per row
 #pragma unroll
-    for (int i = 0; i < kRows * kTpr / kThreads; ++i) {
+    for (int i = 0; i < C::unit * kTpr / kThreads; ++i) {
       const int row = (i * kThreads + tid) / kTpr, ch = (tid % kTpr) * 4;
       float m = row_max[0][row];
 #pragma unroll
-      for (int q = 1; q < kWarps; ++q) m = fmaxf(m, row_max[q][row]);
+      for (int q = 1; q < C::kgs; ++q) m = fmaxf(m, row_max[q][row]);
       const float mz = m == -INFINITY ? 0.0f : m;
       float l = 0.0f;
       float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-      for (int q = 0; q < kWarps; ++q) {
+      for (int q = 0; q < C::kgs; ++q) {
         l = fmaf(row_sum[q][row], ex2(row_max[q][row] - mz), l);
         const float4 y =
-            *reinterpret_cast<const float4*>(obuf + ((size_t)q * kRows + row) * D + ch);
+            *reinterpret_cast<const float4*>(obuf + ((size_t)q * C::unit + row) * D + ch);
         x.x += y.x;
         x.y += y.y;
         x.z += y.z;
         x.w += y.w;
       }
-      if (full) {
-        if (row < nrow) {
-          const float inv = l == 0.0f ? 0.0f : 1.0f / l;  // no visible token: zeros
-          const int64_t orow = (int64_t)(w.d.row0 + i0 + row / a.G) * a.H + w.h * a.G + row % a.G;
-          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + orow * D + ch) =
-              make_uint2(pair_from_floats<kBf16>(x.x * inv, x.y * inv),
-                         pair_from_floats<kBf16>(x.z * inv, x.w * inv));
-          if (a.lse && ch == 0)
-            a.lse[orow] = l == 0.0f ? -INFINITY : (mz - kHeadroom + __log2f(l)) * kLn2;
-        }
+      if (row >= nrow) continue;
+      if (w.whole()) {
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;  // no visible token: zeros
+        const int64_t orow = (int64_t)(w.d.row0 + i0 + row / a.G) * a.H + w.h * a.G + row % a.G;
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + orow * D + ch) =
+            make_uint2(pair_from_floats<kBf16>(x.x * inv, x.y * inv),
+                       pair_from_floats<kBf16>(x.z * inv, x.w * inv));
+        if (a.lse && ch == 0)
+          a.lse[orow] = l == 0.0f ? -INFINITY : (mz - kHeadroom + __log2f(l)) * kLn2;
       } else {
-        *reinterpret_cast<float4*>(pw + row * D + ch) = x;
+        *reinterpret_cast<float4*>(pw + (size_t)row * D + ch) = x;
         if (ch == 0) {
-          pw[kRows * D + row] = m;
-          pw[kRows * D + kRows + row] = l;
+          pw[C::unit * D + row] = m;
+          pw[C::unit * D + C::unit + row] = l;
         }
       }
     }
     __syncthreads();  // the buffers are read before the next unit's copies
-    pos += w.t1 - w.t0;
-    if (pos < rg.w1 && !walk_next(a, w)) break;
-  }
+  } while (w.next(a));
 }
 
-// Joins the parts of the units that were cut: CTA (x, y) takes the unit whose
-// first part is the last of worker x's range, rows y * rows_per .. of it.
-template <int D, bool kBf16>
+template <int D, int kRg, bool kBf16>
 __global__ void __launch_bounds__(kThreads)
 kv8_merge_kernel(const __grid_constant__ Kv8AttnArgs a, int workers) {
-  __shared__ RangeSmem rsm;
-  constexpr int kTpr = D / 4, kRowsPer = kThreads / kTpr;
-  // the ranges depend on kv_len and cu alone, which were there before the kernel
-  // whose parts are joined: only the parts are waited for
-  const Range rg = find_range(a, blockIdx.x, workers, rsm);
-  if (rg.s < 0) {
-    pdl_wait();
-    return;
-  }
-  Walk w;
-  walk_to(a, w, rg.s, rg.rem);
-  int64_t pos = rg.w0;
-  while (true) {
-    w.t1 = (int)min((int64_t)w.u.ng, w.t0 + (rg.w1 - pos));
-    if (pos + (w.t1 - w.t0) >= rg.w1) break;
-    pos += w.t1 - w.t0;
-    if (!walk_next(a, w)) break;
-  }
-  pdl_wait();
-  if (w.t0 != 0 || w.t1 == w.u.ng) return;  // not cut here, or it began before this worker
-  // the unit is granules [pos, pos + ng) of the batch: the parts are workers
-  // blockIdx.x (its last part) .. the one that holds the unit's last granule
-  const int64_t end = pos + w.u.ng;
-  const float* base = reinterpret_cast<const float*>(a.scratch);
-  const size_t pf = part_floats(D);
-  const int last = (int)((end * rg.workers - 1) / rg.total);  // who has granule end - 1
-  const int row = blockIdx.y * kRowsPer + threadIdx.x / kTpr, ch = (threadIdx.x % kTpr) * 4;
-  const int i0 = w.m * w.d.tpm;
-  const int nrow = (min(w.d.n, i0 + w.d.tpm) - i0) * a.G;
-  if (row >= nrow) return;
-  float m = -INFINITY, l = 0.0f;
-  float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-  for (int p = blockIdx.x; p <= last; ++p) {
-    const float* src = base + ((size_t)p * 2 + (p == (int)blockIdx.x ? 1 : 0)) * pf;
-    const float pm = __ldcg(src + kRows * D + row), pl = __ldcg(src + kRows * D + kRows + row);
-    const float4 y = __ldcg(reinterpret_cast<const float4*>(src + row * D + ch));
-    const float nm = fmaxf(m, pm), z = nm == -INFINITY ? 0.0f : nm;
-    const float f0 = ex2(m - z), f1 = ex2(pm - z);
-    m = nm;
-    l = l * f0 + pl * f1;
-    x.x = x.x * f0 + y.x * f1;
-    x.y = x.y * f0 + y.y * f1;
-    x.z = x.z * f0 + y.z * f1;
-    x.w = x.w * f0 + y.w * f1;
-  }
-  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-  const int64_t orow = (int64_t)(w.d.row0 + i0 + row / a.G) * a.H + w.h * a.G + row % a.G;
-  *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + orow * D + ch) =
-      make_uint2(pair_from_floats<kBf16>(x.x * inv, x.y * inv),
-                 pair_from_floats<kBf16>(x.z * inv, x.w * inv));
-  if (a.lse && ch == 0)
-    a.lse[orow] = l == 0.0f ? -INFINITY
-                            : ((m == -INFINITY ? 0.0f : m) - kHeadroom + __log2f(l)) * kLn2;
+  using C = Cfg<D, kRg>;
+  merge_parts<C::unit, C::granule, kWarps, D, kBf16>(a, workers, kHeadroom);
 }
 
-inline int grid_workers(int D) { return device_sm_count() * (D == 128 ? Cfg<128>::ctas : Cfg<64>::ctas); }
+template <int D>
+int grid_workers() {
+  return device_sm_count() * Cfg<D, 1>::ctas;
+}
 
-template <int D, bool kBf16>
+template <int D, int kRg, bool kBf16>
 cudaError_t attn_t(const Kv8AttnArgs& a, cudaStream_t stream) {
-  using C = Cfg<D>;
-  cudaError_t e = cudaFuncSetAttribute(kv8_attn_kernel<D, kBf16>,
+  using C = Cfg<D, kRg>;
+  cudaError_t e = cudaFuncSetAttribute(kv8_attn_kernel<D, kRg, kBf16>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, C::smem);
   if (e != cudaSuccess) return e;
-  const int workers = grid_workers(D);
-  kv8_attn_kernel<D, kBf16><<<workers, kThreads, C::smem, stream>>>(a);
+  const int workers = grid_workers<D>();
+  kv8_attn_kernel<D, kRg, kBf16><<<workers, kThreads, C::smem, stream>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   constexpr int kRowsPer = kThreads / (D / 4);
-  return launch_kernel(kv8_merge_kernel<D, kBf16>, dim3(workers, kRows / kRowsPer), dim3(kThreads),
-                       0, stream, /*pdl=*/true, a, workers);
+  return launch_kernel(kv8_merge_kernel<D, kRg, kBf16>, dim3(workers, C::unit / kRowsPer),
+                       dim3(kThreads), 0, stream, /*pdl=*/true, a, workers);
+}
+
+template <int D, bool kBf16>
+cudaError_t attn_rows(const Kv8AttnArgs& a, int row_groups, cudaStream_t stream) {
+  switch (row_groups) {
+    case 1: return attn_t<D, 1, kBf16>(a, stream);
+    case 2: return attn_t<D, 2, kBf16>(a, stream);
+    default: return attn_t<D, 4, kBf16>(a, stream);
+  }
+}
+
+// Query rows of a KV head per sequence, on average.
+int64_t mean_rows(int S, int T, int G) {
+  return max((int64_t)G, ((int64_t)T * G + S - 1) / S);
 }
 
 }  // namespace
 
 size_t kv8_attn_scratch_bytes(int S, int T, int H, int H_kv, int D) {
   if (D != 64 && D != 128) return 0;
-  return align_up((size_t)grid_workers(D) * 2 * part_floats(D) * 4, 256);
+  const int workers = D == 128 ? grid_workers<128>() : grid_workers<64>();
+  return align_up((size_t)workers * 2 * part_floats(64, D) * 4, 256);
 }
 
 cudaError_t launch_kv8_attn(const Kv8AttnArgs& a, int type, cudaStream_t stream) {
+  const int64_t rows = mean_rows(a.c.S, a.c.T, a.G);
+  const int rg = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
   if (a.c.D == 128)
-    return type == CSA2_BF16 ? attn_t<128, true>(a, stream) : attn_t<128, false>(a, stream);
-  return type == CSA2_BF16 ? attn_t<64, true>(a, stream) : attn_t<64, false>(a, stream);
+    return type == CSA2_BF16 ? attn_rows<128, true>(a, rg, stream)
+                             : attn_rows<128, false>(a, rg, stream);
+  return type == CSA2_BF16 ? attn_rows<64, true>(a, rg, stream)
+                           : attn_rows<64, false>(a, rg, stream);
 }
 
 }  // namespace csa2

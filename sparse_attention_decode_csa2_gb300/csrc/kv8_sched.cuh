@@ -1,0 +1,321 @@
+// How the attention over the 8-bit cache is dealt out.  A unit of work is
+// (sequence, block of up to kUnit query rows = tokens x G heads, KV head); its
+// keys are cut into granules.  The batch's granules, in the order (sequence,
+// block, head, key), are dealt to the grid's CTAs ("workers") as equal
+// contiguous ranges.  Everything is computed on the device from kv_len and cu:
+// there is no host plan, nothing to keep up to date, no CTA for tokens that a
+// sequence does not have, and a captured graph follows the lengths.
+#pragma once
+
+#include "kv8.cuh"
+
+namespace csa2 {
+namespace kv8 {
+
+constexpr float kLn2 = 0.69314718055994530942f;
+
+struct Dims {
+  int n, row0, len, cap;  // the sequence's rows and tokens; tokens the table has room for
+  int tpu, nm;            // tokens of a block of rows, blocks
+};
+
+template <int kUnit>
+__device__ __forceinline__ Dims seq_dims(const Kv8AttnArgs& a, int s) {
+  const Kv8Seq q = kv8_seq(a.c, s);
+  Dims d;
+  d.n = q.n;
+  d.row0 = q.row0;
+  d.len = q.len;
+  d.cap = (int)min((int64_t)q.len, (int64_t)a.c.max_pages << a.c.page_shift);
+  d.tpu = kUnit / a.G;
+  d.nm = (q.n + d.tpu - 1) / d.tpu;
+  return d;
+}
+
+// Tokens [lo, hi) that some row of block m sees, and the granules that cover them.
+struct Span {
+  int lo, hi, g0, ng;
+};
+
+template <int kGranule>
+__device__ __forceinline__ Span unit_span(const Kv8AttnArgs& a, const Dims& d, int m) {
+  Span u;
+  u.lo = 0;
+  u.hi = d.cap;
+  if (a.causal) {
+    const int i0 = m * d.tpu, i1 = min(d.n, i0 + d.tpu);
+    const int64_t p0 = (int64_t)d.len - d.n + i0, p1 = (int64_t)d.len - d.n + i1 - 1;
+    u.hi = (int)max((int64_t)0, min((int64_t)d.cap, p1 + 1));
+    if (a.window > 0) u.lo = (int)max((int64_t)0, p0 - a.window + 1);
+  }
+  if (u.lo > u.hi) u.lo = u.hi;
+  u.g0 = u.lo / kGranule;
+  u.ng = max(1, (u.hi + kGranule - 1) / kGranule - u.g0);  // one at least: it writes the rows
+  return u;
+}
+
+// A worker's range [w0, w1) of the batch's granules and where it starts:
+// granule t0 of unit (s, m, h).  s < 0: no range.
+struct Range {
+  int64_t w0, w1, total;
+  int workers;  // workers that have a range (no more than there are granules)
+  int s, m, h, t0;
+};
+
+template <int kWarps>
+struct RangeSmem {
+  int64_t warp_sum[kWarps];
+  int s, m, h, t0;
+};
+
+// Sums one value per lane of each warp; every lane gets the warp's total.
+__device__ __forceinline__ int64_t warp_total(int64_t x) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+__device__ __forceinline__ int64_t warp_scan(int64_t x, int lane) {  // inclusive
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  return x;
+}
+
+// All threads of the block.  A warp takes a contiguous share of the sequences,
+// 32 at a time: a lane per sequence where the sequences have one block of rows,
+// else the lanes go over a sequence's blocks together.
+template <int kUnit, int kGranule, int kWarps>
+__device__ Range find_range(const Kv8AttnArgs& a, int worker, int workers,
+                            RangeSmem<kWarps>& sm) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = (a.c.S + kWarps - 1) / kWarps;
+  const int s0 = min(a.c.S, warp * per), s1 = min(a.c.S, s0 + per);
+  // granules of the blocks of sequence s, every KV head
+  auto lane_work = [&](const Dims& d) -> int64_t {  // a lane's sequence with one block (or none)
+    return d.nm == 1 ? (int64_t)unit_span<kGranule>(a, d, 0).ng * a.c.H_kv : 0;
+  };
+  auto warp_work = [&](const Dims& d) -> int64_t {  // the warp's sequence, any number of blocks
+    if (!a.causal) return (int64_t)d.nm * unit_span<kGranule>(a, d, 0).ng * a.c.H_kv;
+    int64_t w = 0;
+    for (int m = lane; m < d.nm; m += 32) w += unit_span<kGranule>(a, d, m).ng;
+    return warp_total(w) * a.c.H_kv;
+  };
+  // work of sequence base + lane (0 past s1)
+  auto chunk = [&](int base) -> int64_t {
+    const int s = base + lane;
+    Dims d;
+    d.nm = 0;
+    if (s < s1) d = seq_dims<kUnit>(a, s);
+    int64_t w = lane_work(d);
+    uint32_t big = __ballot_sync(0xffffffffu, d.nm > 1);
+    while (big) {
+      const int l = __ffs(big) - 1;
+      big &= big - 1;
+      const int64_t x = warp_work(seq_dims<kUnit>(a, base + l));
+      if (lane == l) w = x;
+    }
+    return w;
+  };
+  int64_t mine = 0, first = 0;
+  for (int b = s0; b < s1; b += 32) {
+    const int64_t w = chunk(b);
+    if (b == s0) first = w;
+    mine += w;
+  }
+  mine = warp_total(mine);
+  if (lane == 0) sm.warp_sum[warp] = mine;
+  if (tid == 0) sm.s = -1;
+  __syncthreads();
+  int64_t base = 0, total = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) base += sm.warp_sum[w];
+    total += sm.warp_sum[w];
+  }
+  Range r;
+  r.total = total;
+  r.workers = (int)min((int64_t)workers, total);
+  r.w0 = r.w1 = 0;
+  if (worker < r.workers) {
+    r.w0 = total * worker / r.workers;
+    r.w1 = total * (worker + 1) / r.workers;
+  }
+  if (r.w0 < r.w1 && r.w0 >= base && r.w0 < base + mine) {  // this warp's sequences hold w0
+    int64_t at = base;
+    for (int b = s0; b < s1; b += 32) {
+      const int64_t w = b == s0 ? first : chunk(b);
+      const int64_t inc = warp_scan(w, lane);
+      const uint32_t past = __ballot_sync(0xffffffffu, r.w0 < at + inc);
+      if (past) {
+        const int l = __ffs(past) - 1;
+        const int s = b + l;
+        int64_t rem = r.w0 - at - __shfl_sync(0xffffffffu, inc - w, l);
+        const Dims d = seq_dims<kUnit>(a, s);
+        // the block of rows: 32 at a time
+        for (int m0 = 0; m0 < d.nm; m0 += 32) {
+          const int ng = m0 + lane < d.nm ? unit_span<kGranule>(a, d, m0 + lane).ng : 0;
+          const int64_t x = (int64_t)ng * a.c.H_kv, xi = warp_scan(x, lane);
+          const uint32_t pm = __ballot_sync(0xffffffffu, rem < xi);
+          if (pm) {
+            const int k = __ffs(pm) - 1;
+            rem -= __shfl_sync(0xffffffffu, xi - x, k);
+            const int n = __shfl_sync(0xffffffffu, ng, k);
+            if (lane == 0) {
+              sm.s = s;
+              sm.m = m0 + k;
+              sm.h = (int)(rem / n);
+              sm.t0 = (int)(rem % n);
+            }
+            break;
+          }
+          rem -= __shfl_sync(0xffffffffu, xi, 31);
+        }
+        break;
+      }
+      at += __shfl_sync(0xffffffffu, inc, 31);
+    }
+  }
+  __syncthreads();
+  r.s = sm.s;
+  r.m = sm.m;
+  r.h = sm.h;
+  r.t0 = sm.t0;
+  return r;
+}
+
+// Walks the units of a range: unit (s, m, h), granules [t0, t1) of its span.
+template <int kUnit, int kGranule>
+struct Walk {
+  int s, m, h, t0, t1;
+  int64_t pos, end;  // granules of the batch: the unit's t0, the range's end
+  Dims d;
+  Span u;
+
+  __device__ __forceinline__ Walk(const Kv8AttnArgs& a, const Range& r)
+      : s(r.s), m(r.m), h(r.h), t0(r.t0), pos(r.w0), end(r.w1) {
+    d = seq_dims<kUnit>(a, s);
+    u = unit_span<kGranule>(a, d, m);
+    t1 = (int)min((int64_t)u.ng, t0 + (end - pos));
+  }
+  // To the next unit of the range; false at its end.
+  __device__ __forceinline__ bool next(const Kv8AttnArgs& a) {
+    pos += t1 - t0;
+    if (pos >= end) return false;
+    t0 = 0;
+    if (++h == a.c.H_kv) {
+      h = 0;
+      if (++m < d.nm) {
+        u = unit_span<kGranule>(a, d, m);
+      } else {
+        m = 0;
+        do {
+          if (++s >= a.c.S) return false;
+          d = seq_dims<kUnit>(a, s);
+        } while (d.nm == 0);
+        u = unit_span<kGranule>(a, d, 0);
+      }
+    }
+    t1 = (int)min((int64_t)u.ng, t0 + (end - pos));
+    return true;
+  }
+  __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == u.ng; }
+  __device__ __forceinline__ int first_row() const { return m * d.tpu; }  // its first token's row
+  __device__ __forceinline__ int rows(int G) const {
+    return (min(d.n, (m + 1) * d.tpu) - m * d.tpu) * G;
+  }
+};
+
+// A part of a cut unit in scratch: O [kUnit][D], max [kUnit], sum [kUnit].  A
+// worker has two: [0] a part that continues a unit, [1] one that starts it.
+__host__ __device__ constexpr size_t part_floats(int unit, int D) {
+  return (size_t)unit * D + 2 * (size_t)unit;
+}
+
+// 2^x by the hardware's approximation (relative error about 2^-22).
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+template <bool kBf16>
+__device__ __forceinline__ float2 pair_to_float2(uint32_t w) {
+  if (kBf16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+  return half2_bits_to_float2(w);
+}
+template <bool kBf16>
+__device__ __forceinline__ uint32_t pair_from_floats(float lo, float hi) {
+  if (!kBf16) return pack_f16(lo, hi);
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// Exponent that brings a row's largest magnitude mx to [1, 2) (0 for a row of zeros).
+__device__ __forceinline__ int row_exponent(float mx) {
+  const int E = (int)(__float_as_uint(mx) >> 23) - 127;
+  return mx > 0.0f ? max(-126, min(126, E)) : 0;
+}
+
+// Joins the parts of the cut units: block (x, y) takes the unit whose first
+// part ends worker x's range, rows y * (kThreads / (D / 4)) .. of it.  The
+// ranges depend on kv_len and cu alone, which were there before the kernel
+// whose parts are joined: only the parts are waited for.
+template <int kUnit, int kGranule, int kWarps, int D, bool kBf16>
+__device__ __forceinline__ void merge_parts(const Kv8AttnArgs& a, int workers, float headroom) {
+  __shared__ RangeSmem<kWarps> rsm;
+  const Range rg = find_range<kUnit, kGranule, kWarps>(a, blockIdx.x, workers, rsm);
+  if (rg.s < 0) {
+    pdl_wait();
+    return;
+  }
+  Walk<kUnit, kGranule> w(a, rg);
+  while (w.pos + (w.t1 - w.t0) < w.end && w.next(a)) {
+  }
+  pdl_wait();
+  if (w.t0 != 0 || w.t1 == w.u.ng) return;  // not cut here, or it began before this worker
+  // the unit is granules [pos, pos + ng): its parts are those of the workers up
+  // to the one that holds the last of them
+  const int64_t end = w.pos + w.u.ng;
+  const int last = (int)((end * rg.workers - 1) / rg.total);
+  constexpr int kTpr = D / 4, kRowsPer = kWarps * 32 / kTpr;
+  const int row = blockIdx.y * kRowsPer + threadIdx.x / kTpr, ch = (threadIdx.x % kTpr) * 4;
+  if (row >= w.rows(a.G)) return;
+  const float* base = reinterpret_cast<const float*>(a.scratch);
+  const size_t pf = part_floats(kUnit, D);
+  float m = -INFINITY, l = 0.0f;
+  float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+  for (int p = blockIdx.x; p <= last; ++p) {
+    const float* src = base + ((size_t)p * 2 + (p == (int)blockIdx.x ? 1 : 0)) * pf;
+    const float pm = __ldcg(src + kUnit * D + row), pl = __ldcg(src + kUnit * D + kUnit + row);
+    const float4 y = __ldcg(reinterpret_cast<const float4*>(src + (size_t)row * D + ch));
+    const float nm = fmaxf(m, pm), z = nm == -INFINITY ? 0.0f : nm;
+    const float f0 = ex2(m - z), f1 = ex2(pm - z);
+    m = nm;
+    l = l * f0 + pl * f1;
+    x.x = x.x * f0 + y.x * f1;
+    x.y = x.y * f0 + y.y * f1;
+    x.z = x.z * f0 + y.z * f1;
+    x.w = x.w * f0 + y.w * f1;
+  }
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;  // no visible token: zeros
+  const int64_t orow =
+      (int64_t)(w.d.row0 + w.first_row() + row / a.G) * a.H + w.h * a.G + row % a.G;
+  *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + orow * D + ch) =
+      make_uint2(pair_from_floats<kBf16>(x.x * inv, x.y * inv),
+                 pair_from_floats<kBf16>(x.z * inv, x.w * inv));
+  if (a.lse && ch == 0)
+    a.lse[orow] =
+        l == 0.0f ? -INFINITY : ((m == -INFINITY ? 0.0f : m) - headroom + __log2f(l)) * kLn2;
+}
+
+}  // namespace kv8
+}  // namespace csa2
