@@ -443,7 +443,7 @@ csa2_status csa2_kv8_read(const csa2_kv8_cache* cache, const csa2_kv8_batch* bat
  *   call depends on its inputs alone (no atomics).
  *   ws       at least csa2_kv8_workspace_size(cache, batch, H) bytes, 16-byte
  *            aligned.
- * H must be a multiple of H_kv with H / H_kv <= 16 (CSA2_ERR_UNSUPPORTED).
+ * H must be a multiple of H_kv, with H / H_kv <= 256 (else CSA2_ERR_UNSUPPORTED).
  */
 csa2_status csa2_kv8_attn(const void* q, int type, int64_t q_stride, int H,
                           const csa2_kv8_cache* cache, const csa2_kv8_batch* batch, int causal,

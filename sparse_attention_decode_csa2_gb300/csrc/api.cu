@@ -570,7 +570,7 @@ csa2_status csa2_kv8_attn(const void* q, int type, int64_t q_stride, int H,
   if (H < 1 || H % a.c.H_kv != 0) return CSA2_ERR_INVALID_ARG;
   a.H = H;
   a.G = H / a.c.H_kv;
-  if (a.G > 64) return CSA2_ERR_UNSUPPORTED;
+  if (a.G > 256) return CSA2_ERR_UNSUPPORTED;
   if (type != CSA2_BF16 && type != CSA2_FP16) return CSA2_ERR_INVALID_ARG;
   if ((s = check_rows(q, type, q_stride, H, a.c.D)) != CSA2_OK) return s;
   if (window < 0 || (window > 0 && !causal)) return CSA2_ERR_INVALID_ARG;

@@ -95,6 +95,9 @@ struct Kv8AttnArgs {
 };
 
 size_t kv8_attn_scratch_bytes(int S, int T, int H, int H_kv, int D);
+// The kernels for many query rows per sequence (chosen by launch_kv8_attn).
+size_t kv8_attn_tc_scratch_bytes(int D);
+cudaError_t launch_kv8_attn_tc(const Kv8AttnArgs& a, int type, cudaStream_t stream);
 cudaError_t launch_kv8_attn(const Kv8AttnArgs& a, int type, cudaStream_t stream);
 
 }  // namespace csa2

@@ -135,7 +135,8 @@ kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a) {
   float* part =
       reinterpret_cast<float*>(a.scratch) + (size_t)blockIdx.x * 2 * part_floats(C::unit, D);
 
-  Walk<C::unit, C::granule> w(a, rg);
+  Walk<C::unit, C::granule> w;
+  w.start(a, rg);
   do {
     const int i0 = w.first_row(), nrow = w.rows(a.G);
 
@@ -502,12 +503,14 @@ int64_t mean_rows(int S, int T, int G) {
 
 size_t kv8_attn_scratch_bytes(int S, int T, int H, int H_kv, int D) {
   if (D != 64 && D != 128) return 0;
+  if (mean_rows(S, T, H / H_kv) > 64) return kv8_attn_tc_scratch_bytes(D);
   const int workers = D == 128 ? grid_workers<128>() : grid_workers<64>();
   return align_up((size_t)workers * 2 * part_floats(64, D) * 4, 256);
 }
 
 cudaError_t launch_kv8_attn(const Kv8AttnArgs& a, int type, cudaStream_t stream) {
   const int64_t rows = mean_rows(a.c.S, a.c.T, a.G);
+  if (rows > 64) return launch_kv8_attn_tc(a, type, stream);
   const int rg = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
   if (a.c.D == 128)
     return type == CSA2_BF16 ? attn_rows<128, true>(a, rg, stream)

@@ -1,0 +1,571 @@
+// Attention of many query rows per sequence (prompts and prompt chunks) over
+// the 8-bit paged KV cache, on the 5th-generation tensor cores.  The arithmetic
+// is that of the kernel for few rows (kv8_attn.cu): rows scaled by powers of
+// two, block scales in the exponent, weights in fp16, sums and maxima in fp32.
+//
+// One persistent CTA per SM walks its range of units (kv8_sched.cuh): a unit is
+// a KV head's query rows of a block, two tiles of 128 rows (row = token x G +
+// head), against tiles of 128 keys:
+//   S_t[row][key]  = sum_c Q_t[row][c] K[key][c]     A = Q_t (shared memory), B = K
+//   O_t[row][c]   += sum_key P_t[row][key] V[key][c] A = P_t (tensor memory), B = V MN-major
+// Tensor memory holds S_0, S_1 (128 columns each; P_t overwrites S_t as fp16)
+// and O_0, O_1 (D columns each).  While the softmax of one row tile runs, the
+// tensor pipe works on the other: O_0(j) S_0(j+1) O_1(j) S_1(j+1).
+//
+// Warp roles (512 threads):
+//   warps 0-3, 4-7  softmax of row tile 0, 1: a thread owns a row (a tensor-memory
+//                   lane), so row maxima and sums need no exchange.  The reference
+//                   maximum is lazy: it moves, and O is rescaled, only when a logit
+//                   passes it by more than 2^8 (weights stay below 2^15)
+//   warps 8-11      dequantisers: E4M3 codes from global memory (through L2: the
+//                   units of a sequence share them) to fp16 in shared memory,
+//                   128-byte swizzled, double buffered; keys that no row of the
+//                   unit may see, and pages outside the cache, are zeros
+//   warp 12         tensor memory; lane 0 issues every MMA (13-15 only complete
+//                   its warpgroup, for the register split)
+// Every wait is bounded (about 2 s): a role that gives up sets the timeout
+// status and leaves, the others follow, and tensor memory is freed.
+#include "kv8_sched.cuh"
+#include "tc_common.cuh"
+
+namespace csa2 {
+namespace {
+
+using namespace kv8;
+using namespace tc;
+
+constexpr int kSoftWarps = 8, kDeqWarp0 = 8, kDeqWarps = 4, kMmaWarp = 12;
+constexpr int kWarps = 16, kThreads = kWarps * 32;
+// Registers a thread after the roles part (four warpgroups, 512 in all: the 128
+// a thread of the launch): a softmax thread holds a whole row of S.
+constexpr int kSoftRegs = 176, kDeqRegs = 112, kMmaRegs = 48;
+static_assert(2 * kSoftRegs + kDeqRegs + kMmaRegs <= 512, "register split");
+constexpr int kUnit = 256;      // query rows of a unit
+constexpr int kTileE = 128;     // keys of a tile (and rows of a row tile)
+constexpr float kHeadroom = 7.0f, kLazy = 8.0f;  // log2: weights stay below 2^(7 + 8)
+constexpr uint32_t kAtom = 128 * 128;            // bytes: 128 rows of 64 fp16 channels
+
+template <int D>
+struct Lay {
+  static constexpr uint32_t tile = (D / 64) * kAtom;  // bytes of Q_t, of a K or a V stage
+  static constexpr uint32_t q = 0, k = 2 * tile, v = 4 * tile, ctl = 6 * tile;
+  static constexpr uint32_t alloc = ctl + 2048 + 1024;  // slack to align the base to 1 KiB
+};
+static_assert(Lay<128>::alloc <= 232448, "shared memory");
+
+struct Ctl {
+  float4 sc[4][8];  // of a tile's 16-key groups: K scale, log2 V scale, 1 / V scale
+  uint64_t q_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_full[2];
+  uint64_t done;
+  RangeSmem<kWarps> range;
+  Walk<kUnit, kTileE> walk[kMmaWarp + 1];  // each warp's own (kept out of registers)
+  uint32_t tmem;
+  int32_t abort;
+};
+static_assert(sizeof(Ctl) <= 2048, "control block");
+
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int32_t* status) {
+  return __all_sync(0xffffffffu, mbar_wait(su32(bar), parity, status));
+}
+
+// The warp's walk to its next unit (one lane moves it).
+__device__ __forceinline__ bool warp_next(Walk<kUnit, kTileE>& w, const Kv8AttnArgs& a) {
+  __syncwarp();
+  bool more = false;
+  if ((threadIdx.x & 31) == 0) more = w.next(a);
+  more = __shfl_sync(0xffffffffu, more, 0);
+  __syncwarp();
+  return more;
+}
+
+template <int kRegs>
+__device__ __forceinline__ void more_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void fewer_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+
+// Arrives for the warp: its generic writes to shared memory (read by the tensor
+// cores) and its tensor-memory accesses come before.
+__device__ __forceinline__ void warp_arrive(uint64_t* bar) {
+  proxy_fence();
+  tc_fence_before();
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(su32(bar));
+}
+
+// MMAs whose shared-memory descriptors are given by their low words (address and
+// leading offset); the high words are the same for all of a kind.  A from shared
+// memory, and A from tensor memory.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t hi,
+                                       uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+      "mov.b64 x, {%1, %3};\n\tmov.b64 y, {%2, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, p;\n\t}" ::"r"(d),
+      "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"(accumulate));
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t hi,
+                                       uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 y;\n\tsetp.ne.b32 p, %5, 0;\n\tmov.b64 y, {%2, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %4, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b_lo), "r"(hi), "r"(idesc), "r"(accumulate));
+}
+
+#define CSA2_R8(x, i) "=r"(x[i]), "=r"(x[i + 1]), "=r"(x[i + 2]), "=r"(x[i + 3]), \
+                      "=r"(x[i + 4]), "=r"(x[i + 5]), "=r"(x[i + 6]), "=r"(x[i + 7])
+#define CSA2_I8(x, i) "r"(x[i]), "r"(x[i + 1]), "r"(x[i + 2]), "r"(x[i + 3]), \
+                      "r"(x[i + 4]), "r"(x[i + 5]), "r"(x[i + 6]), "r"(x[i + 7])
+// 32 consecutive 32-bit columns of this thread's lane.
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t* x) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+      "%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : CSA2_R8(x, 0), CSA2_R8(x, 8), CSA2_R8(x, 16), CSA2_R8(x, 24)
+      : "r"(addr));
+}
+__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* x) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr),
+      CSA2_I8(x, 0), CSA2_I8(x, 8), CSA2_I8(x, 16), CSA2_I8(x, 24)
+      : "memory");
+}
+
+// 16 E4M3 codes -> fp16, into 16-byte chunks 2 c4, 2 c4 + 1 of key e of an atom.
+__device__ __forceinline__ void put16(uint8_t* atom, int e, int c4, uint4 w) {
+  const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+  uint32_t o[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    o[2 * i] = e4m3x2_to_f16x2((uint16_t)(x[i] & 0xFFFFu));
+    o[2 * i + 1] = e4m3x2_to_f16x2((uint16_t)(x[i] >> 16));
+  }
+  uint8_t* row = atom + (e >> 3) * 1024 + (e & 7) * 128;
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    *reinterpret_cast<uint4*>(row + (((2 * c4 + i) ^ (e & 7)) << 4)) =
+        make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+}
+
+template <int D, bool kBf16>
+__global__ void __launch_bounds__(kThreads, 1)
+kv8_attn_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
+  using L = Lay<D>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = su32(smem_raw);
+  uint8_t* smem = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
+  Ctl& ctl = *reinterpret_cast<Ctl*>(smem + L::ctl);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  int32_t* status = a.c.status;
+  pdl_trigger();
+  if (blockIdx.x == 0) kv8_check_batch(a.c);
+  const Range rg =
+      find_range<kUnit, kTileE, kWarps>(a, blockIdx.x, gridDim.x, ctl.range);
+  if (rg.s < 0) return;
+
+  if (warp == kMmaWarp) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
+        su32(&ctl.tmem)));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(su32(&ctl.q_full[i]), 4);
+      mbar_init(su32(&ctl.p_full[i]), 4);
+      mbar_init(su32(&ctl.k_full[i]), kDeqWarps);
+      mbar_init(su32(&ctl.v_full[i]), kDeqWarps);
+      mbar_init(su32(&ctl.k_empty[i]), 1);
+      mbar_init(su32(&ctl.v_empty[i]), 1);
+      mbar_init(su32(&ctl.s_full[i]), 1);
+      mbar_init(su32(&ctl.o_full[i]), 1);
+    }
+    mbar_init(su32(&ctl.done), 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  Walk<kUnit, kTileE>& w = ctl.walk[min(warp, kMmaWarp)];
+  if (warp <= kMmaWarp && lane == 0) w.start(a, rg);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tm_s = ctl.tmem, tm_o = ctl.tmem + 256;
+  uint32_t it = 0;  // tiles of keys so far, over all units
+  bool alive = true;
+
+  if (warp < kSoftWarps) {
+    // ================= softmax =================
+    more_registers<kSoftRegs>();
+    const int t = warp >> 2, quad = warp & 3;
+    const uint32_t lane_base = (uint32_t)(quad * 32) << 16;
+    const uint32_t ts = tm_s + t * 128 + lane_base, to = tm_o + t * D + lane_base;
+    const int row = t * 128 + quad * 32 + lane;
+    uint8_t* qt = smem + L::q + t * L::tile;
+    const int qr = row & 127;
+    uint32_t cnt = 0, units = 0;
+    do {
+      const int i0 = w.first_row(), nrow = w.rows(a.G), t0 = w.t0, t1 = w.t1;
+      if (t == 1 && nrow <= 128) {
+        it += t1 - t0;
+        continue;
+      }
+      // ---- this thread's row of Q, scaled to a largest magnitude in [1, 2) ----
+      const bool ok = row < nrow;
+      const int tok = i0 + (ok ? row : 0) / a.G, head = w.h * a.G + (ok ? row % a.G : 0);
+      float crow = a.scale_log2;
+      {
+        const uint4* src = reinterpret_cast<const uint4*>(
+            static_cast<const uint16_t*>(a.q) + (int64_t)(w.d.row0 + tok) * a.q_stride +
+            (int64_t)head * D);
+        uint4 x[D / 8];
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) x[i] = ok ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+        float down = 1.0f;
+        if (kBf16) {
+          float mx = 0.0f;
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i) {
+            const uint32_t y[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float2 f = pair_to_float2<true>(y[j]);
+              mx = fmaxf(mx, fmaxf(fabsf(f.x), fabsf(f.y)));
+            }
+          }
+          const int E = row_exponent(mx);
+          down = pow2f(-E);
+          crow *= pow2f(E);
+        }
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+          uint32_t y[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+          if (kBf16) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float2 f = pair_to_float2<true>(y[j]);
+              y[j] = pack_f16(f.x * down, f.y * down);
+            }
+          }
+          *reinterpret_cast<uint4*>(qt + sw128_off(qr, 8 * i, kAtom)) =
+              make_uint4(y[0], y[1], y[2], y[3]);
+        }
+      }
+      warp_arrive(&ctl.q_full[t]);
+      int rlo = w.u.lo, rhi = w.u.hi;
+      if (a.causal && ok) {
+        const int64_t p = (int64_t)w.d.len - w.d.n + tok;
+        rhi = (int)max((int64_t)0, min((int64_t)w.u.hi, p + 1));
+        if (a.window > 0) rlo = (int)max((int64_t)rlo, p - a.window + 1);
+      }
+
+      float m_ref = -INFINITY, l = 0.0f;
+      for (int j = t0, key0 = (w.u.g0 + t0) * kTileE; j < t1; ++j, ++it, ++cnt, key0 += kTileE) {
+        if (!warp_wait(&ctl.s_full[t], cnt & 1u, status)) {
+          alive = false;
+          break;
+        }
+        tc_fence_after();
+        uint32_t s[128];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) tmem_ld32(ts + 32 * i, s + 32 * i);
+        tmem_wait_ld();
+        if (__any_sync(0xffffffffu, key0 < rlo || key0 + kTileE > rhi)) {
+#pragma unroll
+          for (int i = 0; i < 128; ++i)
+            if (key0 + i < rlo || key0 + i >= rhi) s[i] = __float_as_uint(-INFINITY);
+        }
+        const float4* sc = ctl.sc[it & 3];
+        // ---- maximum ----
+        float xmax = -INFINITY;
+#pragma unroll
+        for (int gi = 0; gi < 8; ++gi) {
+          float mx = __uint_as_float(s[16 * gi]);
+#pragma unroll
+          for (int i = 1; i < 16; ++i) mx = fmaxf(mx, __uint_as_float(s[16 * gi + i]));
+          const float4 b = sc[gi];
+          xmax = fmaxf(xmax, fmaf(mx, fmaxf(crow * b.x, 1.17549435e-38f), b.y));
+        }
+        float alpha = 1.0f;
+        if (xmax > m_ref + kLazy) {
+          alpha = ex2(m_ref - xmax);
+          m_ref = xmax;
+        }
+        if (__any_sync(0xffffffffu, alpha != 1.0f)) {
+          l *= alpha;
+          // S_t(j) is done, so O_t(j - 1), issued before it, is too
+          if (j > t0) {
+#pragma unroll 1
+            for (int i = 0; i < D; i += 16) {
+              float o[16];
+              tmem_ld16(to + i, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int k = 0; k < 16; ++k) o[k] *= alpha;
+              tmem_st16(to + i, o);
+            }
+          }
+        }
+        // ---- weights ----
+        const float base = (m_ref == -INFINITY ? 0.0f : m_ref) - kHeadroom;
+#pragma unroll
+        for (int gi = 0; gi < 8; ++gi) {
+          const float4 b = sc[gi];
+          const float c = fmaxf(crow * b.x, 1.17549435e-38f), d = b.y - base;
+          float sum = 0.0f;
+#pragma unroll
+          for (int i = 0; i < 16; i += 2) {
+            const float p0 = ex2(fmaf(__uint_as_float(s[16 * gi + i]), c, d));
+            const float p1 = ex2(fmaf(__uint_as_float(s[16 * gi + i + 1]), c, d));
+            sum += p0 + p1;
+            s[8 * gi + i / 2] = pack_f16(p0, p1);
+          }
+          l = fmaf(sum, b.z, l);
+        }
+        tmem_st32(ts, s);
+        tmem_st32(ts + 32, s + 32);
+        tmem_wait_st();
+        warp_arrive(&ctl.p_full[t]);
+      }
+      if (!alive || !warp_wait(&ctl.o_full[t], units & 1u, status)) {
+        alive = false;
+        break;
+      }
+      ++units;
+      tc_fence_after();
+      // ---- output, or a part of it ----
+      const bool whole = w.whole();
+      const float inv = !whole ? 1.0f : l == 0.0f ? 0.0f : 1.0f / l;  // no visible token: zeros
+      const int64_t orow = (int64_t)(w.d.row0 + tok) * a.H + head;
+      float* part = reinterpret_cast<float*>(a.scratch) +
+                    ((size_t)blockIdx.x * 2 + (t0 == 0 ? 1 : 0)) * part_floats(kUnit, D);
+#pragma unroll 1
+      for (int i = 0; i < D; i += 32) {
+        uint32_t o[32];
+        tmem_ld32(to + i, o);
+        tmem_wait_ld();
+        if (!ok) continue;
+        if (whole) {
+          uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + orow * D + i);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint32_t y[4];
+#pragma unroll
+            for (int n = 0; n < 4; ++n)
+              y[n] = pair_from_floats<kBf16>(__uint_as_float(o[8 * k + 2 * n]) * inv,
+                                             __uint_as_float(o[8 * k + 2 * n + 1]) * inv);
+            dst[k] = make_uint4(y[0], y[1], y[2], y[3]);
+          }
+        } else {
+          uint4* dst = reinterpret_cast<uint4*>(part + (size_t)row * D + i);
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            dst[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+        }
+      }
+      if (ok) {
+        if (whole) {
+          if (a.lse)
+            a.lse[orow] = l == 0.0f ? -INFINITY
+                                    : ((m_ref == -INFINITY ? 0.0f : m_ref) - kHeadroom + __log2f(l)) * kLn2;
+        } else {
+          part[kUnit * D + row] = m_ref;
+          part[kUnit * D + kUnit + row] = l;
+        }
+      }
+    } while (warp_next(w, a));
+  } else if (warp < kMmaWarp) {
+    // ================= dequantisers =================
+    fewer_registers<kDeqRegs>();
+    const int dt = tid - kDeqWarp0 * 32, dw = dt >> 5;
+    const int sub = lane & 7, c4 = lane >> 3;
+    const int page_mask = (1 << a.c.page_shift) - 1;
+    uint4 kw[4][D / 64], vw[4][D / 64];
+    int pid[4];
+    float4 scale;
+    do {
+      const int32_t* table = a.c.table + (int64_t)w.s * a.c.max_pages;
+      const int t1 = w.t1, g0 = w.u.g0, lo = w.u.lo, hi = w.u.hi, h = w.h;
+      // page of a key: -1 where no row sees it or the entry is outside the cache
+      auto page_of = [&](int key) -> int {
+        if (key < lo || key >= hi) return -1;
+        const int p = table[key >> a.c.page_shift];
+        if (p >= 0 && p < a.c.n_pages) return p;
+        set_status(status, kStatusBadIndex);
+        return -1;
+      };
+      auto find = [&](int j) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          pid[i] = page_of((g0 + j) * kTileE + 32 * dw + 8 * i + sub);
+      };
+      auto load = [&](int j) {
+        const int key0 = (g0 + j) * kTileE;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int key = key0 + 32 * dw + 8 * i + sub;
+          const int64_t off =
+              ((((int64_t)pid[i] * a.c.H_kv + h) << a.c.page_shift) + (key & page_mask)) * D + 16 * c4;
+#pragma unroll
+          for (int hf = 0; hf < D / 64; ++hf) {
+            kw[i][hf] = vw[i][hf] = make_uint4(0, 0, 0, 0);
+            if (pid[i] >= 0) {
+              kw[i][hf] = __ldg(reinterpret_cast<const uint4*>(a.c.k + off + 64 * hf));
+              vw[i][hf] = __ldg(reinterpret_cast<const uint4*>(a.c.v + off + 64 * hf));
+            }
+          }
+        }
+        if (dt < 8) {  // the block scales of 16-key group dt
+          const int from = max(lo, key0 + 16 * dt), to = min(hi, key0 + 16 * dt + 16);
+          const int p = from < to ? page_of(from) : -1;
+          scale = make_float4(1.0f, -INFINITY, 0.0f, 0.0f);
+          if (p >= 0) {
+            const int64_t b = (int64_t)p * a.c.H_kv + h;
+            const float vs = a.c.v_scale[b];
+            scale = make_float4(a.c.k_scale[b], __log2f(vs), 1.0f / vs, 0.0f);
+          }
+        }
+      };
+      find(w.t0);
+      load(w.t0);
+      for (int j = w.t0; j < t1; ++j, ++it) {
+        const uint32_t st = it & 1u, par = ((it >> 1) & 1u) ^ 1u;
+        if (j + 1 < t1) find(j + 1);
+        if (!warp_wait(&ctl.k_empty[st], par, status)) {
+          alive = false;
+          break;
+        }
+        uint8_t* kt = smem + L::k + st * L::tile;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int hf = 0; hf < D / 64; ++hf)
+            put16(kt + hf * kAtom, 32 * dw + 8 * i + sub, c4, kw[i][hf]);
+        if (dt < 8) ctl.sc[it & 3][dt] = scale;
+        warp_arrive(&ctl.k_full[st]);
+        if (!warp_wait(&ctl.v_empty[st], par, status)) {
+          alive = false;
+          break;
+        }
+        uint8_t* vt = smem + L::v + st * L::tile;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int hf = 0; hf < D / 64; ++hf)
+            put16(vt + hf * kAtom, 32 * dw + 8 * i + sub, c4, vw[i][hf]);
+        warp_arrive(&ctl.v_full[st]);
+        // the next tile's loads only now: an arrive (release) waits for the loads
+        // that its thread has in flight
+        if (j + 1 < t1) load(j + 1);
+      }
+    } while (alive && warp_next(w, a));
+  } else {
+    fewer_registers<kMmaRegs>();
+  }
+  if (warp == kMmaWarp && lane == 0) {
+    // ================= MMA issuer =================
+    const uint32_t id_s = idesc_f16(kTileE, false);
+    const uint32_t id_o = idesc_f16(D, false) | (1u << 16);  // B (V) MN-major
+    const uint32_t sb = su32(smem);
+    const uint32_t dq = (uint32_t)sw128_desc(sb + L::q, 16, 1024);
+    const uint32_t dk = (uint32_t)sw128_desc(sb + L::k, 16, 1024);
+    const uint32_t dv = (uint32_t)sw128_desc(sb + L::v, kAtom, 1024);
+    const uint32_t hi = (uint32_t)(sw128_desc(0, 16, 1024) >> 32);
+    uint32_t cnt = 0, units = 0;  // bit t: parity of row tile t's softmax tiles, of its units
+    auto mma_s = [&](int t, uint32_t i) {
+      const uint32_t qa = dq + t * (L::tile >> 4), kb = dk + (i & 1u) * (L::tile >> 4);
+#pragma unroll
+      for (int x = 0; x < D / 16; ++x) {  // 16 channels: 32 bytes of atom x / 4
+        const uint32_t off = ((x >> 2) * kAtom + (x & 3) * 32) >> 4;
+        mma_ss(tm_s + t * 128, qa + off, kb + off, hi, id_s, x != 0);
+      }
+      mma_commit(su32(&ctl.s_full[t]));
+    };
+    auto mma_o = [&](int t, uint32_t i, bool first) {
+      const uint32_t vb = dv + (i & 1u) * (L::tile >> 4);
+#pragma unroll
+      for (int x = 0; x < kTileE / 16; ++x)  // 16 keys: 8 columns of P, 2048 bytes of V
+        mma_ts(tm_o + t * D, tm_s + t * 128 + 8 * x, vb + x * (2048 >> 4), hi, id_o,
+               x != 0 || !first);
+    };
+    do {
+      const int nt = w.rows(a.G) > 128 ? 2 : 1;
+      const uint32_t i0 = it;
+#pragma unroll 1
+      for (int t = 0; t < nt && alive; ++t) {
+        alive = mbar_wait(su32(&ctl.q_full[t]), (units >> t) & 1u, status);
+        units ^= 1u << t;
+      }
+      if (!alive || !(alive = mbar_wait(su32(&ctl.k_full[it & 1u]), (it >> 1) & 1u, status))) break;
+      tc_fence_after();
+#pragma unroll 1
+      for (int t = 0; t < nt; ++t) mma_s(t, it);
+      mma_commit(su32(&ctl.k_empty[it & 1u]));
+      for (int j = w.t0; j < w.t1; ++j, ++it) {
+        const bool more = j + 1 < w.t1;
+        if (!(alive = mbar_wait(su32(&ctl.v_full[it & 1u]), (it >> 1) & 1u, status))) break;
+#pragma unroll 1
+        for (int t = 0; t < nt; ++t) {
+          if (!(alive = mbar_wait(su32(&ctl.p_full[t]), (cnt >> t) & 1u, status))) break;
+          cnt ^= 1u << t;
+          tc_fence_after();
+          mma_o(t, it, it == i0);
+          if (t == nt - 1) mma_commit(su32(&ctl.v_empty[it & 1u]));
+          if (!more) mma_commit(su32(&ctl.o_full[t]));
+          if (more) {
+            if (t == 0 && !(alive = mbar_wait(su32(&ctl.k_full[(it + 1) & 1u]),
+                                              ((it + 1) >> 1) & 1u, status)))
+              break;
+            tc_fence_after();
+            mma_s(t, it + 1);
+            if (t == nt - 1) mma_commit(su32(&ctl.k_empty[(it + 1) & 1u]));
+          }
+        }
+        if (!alive) break;
+      }
+    } while (alive && w.next(a));
+    // nothing is in flight when tensor memory is freed
+    mma_commit(su32(&ctl.done));
+    mbar_wait(su32(&ctl.done), 0u, status);
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kMmaWarp)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tm_s));
+}
+
+template <int D, bool kBf16>
+__global__ void __launch_bounds__(128)
+kv8_merge_tc_kernel(const __grid_constant__ Kv8AttnArgs a, int workers) {
+  merge_parts<kUnit, kTileE, 4, D, kBf16>(a, workers, kHeadroom);
+}
+
+template <int D, bool kBf16>
+cudaError_t attn_tc_t(const Kv8AttnArgs& a, cudaStream_t stream) {
+  using L = Lay<D>;
+  cudaError_t e = cudaFuncSetAttribute(kv8_attn_tc_kernel<D, kBf16>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, L::alloc);
+  if (e != cudaSuccess) return e;
+  const int workers = device_sm_count();
+  kv8_attn_tc_kernel<D, kBf16><<<workers, kThreads, L::alloc, stream>>>(a);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  return launch_kernel(kv8_merge_tc_kernel<D, kBf16>, dim3(workers, 8), dim3(128), 0, stream,
+                       /*pdl=*/true, a, workers);
+}
+
+}  // namespace
+
+size_t kv8_attn_tc_scratch_bytes(int D) {
+  return align_up((size_t)device_sm_count() * 2 * part_floats(kUnit, D) * 4, 256);
+}
+
+cudaError_t launch_kv8_attn_tc(const Kv8AttnArgs& a, int type, cudaStream_t stream) {
+  if (a.c.D == 128)
+    return type == CSA2_BF16 ? attn_tc_t<128, true>(a, stream) : attn_tc_t<128, false>(a, stream);
+  return type == CSA2_BF16 ? attn_tc_t<64, true>(a, stream) : attn_tc_t<64, false>(a, stream);
+}
+
+}  // namespace csa2

@@ -193,8 +193,13 @@ struct Walk {
   Dims d;
   Span u;
 
-  __device__ __forceinline__ Walk(const Kv8AttnArgs& a, const Range& r)
-      : s(r.s), m(r.m), h(r.h), t0(r.t0), pos(r.w0), end(r.w1) {
+  __device__ __forceinline__ void start(const Kv8AttnArgs& a, const Range& r) {
+    s = r.s;
+    m = r.m;
+    h = r.h;
+    t0 = r.t0;
+    pos = r.w0;
+    end = r.w1;
     d = seq_dims<kUnit>(a, s);
     u = unit_span<kGranule>(a, d, m);
     t1 = (int)min((int64_t)u.ng, t0 + (end - pos));
@@ -265,7 +270,7 @@ __device__ __forceinline__ int row_exponent(float mx) {
 }
 
 // Joins the parts of the cut units: block (x, y) takes the unit whose first
-// part ends worker x's range, rows y * (kThreads / (D / 4)) .. of it.  The
+// part ends worker x's range, every gridDim.y-th group of its rows.  The
 // ranges depend on kv_len and cu alone, which were there before the kernel
 // whose parts are joined: only the parts are waited for.
 template <int kUnit, int kGranule, int kWarps, int D, bool kBf16>
@@ -276,7 +281,8 @@ __device__ __forceinline__ void merge_parts(const Kv8AttnArgs& a, int workers, f
     pdl_wait();
     return;
   }
-  Walk<kUnit, kGranule> w(a, rg);
+  Walk<kUnit, kGranule> w;
+  w.start(a, rg);
   while (w.pos + (w.t1 - w.t0) < w.end && w.next(a)) {
   }
   pdl_wait();
@@ -286,35 +292,37 @@ __device__ __forceinline__ void merge_parts(const Kv8AttnArgs& a, int workers, f
   const int64_t end = w.pos + w.u.ng;
   const int last = (int)((end * rg.workers - 1) / rg.total);
   constexpr int kTpr = D / 4, kRowsPer = kWarps * 32 / kTpr;
-  const int row = blockIdx.y * kRowsPer + threadIdx.x / kTpr, ch = (threadIdx.x % kTpr) * 4;
-  if (row >= w.rows(a.G)) return;
   const float* base = reinterpret_cast<const float*>(a.scratch);
   const size_t pf = part_floats(kUnit, D);
-  float m = -INFINITY, l = 0.0f;
-  float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  const int ch = (threadIdx.x % kTpr) * 4, nrow = w.rows(a.G);
+  for (int row = blockIdx.y * kRowsPer + threadIdx.x / kTpr; row < nrow;
+       row += gridDim.y * kRowsPer) {
+    float m = -INFINITY, l = 0.0f;
+    float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 4
-  for (int p = blockIdx.x; p <= last; ++p) {
-    const float* src = base + ((size_t)p * 2 + (p == (int)blockIdx.x ? 1 : 0)) * pf;
-    const float pm = __ldcg(src + kUnit * D + row), pl = __ldcg(src + kUnit * D + kUnit + row);
-    const float4 y = __ldcg(reinterpret_cast<const float4*>(src + (size_t)row * D + ch));
-    const float nm = fmaxf(m, pm), z = nm == -INFINITY ? 0.0f : nm;
-    const float f0 = ex2(m - z), f1 = ex2(pm - z);
-    m = nm;
-    l = l * f0 + pl * f1;
-    x.x = x.x * f0 + y.x * f1;
-    x.y = x.y * f0 + y.y * f1;
-    x.z = x.z * f0 + y.z * f1;
-    x.w = x.w * f0 + y.w * f1;
+    for (int p = blockIdx.x; p <= last; ++p) {
+      const float* src = base + ((size_t)p * 2 + (p == (int)blockIdx.x ? 1 : 0)) * pf;
+      const float pm = __ldcg(src + kUnit * D + row), pl = __ldcg(src + kUnit * D + kUnit + row);
+      const float4 y = __ldcg(reinterpret_cast<const float4*>(src + (size_t)row * D + ch));
+      const float nm = fmaxf(m, pm), z = nm == -INFINITY ? 0.0f : nm;
+      const float f0 = ex2(m - z), f1 = ex2(pm - z);
+      m = nm;
+      l = l * f0 + pl * f1;
+      x.x = x.x * f0 + y.x * f1;
+      x.y = x.y * f0 + y.y * f1;
+      x.z = x.z * f0 + y.z * f1;
+      x.w = x.w * f0 + y.w * f1;
+    }
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;  // no visible token: zeros
+    const int64_t orow =
+        (int64_t)(w.d.row0 + w.first_row() + row / a.G) * a.H + w.h * a.G + row % a.G;
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + orow * D + ch) =
+        make_uint2(pair_from_floats<kBf16>(x.x * inv, x.y * inv),
+                   pair_from_floats<kBf16>(x.z * inv, x.w * inv));
+    if (a.lse && ch == 0)
+      a.lse[orow] =
+          l == 0.0f ? -INFINITY : ((m == -INFINITY ? 0.0f : m) - headroom + __log2f(l)) * kLn2;
   }
-  const float inv = l == 0.0f ? 0.0f : 1.0f / l;  // no visible token: zeros
-  const int64_t orow =
-      (int64_t)(w.d.row0 + w.first_row() + row / a.G) * a.H + w.h * a.G + row % a.G;
-  *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + orow * D + ch) =
-      make_uint2(pair_from_floats<kBf16>(x.x * inv, x.y * inv),
-                 pair_from_floats<kBf16>(x.z * inv, x.w * inv));
-  if (a.lse && ch == 0)
-    a.lse[orow] =
-        l == 0.0f ? -INFINITY : ((m == -INFINITY ? 0.0f : m) - headroom + __log2f(l)) * kLn2;
 }
 
 }  // namespace kv8

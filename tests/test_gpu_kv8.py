@@ -256,6 +256,39 @@ def test_attn_prompts_of_uneven_lengths(C, dtype, causal, window, D, page, Hk, G
     _check_attn(C, w, _q(w.rng, cu[-1], Hk * G, D, dtype), cu, causal, window)
 
 
+@pytest.mark.parametrize("D,page,G,n", [(128, 64, 17, 1), (64, 16, 32, 1), (128, 32, 33, 2), (128, 64, 64, 1),
+                                        (64, 64, 65, 1), (128, 128, 100, 2), (64, 32, 256, 1), (128, 16, 129, 1)])
+def test_attn_many_query_heads_per_kv_head(C, D, page, G, n):
+    lens = [1, 33, 0, 200, 385]
+    w = World(C, 32 + G, lens, 1, D, page).fill()
+    _check_attn(C, w, _q(w.rng, n * len(lens), G, D, BF16), None)
+
+
+@pytest.mark.parametrize("D,page,window", [(128, 64, 0), (64, 16, 0), (128, 16, 700)])
+def test_attn_chunk_over_a_long_context_is_split(C, D, page, window):
+    # two units over a long context: the tokens are split over every CTA and joined
+    w = World(C, 33, [6001], 2, D, page).fill()
+    q = _q(w.rng, 67, 4, D, BF16)
+    a = _check_attn(C, w, q, None, True, window)
+    b = _check_attn(C, w, q, None, True, window)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_attn_prompt_rows_with_growing_logits(C, D):
+    # logits that grow along the keys: the running maximum moves in every tile, past a lazy margin
+    L = 700
+    w = World(C, 34, [L], 1, D, 64).fill(span=1)
+    for j in range(L):
+        p = w.table[0, j // 64]
+        w.k[p, 0, j % 64] = R.encode(R.E4M3[w.k[p, 0, j % 64]] * 0.02)
+        w.k[p, 0, j % 64, 0] = R.encode(np.array(0.6 * j))
+        w.ks[p] = 2.0 ** -3
+    q = _q(w.rng, 140, 1, D, BF16, 0.2)
+    q[:, 0, 0] = 4.0
+    _check_attn(C, w, q, None, scale=0.3)
+
+
 def test_attn_long_context_split_over_the_grid(C):
     # two sequences, one head: the tokens are split over every CTA and joined
     lens = [5000, 3001]
