@@ -16,13 +16,21 @@
 //   warps 0-3, 4-7  softmax of row tile 0, 1: a thread owns a row (a tensor-memory
 //                   lane), so row maxima and sums need no exchange.  The reference
 //                   maximum is lazy: it moves, and O is rescaled, only when a logit
-//                   passes it by more than 2^8 (weights stay below 2^15)
-//   warps 8-11      dequantisers: E4M3 codes from global memory (through L2: the
-//                   units of a sequence share them) to fp16 in shared memory,
-//                   128-byte swizzled, double buffered; keys that no row of the
-//                   unit may see, and pages outside the cache, are zeros
-//   warp 12         tensor memory; lane 0 issues every MMA (13-15 only complete
-//                   its warpgroup, for the register split)
+//                   passes it by more than 2^8 (weights stay below 2^15).  So the
+//                   weights are formed in one pass with the old reference, and only
+//                   a tile that passes it is looked through and formed again
+//   warps 8-11      dequantisers: E4M3 codes to fp16, 128-byte swizzled, double
+//                   buffered; keys that no row of the unit may see, and those of
+//                   pages outside the cache, become zeros
+//   warp 12         tensor memory; lane 0 issues every MMA
+//   warp 13         loader: the block table and scales, and the codes of a tile's
+//                   pages into shared memory by bulk copies (through L2, where the
+//                   units of a sequence share them); a tile's K is requested while
+//                   its predecessor's V is converted and the reverse
+//   (warps 14, 15 only complete their warpgroup, for the register split)
+// Measured before the loader had a warp of its own (the dequantisers looked up
+// pages and scales and loaded to registers): 6600 cycles a pair of tiles against
+// the 2048 of its MMAs, 3000 of them in those dependent loads.
 // Every wait is bounded (about 2 s): a role that gives up sets the timeout
 // status and leaves, the others follow, and tensor memory is freed.
 #include "kv8_sched.cuh"
@@ -34,11 +42,11 @@ namespace {
 using namespace kv8;
 using namespace tc;
 
-constexpr int kSoftWarps = 8, kDeqWarp0 = 8, kDeqWarps = 4, kMmaWarp = 12;
+constexpr int kSoftWarps = 8, kDeqWarp0 = 8, kDeqWarps = 4, kMmaWarp = 12, kLoadWarp = 13;
 constexpr int kWarps = 16, kThreads = kWarps * 32;
 // Registers a thread after the roles part (four warpgroups, 512 in all: the 128
-// a thread of the launch): a softmax thread holds a whole row of S.
-constexpr int kSoftRegs = 176, kDeqRegs = 112, kMmaRegs = 48;
+// a thread of the launch): a softmax thread holds a row of P and a part of S.
+constexpr int kSoftRegs = 184, kDeqRegs = 80, kMmaRegs = 64;
 static_assert(2 * kSoftRegs + kDeqRegs + kMmaRegs <= 512, "register split");
 constexpr int kUnit = 256;      // query rows of a unit
 constexpr int kTileE = 128;     // keys of a tile (and rows of a row tile)
@@ -48,19 +56,25 @@ constexpr uint32_t kAtom = 128 * 128;            // bytes: 128 rows of 64 fp16 c
 template <int D>
 struct Lay {
   static constexpr uint32_t tile = (D / 64) * kAtom;  // bytes of Q_t, of a K or a V stage
-  static constexpr uint32_t q = 0, k = 2 * tile, v = 4 * tile, ctl = 6 * tile;
+  static constexpr uint32_t raw = kTileE * D;         // bytes of a tile's codes of K (or V)
+  static constexpr uint32_t q = 0, k = 2 * tile, v = 4 * tile, rk = 6 * tile, rv = rk + raw;
+  static constexpr uint32_t ctl = rv + raw;
   static constexpr uint32_t alloc = ctl + 2048 + 1024;  // slack to align the base to 1 KiB
 };
 static_assert(Lay<128>::alloc <= 232448, "shared memory");
 
 struct Ctl {
-  float4 sc[4][8];  // of a tile's 16-key groups: K scale, log2 V scale, 1 / V scale
+  // of a tile's 16-key groups: K scale, log2 V scale, 1 / V scale (0: nothing of it is
+  // seen).  Four tiles: the loader is at most one ahead of the dequantisers, which
+  // are at most two ahead of the slower softmax
+  float4 sc[4][8];
+  int32_t clean[4];  // every key of the tile is seen by some row
+  uint64_t rk_full, rk_empty, rv_full, rv_empty;  // the codes of a tile
   uint64_t q_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_full[2];
   uint64_t done;
   RangeSmem<kWarps> range;
-  Walk<kUnit, kTileE> walk[kMmaWarp + 1];  // each warp's own (kept out of registers)
+  Walk<kUnit, kTileE> walk[kLoadWarp + 1];  // each warp's own (kept out of registers)
   uint32_t tmem;
-  int32_t abort;
 };
 static_assert(sizeof(Ctl) <= 2048, "control block");
 
@@ -135,9 +149,61 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* x) {
       : "memory");
 }
 
+// Waits for the loads from tensor memory; x is theirs.
+__device__ __forceinline__ void tmem_wait_ld32(uint32_t* x) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(x[0]), "+r"(x[1]), "+r"(x[2]), "+r"(x[3]), "+r"(x[4]), "+r"(x[5]),
+                 "+r"(x[6]), "+r"(x[7]), "+r"(x[8]), "+r"(x[9]), "+r"(x[10]), "+r"(x[11]),
+                 "+r"(x[12]), "+r"(x[13]), "+r"(x[14]), "+r"(x[15]), "+r"(x[16]), "+r"(x[17]),
+                 "+r"(x[18]), "+r"(x[19]), "+r"(x[20]), "+r"(x[21]), "+r"(x[22]), "+r"(x[23]),
+                 "+r"(x[24]), "+r"(x[25]), "+r"(x[26]), "+r"(x[27]), "+r"(x[28]), "+r"(x[29])
+               :
+               : "memory");
+  asm volatile("" : "+r"(x[30]), "+r"(x[31]));
+}
+
+// Pairs of fp32 operations in one instruction.
+struct F2 {
+  float lo, hi;
+};
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "mov.b64 c, {%6, %7};\n\tfma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(r.lo), "=f"(r.hi)
+      : "f"(a.lo), "f"(a.hi), "f"(b.lo), "f"(b.hi), "f"(c.lo), "f"(c.hi));
+  return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 r;
+  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(r.lo), "=f"(r.hi)
+      : "f"(a.lo), "f"(a.hi), "f"(b.lo), "f"(b.hi));
+  return r;
+}
+
+// Columns key .. key + 31 of S that the row does not see become -infinity.
+__device__ __forceinline__ void mask32(uint32_t* s, int key, int rlo, int rhi) {
+#pragma unroll
+  for (int i = 0; i < 32; ++i)
+    if (key + i < rlo || key + i >= rhi) s[i] = 0xFF800000u;
+}
+
+// `bytes` contiguous bytes of global memory into shared memory, completing on bar.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
+                                          uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
+          "r"(dst), "l"(src), "r"(bytes), "r"(bar)
+      : "memory");
+}
+
 // 16 E4M3 codes -> fp16, into 16-byte chunks 2 c4, 2 c4 + 1 of key e of an atom.
-__device__ __forceinline__ void put16(uint8_t* atom, int e, int c4, uint4 w) {
-  const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+// swap: the second chunk first (the lanes of a warp that write another atom of the
+// same keys then meet other banks).
+__device__ __forceinline__ void put16(uint8_t* atom, int e, int c4, uint4 w, bool swap) {
+  const uint32_t x[4] = {swap ? w.z : w.x, swap ? w.w : w.y, swap ? w.x : w.z, swap ? w.y : w.w};
   uint32_t o[8];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -147,7 +213,7 @@ __device__ __forceinline__ void put16(uint8_t* atom, int e, int c4, uint4 w) {
   uint8_t* row = atom + (e >> 3) * 1024 + (e & 7) * 128;
 #pragma unroll
   for (int i = 0; i < 2; ++i)
-    *reinterpret_cast<uint4*>(row + (((2 * c4 + i) ^ (e & 7)) << 4)) =
+    *reinterpret_cast<uint4*>(row + (((2 * c4 + (i ^ (int)swap)) ^ (e & 7)) << 4)) =
         make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
 }
 
@@ -184,10 +250,14 @@ kv8_attn_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
       mbar_init(su32(&ctl.o_full[i]), 1);
     }
     mbar_init(su32(&ctl.done), 1);
+    mbar_init(su32(&ctl.rk_full), 1);
+    mbar_init(su32(&ctl.rv_full), 1);
+    mbar_init(su32(&ctl.rk_empty), kDeqWarps);
+    mbar_init(su32(&ctl.rv_empty), kDeqWarps);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  Walk<kUnit, kTileE>& w = ctl.walk[min(warp, kMmaWarp)];
-  if (warp <= kMmaWarp && lane == 0) w.start(a, rg);
+  Walk<kUnit, kTileE>& w = ctl.walk[min(warp, kLoadWarp)];
+  if (warp <= kLoadWarp && lane == 0) w.start(a, rg);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -267,32 +337,53 @@ kv8_attn_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
           break;
         }
         tc_fence_after();
-        uint32_t s[128];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) tmem_ld32(ts + 32 * i, s + 32 * i);
-        tmem_wait_ld();
-        if (__any_sync(0xffffffffu, key0 < rlo || key0 + kTileE > rhi)) {
-#pragma unroll
-          for (int i = 0; i < 128; ++i)
-            if (key0 + i < rlo || key0 + i >= rhi) s[i] = __float_as_uint(-INFINITY);
-        }
         const float4* sc = ctl.sc[it & 3];
-        // ---- maximum ----
-        float xmax = -INFINITY;
+        const bool masked = __any_sync(0xffffffffu, key0 < rlo || key0 + kTileE > rhi);
+        uint32_t p[64];
+        float sum, top;
+        // the weights with the reference as it is; `top`: the largest exponent
+        auto weights = [&]() {
+          const float base = (m_ref == -INFINITY ? 0.0f : m_ref) - kHeadroom;
+          uint32_t s[2][32];
+          tmem_ld32(ts, s[0]);
+          sum = 0.0f;
+          top = -INFINITY;
 #pragma unroll
-        for (int gi = 0; gi < 8; ++gi) {
-          float mx = __uint_as_float(s[16 * gi]);
+          for (int i = 0; i < 4; ++i) {
+            uint32_t* x = s[i & 1];
+            tmem_wait_ld32(x);
+            if (i < 3) tmem_ld32(ts + 32 * (i + 1), s[(i + 1) & 1]);
+            if (masked) mask32(x, key0 + 32 * i, rlo, rhi);
 #pragma unroll
-          for (int i = 1; i < 16; ++i) mx = fmaxf(mx, __uint_as_float(s[16 * gi + i]));
-          const float4 b = sc[gi];
-          xmax = fmaxf(xmax, fmaf(mx, fmaxf(crow * b.x, 1.17549435e-38f), b.y));
-        }
-        float alpha = 1.0f;
-        if (xmax > m_ref + kLazy) {
-          alpha = ex2(m_ref - xmax);
-          m_ref = xmax;
-        }
-        if (__any_sync(0xffffffffu, alpha != 1.0f)) {
+            for (int gi = 0; gi < 2; ++gi) {
+              const float4 b = sc[2 * i + gi];
+              const float c = fmaxf(crow * b.x, 1.17549435e-38f), d = b.y - base;
+              F2 part[2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};
+#pragma unroll
+              for (int k = 0; k < 16; k += 2) {
+                const F2 y = fma2({__uint_as_float(x[16 * gi + k]), __uint_as_float(x[16 * gi + k + 1])},
+                                  {c, c}, {d, d});
+                top = fmaxf(top, fmaxf(y.lo, y.hi));
+                const F2 w2 = {ex2(y.lo), ex2(y.hi)};
+                part[(k >> 1) & 1] = add2(part[(k >> 1) & 1], w2);
+                p[16 * i + 8 * gi + k / 2] = pack_f16(w2.lo, w2.hi);
+              }
+              const F2 both = add2(part[0], part[1]);
+              sum = fmaf(both.lo + both.hi, b.z, sum);
+            }
+          }
+        };
+        weights();
+        // a row whose first visible key this is, or whose reference is passed
+        bool again = __any_sync(0xffffffffu, (m_ref == -INFINITY && top > -INFINITY) ||
+                                                 top > kHeadroom + kLazy);
+        if (again) {
+          const float x = top + ((m_ref == -INFINITY ? 0.0f : m_ref) - kHeadroom);  // the largest logit
+          float alpha = 1.0f;
+          if (x > m_ref + kLazy || m_ref == -INFINITY) {
+            alpha = x == -INFINITY ? 1.0f : ex2(m_ref - x);
+            m_ref = x;
+          }
           l *= alpha;
           // S_t(j) is done, so O_t(j - 1), issued before it, is too
           if (j > t0) {
@@ -306,25 +397,11 @@ kv8_attn_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
               tmem_st16(to + i, o);
             }
           }
+          weights();
         }
-        // ---- weights ----
-        const float base = (m_ref == -INFINITY ? 0.0f : m_ref) - kHeadroom;
-#pragma unroll
-        for (int gi = 0; gi < 8; ++gi) {
-          const float4 b = sc[gi];
-          const float c = fmaxf(crow * b.x, 1.17549435e-38f), d = b.y - base;
-          float sum = 0.0f;
-#pragma unroll
-          for (int i = 0; i < 16; i += 2) {
-            const float p0 = ex2(fmaf(__uint_as_float(s[16 * gi + i]), c, d));
-            const float p1 = ex2(fmaf(__uint_as_float(s[16 * gi + i + 1]), c, d));
-            sum += p0 + p1;
-            s[8 * gi + i / 2] = pack_f16(p0, p1);
-          }
-          l = fmaf(sum, b.z, l);
-        }
-        tmem_st32(ts, s);
-        tmem_st32(ts + 32, s + 32);
+        l += sum;
+        tmem_st32(ts, p);
+        tmem_st32(ts + 32, p + 32);
         tmem_wait_st();
         warp_arrive(&ctl.p_full[t]);
       }
@@ -378,90 +455,117 @@ kv8_attn_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
   } else if (warp < kMmaWarp) {
     // ================= dequantisers =================
     fewer_registers<kDeqRegs>();
-    const int dt = tid - kDeqWarp0 * 32, dw = dt >> 5;
-    const int sub = lane & 7, c4 = lane >> 3;
-    const int page_mask = (1 << a.c.page_shift) - 1;
-    uint4 kw[4][D / 64], vw[4][D / 64];
-    int pid[4];
-    float4 scale;
+    // a lane converts 16 channels (chunk c of the key's codes) of D / 16 lanes a
+    // key: it reads 16 contiguous bytes of a run, and writes two 16-byte chunks of
+    // atom c / 4
+    constexpr int kCh = D / 16, kKeys = 32 / kCh;  // lanes a key, keys an instruction
+    const int dw = warp - kDeqWarp0, c = lane % kCh, sub = lane / kCh;
+    const bool swap = c >= 4;
     do {
-      const int32_t* table = a.c.table + (int64_t)w.s * a.c.max_pages;
+      const int t1 = w.t1, g0 = w.u.g0, lo = w.u.lo, hi = w.u.hi;
+      for (int j = w.t0; j < t1; ++j, ++it) {
+        const uint32_t st = it & 1u, par = ((it >> 1) & 1u) ^ 1u;
+        const int key0 = (g0 + j) * kTileE;
+        auto convert = [&](const uint8_t* raw, uint8_t* to, bool clean) {
+#pragma unroll 4
+          for (int i = 0; i < 32 / kKeys; ++i) {
+            const int e = 32 * dw + kKeys * i + sub;
+            uint4 x = *reinterpret_cast<const uint4*>(raw + e * D + 16 * c);
+            if (!clean && (key0 + e < lo || key0 + e >= hi || ctl.sc[it & 3][e >> 4].z == 0.0f))
+              x = make_uint4(0, 0, 0, 0);
+            put16(to + (c >> 2) * kAtom, e, c & 3, x, swap);
+          }
+        };
+        if (!warp_wait(&ctl.rk_full, it & 1u, status) ||
+            !warp_wait(&ctl.k_empty[st], par, status)) {
+          alive = false;
+          break;
+        }
+        const bool clean = ctl.clean[it & 3] != 0;
+        convert(smem + L::rk, smem + L::k + st * L::tile, clean);
+        warp_arrive(&ctl.k_full[st]);
+        if (lane == 0) mbar_arrive(su32(&ctl.rk_empty));
+        if (!warp_wait(&ctl.rv_full, it & 1u, status) ||
+            !warp_wait(&ctl.v_empty[st], par, status)) {
+          alive = false;
+          break;
+        }
+        convert(smem + L::rv, smem + L::v + st * L::tile, clean);
+        warp_arrive(&ctl.v_full[st]);
+        if (lane == 0) mbar_arrive(su32(&ctl.rv_empty));
+      }
+    } while (alive && warp_next(w, a));
+  } else {
+    fewer_registers<kMmaRegs>();
+  }
+  if (warp == kLoadWarp) {
+    // ================= loader =================
+    // lanes 0-7: a 16-key group of the tile each; the first of a page's groups
+    // (a run) requests the page's codes
+    const int page = 1 << a.c.page_shift, run = min(page, kTileE);
+    const uint32_t run_bytes = (uint32_t)(run * D);
+    const bool leads = lane < 8 && (16 * lane) % run == 0;
+    uint32_t ks_out = 0, vs_out = 0;  // tiles whose K, V have been requested
+    do {
       const int t1 = w.t1, g0 = w.u.g0, lo = w.u.lo, hi = w.u.hi, h = w.h;
-      // page of a key: -1 where no row sees it or the entry is outside the cache
-      auto page_of = [&](int key) -> int {
-        if (key < lo || key >= hi) return -1;
+      const int32_t* table = a.c.table + (int64_t)w.s * a.c.max_pages;
+      // page of the lane's group in tile j: -1 where no key of its run is seen or the
+      // entry is outside the cache
+      auto find = [&](int j) -> int {
+        const int key = (g0 + j) * kTileE + 16 * lane, from = key & ~(run - 1);
+        if (j >= t1 || lane >= 8 || from >= hi || from + run <= lo) return -1;
         const int p = table[key >> a.c.page_shift];
         if (p >= 0 && p < a.c.n_pages) return p;
         set_status(status, kStatusBadIndex);
         return -1;
       };
-      auto find = [&](int j) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          pid[i] = page_of((g0 + j) * kTileE + 32 * dw + 8 * i + sub);
-      };
-      auto load = [&](int j) {
-        const int key0 = (g0 + j) * kTileE;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int key = key0 + 32 * dw + 8 * i + sub;
-          const int64_t off =
-              ((((int64_t)pid[i] * a.c.H_kv + h) << a.c.page_shift) + (key & page_mask)) * D + 16 * c4;
-#pragma unroll
-          for (int hf = 0; hf < D / 64; ++hf) {
-            kw[i][hf] = vw[i][hf] = make_uint4(0, 0, 0, 0);
-            if (pid[i] >= 0) {
-              kw[i][hf] = __ldg(reinterpret_cast<const uint4*>(a.c.k + off + 64 * hf));
-              vw[i][hf] = __ldg(reinterpret_cast<const uint4*>(a.c.v + off + 64 * hf));
-            }
-          }
-        }
-        if (dt < 8) {  // the block scales of 16-key group dt
-          const int from = max(lo, key0 + 16 * dt), to = min(hi, key0 + 16 * dt + 16);
-          const int p = from < to ? page_of(from) : -1;
-          scale = make_float4(1.0f, -INFINITY, 0.0f, 0.0f);
-          if (p >= 0) {
-            const int64_t b = (int64_t)p * a.c.H_kv + h;
-            const float vs = a.c.v_scale[b];
-            scale = make_float4(a.c.k_scale[b], __log2f(vs), 1.0f / vs, 0.0f);
-          }
+      float ks = 0.0f, vs = 0.0f;
+      auto scales = [&](int p) {
+        if (p >= 0) {
+          ks = __ldg(a.c.k_scale + (int64_t)p * a.c.H_kv + h);
+          vs = __ldg(a.c.v_scale + (int64_t)p * a.c.H_kv + h);
         }
       };
-      find(w.t0);
-      load(w.t0);
+      int pid = find(w.t0), next = find(w.t0 + 1);
+      scales(pid);
       for (int j = w.t0; j < t1; ++j, ++it) {
-        const uint32_t st = it & 1u, par = ((it >> 1) & 1u) ^ 1u;
-        if (j + 1 < t1) find(j + 1);
-        if (!warp_wait(&ctl.k_empty[st], par, status)) {
+        const int key0 = (g0 + j) * kTileE, key = key0 + 16 * lane;
+        const bool seen = pid >= 0 && key < hi && key + 16 > lo;
+        const uint32_t all = __ballot_sync(0xffffffffu, seen || lane >= 8);
+        const float4 sc = seen ? make_float4(ks, __log2f(vs), 1.0f / vs, 0.0f)
+                               : make_float4(1.0f, -INFINITY, 0.0f, 0.0f);
+        const int64_t off = ((((int64_t)pid * a.c.H_kv + h) << a.c.page_shift) + (key & (page - 1))) * D;
+        const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, leads && pid >= 0)) * run_bytes;
+        if (!warp_wait(&ctl.rk_empty, (it & 1u) ^ 1u, status)) {
           alive = false;
           break;
         }
-        uint8_t* kt = smem + L::k + st * L::tile;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int hf = 0; hf < D / 64; ++hf)
-            put16(kt + hf * kAtom, 32 * dw + 8 * i + sub, c4, kw[i][hf]);
-        if (dt < 8) ctl.sc[it & 3][dt] = scale;
-        warp_arrive(&ctl.k_full[st]);
-        if (!warp_wait(&ctl.v_empty[st], par, status)) {
+        if (lane < 8) ctl.sc[it & 3][lane] = sc;
+        if (lane == 0)
+          ctl.clean[it & 3] = all == 0xffffffffu && key0 >= lo && key0 + kTileE <= hi;
+        __syncwarp();
+        if (lane == 0) mbar_expect_tx(su32(&ctl.rk_full), bytes);
+        __syncwarp();
+        if (leads && pid >= 0)
+          bulk_load(su32(smem + L::rk) + 16 * lane * D, a.c.k + off, run_bytes, su32(&ctl.rk_full));
+        ++ks_out;
+        if (!warp_wait(&ctl.rv_empty, (it & 1u) ^ 1u, status)) {
           alive = false;
           break;
         }
-        uint8_t* vt = smem + L::v + st * L::tile;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int hf = 0; hf < D / 64; ++hf)
-            put16(vt + hf * kAtom, 32 * dw + 8 * i + sub, c4, vw[i][hf]);
-        warp_arrive(&ctl.v_full[st]);
-        // the next tile's loads only now: an arrive (release) waits for the loads
-        // that its thread has in flight
-        if (j + 1 < t1) load(j + 1);
+        if (lane == 0) mbar_expect_tx(su32(&ctl.rv_full), bytes);
+        __syncwarp();
+        if (leads && pid >= 0)
+          bulk_load(su32(smem + L::rv) + 16 * lane * D, a.c.v + off, run_bytes, su32(&ctl.rv_full));
+        ++vs_out;
+        pid = next;
+        scales(pid);
+        next = find(j + 2);
       }
     } while (alive && warp_next(w, a));
-  } else {
-    fewer_registers<kMmaRegs>();
+    // no copy is in flight when the CTA ends: the last ones are waited for
+    if (ks_out > 0) warp_wait(&ctl.rk_full, (ks_out - 1) & 1u, status);
+    if (vs_out > 0) warp_wait(&ctl.rv_full, (vs_out - 1) & 1u, status);
   }
   if (warp == kMmaWarp && lane == 0) {
     // ================= MMA issuer =================

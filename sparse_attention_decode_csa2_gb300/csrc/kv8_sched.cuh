@@ -238,10 +238,11 @@ __host__ __device__ constexpr size_t part_floats(int unit, int D) {
   return (size_t)unit * D + 2 * (size_t)unit;
 }
 
-// 2^x by the hardware's approximation (relative error about 2^-22).
+// 2^x by the hardware's approximation (relative error about 2^-22); results
+// below 2^-126 are zeros (the form that keeps them costs three more instructions).
 __device__ __forceinline__ float ex2(float x) {
   float r;
-  asm("ex2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
 
