@@ -112,21 +112,31 @@ __device__ __forceinline__ void warp_arrive(uint64_t* bar) {
 
 // MMAs whose shared-memory descriptors are given by their low words (address and
 // leading offset); the high words are the same for all of a kind.  A from shared
-// memory, and A from tensor memory.
-__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t hi,
-                                       uint32_t idesc, uint32_t accumulate) {
+// memory, and A from tensor memory.  Every lane of the warp comes here with the
+// same operands (they stay in uniform registers), the leader issues.
+__device__ __forceinline__ void mma_ss(uint32_t leader, uint32_t d, uint32_t a_lo, uint32_t b_lo,
+                                       uint32_t hi, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 x, y;\n\tsetp.ne.b32 p, %5, 0;\n\tsetp.ne.b32 q, %6, 0;\n\t"
       "mov.b64 x, {%1, %3};\n\tmov.b64 y, {%2, %3};\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, p;\n\t}" ::"r"(d),
-      "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"(accumulate));
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, p;\n\t}" ::"r"(d),
+      "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"(accumulate), "r"(leader));
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t hi,
-                                       uint32_t idesc, uint32_t accumulate) {
+__device__ __forceinline__ void mma_ts(uint32_t leader, uint32_t d, uint32_t a, uint32_t b_lo,
+                                       uint32_t hi, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 y;\n\tsetp.ne.b32 p, %5, 0;\n\tmov.b64 y, {%2, %3};\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %4, p;\n\t}" ::"r"(d),
-      "r"(a), "r"(b_lo), "r"(hi), "r"(idesc), "r"(accumulate));
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 y;\n\tsetp.ne.b32 p, %5, 0;\n\tsetp.ne.b32 q, %6, 0;\n\t"
+      "mov.b64 y, {%2, %3};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %4, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b_lo), "r"(hi), "r"(idesc), "r"(accumulate), "r"(leader));
+}
+__device__ __forceinline__ void commit_if(uint32_t leader, uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
+          su32(bar)),
+      "r"(leader)
+      : "memory");
 }
 
 #define CSA2_R8(x, i) "=r"(x[i]), "=r"(x[i + 1]), "=r"(x[i + 2]), "=r"(x[i + 3]), \
@@ -338,22 +348,31 @@ kv8_attn_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
         }
         tc_fence_after();
         const float4* sc = ctl.sc[it & 3];
-        const bool masked = __any_sync(0xffffffffu, key0 < rlo || key0 + kTileE > rhi);
+        if (__any_sync(0xffffffffu, key0 < rlo || key0 + kTileE > rhi)) {
+#pragma unroll 1
+          for (int i = 0; i < kTileE; i += 32) {  // (rolled: the code of the roles shares a cache)
+            uint32_t x[32];
+            tmem_ld32(ts + i, x);
+            tmem_wait_ld32(x);
+            mask32(x, key0 + i, rlo, rhi);
+            tmem_st32(ts + i, x);
+          }
+          tmem_wait_st();
+        }
         uint32_t p[64];
-        float sum, top;
-        // the weights with the reference as it is; `top`: the largest exponent
-        auto weights = [&]() {
+        float sum;
+        while (true) {
+          // the weights with the reference as it is; `top`: the largest exponent
           const float base = (m_ref == -INFINITY ? 0.0f : m_ref) - kHeadroom;
+          float top = -INFINITY;
+          sum = 0.0f;
           uint32_t s[2][32];
           tmem_ld32(ts, s[0]);
-          sum = 0.0f;
-          top = -INFINITY;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             uint32_t* x = s[i & 1];
             tmem_wait_ld32(x);
             if (i < 3) tmem_ld32(ts + 32 * (i + 1), s[(i + 1) & 1]);
-            if (masked) mask32(x, key0 + 32 * i, rlo, rhi);
 #pragma unroll
             for (int gi = 0; gi < 2; ++gi) {
               const float4 b = sc[2 * i + gi];
@@ -372,13 +391,11 @@ kv8_attn_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
               sum = fmaf(both.lo + both.hi, b.z, sum);
             }
           }
-        };
-        weights();
-        // a row whose first visible key this is, or whose reference is passed
-        bool again = __any_sync(0xffffffffu, (m_ref == -INFINITY && top > -INFINITY) ||
-                                                 top > kHeadroom + kLazy);
-        if (again) {
-          const float x = top + ((m_ref == -INFINITY ? 0.0f : m_ref) - kHeadroom);  // the largest logit
+          // again where this is a row's first visible key, or its reference is passed
+          if (!__any_sync(0xffffffffu, (m_ref == -INFINITY && top > -INFINITY) ||
+                                           top > kHeadroom + kLazy))
+            break;
+          const float x = top + base;  // the largest logit
           float alpha = 1.0f;
           if (x > m_ref + kLazy || m_ref == -INFINITY) {
             alpha = x == -INFINITY ? 1.0f : ex2(m_ref - x);
@@ -397,7 +414,6 @@ kv8_attn_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
               tmem_st16(to + i, o);
             }
           }
-          weights();
         }
         l += sum;
         tmem_st32(ts, p);
@@ -567,71 +583,71 @@ kv8_attn_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
     if (ks_out > 0) warp_wait(&ctl.rk_full, (ks_out - 1) & 1u, status);
     if (vs_out > 0) warp_wait(&ctl.rv_full, (vs_out - 1) & 1u, status);
   }
-  if (warp == kMmaWarp && lane == 0) {
+  if (warp == kMmaWarp) {
     // ================= MMA issuer =================
     const uint32_t id_s = idesc_f16(kTileE, false);
     const uint32_t id_o = idesc_f16(D, false) | (1u << 16);  // B (V) MN-major
-    const uint32_t sb = su32(smem);
+    const uint32_t sb = __shfl_sync(0xffffffffu, su32(smem), 0);
+    const uint32_t ms = __shfl_sync(0xffffffffu, tm_s, 0), mo = ms + 256;
     const uint32_t dq = (uint32_t)sw128_desc(sb + L::q, 16, 1024);
     const uint32_t dk = (uint32_t)sw128_desc(sb + L::k, 16, 1024);
     const uint32_t dv = (uint32_t)sw128_desc(sb + L::v, kAtom, 1024);
     const uint32_t hi = (uint32_t)(sw128_desc(0, 16, 1024) >> 32);
+    const uint32_t leader = lane == 0;
     uint32_t cnt = 0, units = 0;  // bit t: parity of row tile t's softmax tiles, of its units
     auto mma_s = [&](int t, uint32_t i) {
       const uint32_t qa = dq + t * (L::tile >> 4), kb = dk + (i & 1u) * (L::tile >> 4);
 #pragma unroll
       for (int x = 0; x < D / 16; ++x) {  // 16 channels: 32 bytes of atom x / 4
         const uint32_t off = ((x >> 2) * kAtom + (x & 3) * 32) >> 4;
-        mma_ss(tm_s + t * 128, qa + off, kb + off, hi, id_s, x != 0);
+        mma_ss(leader, ms + t * 128, qa + off, kb + off, hi, id_s, x != 0);
       }
-      mma_commit(su32(&ctl.s_full[t]));
+      commit_if(leader, &ctl.s_full[t]);
     };
     auto mma_o = [&](int t, uint32_t i, bool first) {
       const uint32_t vb = dv + (i & 1u) * (L::tile >> 4);
 #pragma unroll
       for (int x = 0; x < kTileE / 16; ++x)  // 16 keys: 8 columns of P, 2048 bytes of V
-        mma_ts(tm_o + t * D, tm_s + t * 128 + 8 * x, vb + x * (2048 >> 4), hi, id_o,
+        mma_ts(leader, mo + t * D, ms + t * 128 + 8 * x, vb + x * (2048 >> 4), hi, id_o,
                x != 0 || !first);
     };
     do {
-      const int nt = w.rows(a.G) > 128 ? 2 : 1;
-      const uint32_t i0 = it;
+      const int nt = __shfl_sync(0xffffffffu, w.rows(a.G) > 128 ? 2 : 1, 0);
+      const int n = __shfl_sync(0xffffffffu, w.t1 - w.t0, 0);
+      // S_t(0) of the unit, then for each tile j of keys O_t(j) and S_t(j + 1)
 #pragma unroll 1
-      for (int t = 0; t < nt && alive; ++t) {
-        alive = mbar_wait(su32(&ctl.q_full[t]), (units >> t) & 1u, status);
-        units ^= 1u << t;
-      }
-      if (!alive || !(alive = mbar_wait(su32(&ctl.k_full[it & 1u]), (it >> 1) & 1u, status))) break;
-      tc_fence_after();
+      for (int j = -1; j < n && alive; ++j) {
+        const uint32_t o = it + j, s2 = o + 1;  // tiles of the CTA: of O, of S
+        if (j >= 0) alive = warp_wait(&ctl.v_full[o & 1u], (o >> 1) & 1u, status);
+        if (alive && j + 1 < n) alive = warp_wait(&ctl.k_full[s2 & 1u], (s2 >> 1) & 1u, status);
 #pragma unroll 1
-      for (int t = 0; t < nt; ++t) mma_s(t, it);
-      mma_commit(su32(&ctl.k_empty[it & 1u]));
-      for (int j = w.t0; j < w.t1; ++j, ++it) {
-        const bool more = j + 1 < w.t1;
-        if (!(alive = mbar_wait(su32(&ctl.v_full[it & 1u]), (it >> 1) & 1u, status))) break;
-#pragma unroll 1
-        for (int t = 0; t < nt; ++t) {
-          if (!(alive = mbar_wait(su32(&ctl.p_full[t]), (cnt >> t) & 1u, status))) break;
-          cnt ^= 1u << t;
+        for (int t = 0; t < nt && alive; ++t) {
+          // P_t(j) is written and O_t rescaled; before the first tile: Q_t is written
+          if (j >= 0) {
+            alive = warp_wait(&ctl.p_full[t], (cnt >> t) & 1u, status);
+            cnt ^= 1u << t;
+          } else {
+            alive = warp_wait(&ctl.q_full[t], (units >> t) & 1u, status);
+            units ^= 1u << t;
+          }
+          if (!alive) break;
           tc_fence_after();
-          mma_o(t, it, it == i0);
-          if (t == nt - 1) mma_commit(su32(&ctl.v_empty[it & 1u]));
-          if (!more) mma_commit(su32(&ctl.o_full[t]));
-          if (more) {
-            if (t == 0 && !(alive = mbar_wait(su32(&ctl.k_full[(it + 1) & 1u]),
-                                              ((it + 1) >> 1) & 1u, status)))
-              break;
-            tc_fence_after();
-            mma_s(t, it + 1);
-            if (t == nt - 1) mma_commit(su32(&ctl.k_empty[(it + 1) & 1u]));
+          if (j >= 0) {
+            mma_o(t, o, j == 0);
+            if (t == nt - 1) commit_if(leader, &ctl.v_empty[o & 1u]);
+            if (j + 1 == n) commit_if(leader, &ctl.o_full[t]);
+          }
+          if (j + 1 < n) {
+            mma_s(t, s2);
+            if (t == nt - 1) commit_if(leader, &ctl.k_empty[s2 & 1u]);
           }
         }
-        if (!alive) break;
       }
-    } while (alive && w.next(a));
+      it += n;
+    } while (alive && warp_next(w, a));
     // nothing is in flight when tensor memory is freed
-    mma_commit(su32(&ctl.done));
-    mbar_wait(su32(&ctl.done), 0u, status);
+    commit_if(leader, &ctl.done);
+    warp_wait(&ctl.done, 0u, status);
   }
   __syncwarp();
   tc_fence_before();
