@@ -110,33 +110,23 @@ __device__ __forceinline__ void warp_arrive(uint64_t* bar) {
   if ((threadIdx.x & 31) == 0) mbar_arrive(su32(bar));
 }
 
-// MMAs whose shared-memory descriptors are given by their low words (address and
-// leading offset); the high words are the same for all of a kind.  A from shared
-// memory, and A from tensor memory.  Every lane of the warp comes here with the
-// same operands (they stay in uniform registers), the leader issues.
-__device__ __forceinline__ void mma_ss(uint32_t leader, uint32_t d, uint32_t a_lo, uint32_t b_lo,
-                                       uint32_t hi, uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t.reg .b64 x, y;\n\tsetp.ne.b32 p, %5, 0;\n\tsetp.ne.b32 q, %6, 0;\n\t"
-      "mov.b64 x, {%1, %3};\n\tmov.b64 y, {%2, %3};\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, p;\n\t}" ::"r"(d),
-      "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"(accumulate), "r"(leader));
+// One lane of the warp.  The tensor-core instructions stand in a branch on it: the
+// compiler then keeps their operands in uniform registers.  Measured for eight
+// MMAs of 128 x 128 x 16 in a row: 283 cycles to issue them so, 566 behind
+// `lane == 0`, 725 as a loop with the instruction predicated.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred P;\n\telect.sync _|P, 0xffffffff;\n\tselp.u32 %0, 1, 0, P;\n\t}"
+               : "=r"(p));
+  return p != 0;
 }
-__device__ __forceinline__ void mma_ts(uint32_t leader, uint32_t d, uint32_t a, uint32_t b_lo,
-                                       uint32_t hi, uint32_t idesc, uint32_t accumulate) {
+// MMA with A from tensor memory.
+__device__ __forceinline__ void mma_f16_ta(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                           uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\t.reg .b64 y;\n\tsetp.ne.b32 p, %5, 0;\n\tsetp.ne.b32 q, %6, 0;\n\t"
-      "mov.b64 y, {%2, %3};\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %4, p;\n\t}" ::"r"(d),
-      "r"(a), "r"(b_lo), "r"(hi), "r"(idesc), "r"(accumulate), "r"(leader));
-}
-__device__ __forceinline__ void commit_if(uint32_t leader, uint64_t* bar) {
-  asm volatile(
-      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
-      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
-          su32(bar)),
-      "r"(leader)
-      : "memory");
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate));
 }
 
 #define CSA2_R8(x, i) "=r"(x[i]), "=r"(x[i + 1]), "=r"(x[i + 2]), "=r"(x[i + 3]), \
@@ -299,15 +289,13 @@ kv8_attn_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
         const uint4* src = reinterpret_cast<const uint4*>(
             static_cast<const uint16_t*>(a.q) + (int64_t)(w.d.row0 + tok) * a.q_stride +
             (int64_t)head * D);
-        uint4 x[D / 8];
-#pragma unroll
-        for (int i = 0; i < D / 8; ++i) x[i] = ok ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
         float down = 1.0f;
         if (kBf16) {
           float mx = 0.0f;
-#pragma unroll
+#pragma unroll 4
           for (int i = 0; i < D / 8; ++i) {
-            const uint32_t y[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+            const uint4 x = ok ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+            const uint32_t y[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               const float2 f = pair_to_float2<true>(y[j]);
@@ -318,9 +306,10 @@ kv8_attn_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
           down = pow2f(-E);
           crow *= pow2f(E);
         }
-#pragma unroll
+#pragma unroll 2
         for (int i = 0; i < D / 8; ++i) {
-          uint32_t y[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+          const uint4 x = ok ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+          uint32_t y[4] = {x.x, x.y, x.z, x.w};
           if (kBf16) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -359,65 +348,81 @@ kv8_attn_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
           }
           tmem_wait_st();
         }
-        uint32_t p[64];
-        float sum;
-        while (true) {
-          // the weights with the reference as it is; `top`: the largest exponent
-          const float base = (m_ref == -INFINITY ? 0.0f : m_ref) - kHeadroom;
-          float top = -INFINITY;
-          sum = 0.0f;
-          uint32_t s[2][32];
-          tmem_ld32(ts, s[0]);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint32_t* x = s[i & 1];
-            tmem_wait_ld32(x);
-            if (i < 3) tmem_ld32(ts + 32 * (i + 1), s[(i + 1) & 1]);
-#pragma unroll
-            for (int gi = 0; gi < 2; ++gi) {
-              const float4 b = sc[2 * i + gi];
-              const float c = fmaxf(crow * b.x, 1.17549435e-38f), d = b.y - base;
-              F2 part[2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};
-#pragma unroll
-              for (int k = 0; k < 16; k += 2) {
-                const F2 y = fma2({__uint_as_float(x[16 * gi + k]), __uint_as_float(x[16 * gi + k + 1])},
-                                  {c, c}, {d, d});
-                top = fmaxf(top, fmaxf(y.lo, y.hi));
-                const F2 w2 = {ex2(y.lo), ex2(y.hi)};
-                part[(k >> 1) & 1] = add2(part[(k >> 1) & 1], w2);
-                p[16 * i + 8 * gi + k / 2] = pack_f16(w2.lo, w2.hi);
-              }
-              const F2 both = add2(part[0], part[1]);
-              sum = fmaf(both.lo + both.hi, b.z, sum);
-            }
-          }
-          // again where this is a row's first visible key, or its reference is passed
-          if (!__any_sync(0xffffffffu, (m_ref == -INFINITY && top > -INFINITY) ||
-                                           top > kHeadroom + kLazy))
-            break;
-          const float x = top + base;  // the largest logit
-          float alpha = 1.0f;
-          if (x > m_ref + kLazy || m_ref == -INFINITY) {
-            alpha = x == -INFINITY ? 1.0f : ex2(m_ref - x);
-            m_ref = x;
-          }
-          l *= alpha;
-          // S_t(j) is done, so O_t(j - 1), issued before it, is too
-          if (j > t0) {
+        // two halves of 64 keys (a loop: the code of all roles shares the SM's
+        // instruction cache, and unrolled it misses)
 #pragma unroll 1
-            for (int i = 0; i < D; i += 16) {
-              float o[16];
-              tmem_ld16(to + i, o);
-              tmem_wait_ld();
+        for (int half = 0; half < 2; ++half) {
+          uint32_t p[32];
+          float sum;
+          while (true) {
+            // the weights with the reference as it is; `top`: the largest exponent
+            const float base = (m_ref == -INFINITY ? 0.0f : m_ref) - kHeadroom;
+            float top = -INFINITY;
+            sum = 0.0f;
+            uint32_t s[2][32];
+            tmem_ld32(ts + 64 * half, s[0]);
 #pragma unroll
-              for (int k = 0; k < 16; ++k) o[k] *= alpha;
-              tmem_st16(to + i, o);
+            for (int i = 0; i < 2; ++i) {
+              uint32_t* x = s[i];
+              tmem_wait_ld32(x);
+              if (i == 0) tmem_ld32(ts + 64 * half + 32, s[1]);
+#pragma unroll
+              for (int gi = 0; gi < 2; ++gi) {
+                const float4 b = sc[4 * half + 2 * i + gi];
+                const float c = fmaxf(crow * b.x, 1.17549435e-38f), d = b.y - base;
+                F2 part[2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};
+#pragma unroll
+                for (int k = 0; k < 16; k += 2) {
+                  const F2 y = fma2(
+                      {__uint_as_float(x[16 * gi + k]), __uint_as_float(x[16 * gi + k + 1])}, {c, c},
+                      {d, d});
+                  top = fmaxf(top, fmaxf(y.lo, y.hi));
+                  const F2 w2 = {ex2(y.lo), ex2(y.hi)};
+                  part[(k >> 1) & 1] = add2(part[(k >> 1) & 1], w2);
+                  p[16 * i + 8 * gi + k / 2] = pack_f16(w2.lo, w2.hi);
+                }
+                const F2 both = add2(part[0], part[1]);
+                sum = fmaf(both.lo + both.hi, b.z, sum);
+              }
+            }
+            // again where this is a row's first visible key, or its reference is passed
+            if (!__any_sync(0xffffffffu, (m_ref == -INFINITY && top > -INFINITY) ||
+                                             top > kHeadroom + kLazy))
+              break;
+            const float x = top + base;  // the largest logit
+            float alpha = 1.0f;
+            if (x > m_ref + kLazy || m_ref == -INFINITY) {
+              alpha = x == -INFINITY ? 1.0f : ex2(m_ref - x);
+              m_ref = x;
+            }
+            l *= alpha;
+            // S_t(j) is done, so O_t(j - 1), issued before it, is too
+            if (j > t0) {
+#pragma unroll 1
+              for (int i = 0; i < D; i += 16) {
+                float o[16];
+                tmem_ld16(to + i, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int k = 0; k < 16; ++k) o[k] *= alpha;
+                tmem_st16(to + i, o);
+              }
+            }
+            if (half == 1) {  // the first half's weights had the old reference
+              const __half2 a2 = __float2half2_rn(alpha);
+              tmem_ld32(ts, s[0]);
+              tmem_wait_ld32(s[0]);
+#pragma unroll
+              for (int k = 0; k < 32; ++k) {
+                const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&s[0][k]), a2);
+                s[0][k] = *reinterpret_cast<const uint32_t*>(&y);
+              }
+              tmem_st32(ts, s[0]);
             }
           }
+          l += sum;
+          tmem_st32(ts + 32 * half, p);
         }
-        l += sum;
-        tmem_st32(ts, p);
-        tmem_st32(ts + 32, p + 32);
         tmem_wait_st();
         warp_arrive(&ctl.p_full[t]);
       }
@@ -482,7 +487,16 @@ kv8_attn_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
       for (int j = w.t0; j < t1; ++j, ++it) {
         const uint32_t st = it & 1u, par = ((it >> 1) & 1u) ^ 1u;
         const int key0 = (g0 + j) * kTileE;
-        auto convert = [&](const uint8_t* raw, uint8_t* to, bool clean) {
+#pragma unroll 1
+        for (int kv = 0; kv < 2 && alive; ++kv) {  // K, V
+          uint64_t* bars = kv ? &ctl.rv_full : &ctl.rk_full;  // full, empty
+          uint64_t* full = kv ? ctl.v_full : ctl.k_full;
+          uint64_t* empty = kv ? ctl.v_empty : ctl.k_empty;
+          alive = warp_wait(bars, it & 1u, status) && warp_wait(empty + st, par, status);
+          if (!alive) break;
+          const bool clean = ctl.clean[it & 3] != 0;
+          const uint8_t* raw = smem + L::rk + kv * L::raw;
+          uint8_t* to = smem + L::k + (2 * kv + st) * L::tile;
 #pragma unroll 4
           for (int i = 0; i < 32 / kKeys; ++i) {
             const int e = 32 * dw + kKeys * i + sub;
@@ -491,24 +505,10 @@ kv8_attn_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
               x = make_uint4(0, 0, 0, 0);
             put16(to + (c >> 2) * kAtom, e, c & 3, x, swap);
           }
-        };
-        if (!warp_wait(&ctl.rk_full, it & 1u, status) ||
-            !warp_wait(&ctl.k_empty[st], par, status)) {
-          alive = false;
-          break;
+          warp_arrive(full + st);
+          if (lane == 0) mbar_arrive(su32(bars + 1));
         }
-        const bool clean = ctl.clean[it & 3] != 0;
-        convert(smem + L::rk, smem + L::k + st * L::tile, clean);
-        warp_arrive(&ctl.k_full[st]);
-        if (lane == 0) mbar_arrive(su32(&ctl.rk_empty));
-        if (!warp_wait(&ctl.rv_full, it & 1u, status) ||
-            !warp_wait(&ctl.v_empty[st], par, status)) {
-          alive = false;
-          break;
-        }
-        convert(smem + L::rv, smem + L::v + st * L::tile, clean);
-        warp_arrive(&ctl.v_full[st]);
-        if (lane == 0) mbar_arrive(su32(&ctl.rv_empty));
+        if (!alive) break;
       }
     } while (alive && warp_next(w, a));
   } else {
@@ -587,29 +587,27 @@ kv8_attn_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
     // ================= MMA issuer =================
     const uint32_t id_s = idesc_f16(kTileE, false);
     const uint32_t id_o = idesc_f16(D, false) | (1u << 16);  // B (V) MN-major
-    const uint32_t sb = __shfl_sync(0xffffffffu, su32(smem), 0);
-    const uint32_t ms = __shfl_sync(0xffffffffu, tm_s, 0), mo = ms + 256;
-    const uint32_t dq = (uint32_t)sw128_desc(sb + L::q, 16, 1024);
-    const uint32_t dk = (uint32_t)sw128_desc(sb + L::k, 16, 1024);
-    const uint32_t dv = (uint32_t)sw128_desc(sb + L::v, kAtom, 1024);
-    const uint32_t hi = (uint32_t)(sw128_desc(0, 16, 1024) >> 32);
-    const uint32_t leader = lane == 0;
+    const uint32_t sb = su32(smem);
+    const uint64_t dq = sw128_desc(sb + L::q, 16, 1024);
+    const uint64_t dk = sw128_desc(sb + L::k, 16, 1024);
+    const uint64_t dv = sw128_desc(sb + L::v, kAtom, 1024);
     uint32_t cnt = 0, units = 0;  // bit t: parity of row tile t's softmax tiles, of its units
     auto mma_s = [&](int t, uint32_t i) {
-      const uint32_t qa = dq + t * (L::tile >> 4), kb = dk + (i & 1u) * (L::tile >> 4);
+      const uint64_t qa = dq + t * (L::tile >> 4), kb = dk + (i & 1u) * (L::tile >> 4);
+      const uint32_t d = tm_s + t * 128;
 #pragma unroll
       for (int x = 0; x < D / 16; ++x) {  // 16 channels: 32 bytes of atom x / 4
         const uint32_t off = ((x >> 2) * kAtom + (x & 3) * 32) >> 4;
-        mma_ss(leader, ms + t * 128, qa + off, kb + off, hi, id_s, x != 0);
+        mma_f16(d, qa + off, kb + off, id_s, x != 0);
       }
-      commit_if(leader, &ctl.s_full[t]);
+      mma_commit(su32(&ctl.s_full[t]));
     };
     auto mma_o = [&](int t, uint32_t i, bool first) {
-      const uint32_t vb = dv + (i & 1u) * (L::tile >> 4);
+      const uint64_t vb = dv + (i & 1u) * (L::tile >> 4);
+      const uint32_t d = tm_o + t * D, p = tm_s + t * 128;
 #pragma unroll
       for (int x = 0; x < kTileE / 16; ++x)  // 16 keys: 8 columns of P, 2048 bytes of V
-        mma_ts(leader, mo + t * D, ms + t * 128 + 8 * x, vb + x * (2048 >> 4), hi, id_o,
-               x != 0 || !first);
+        mma_f16_ta(d, p + 8 * x, vb + x * (2048 >> 4), id_o, x != 0 || !first);
     };
     do {
       const int nt = __shfl_sync(0xffffffffu, w.rows(a.G) > 128 ? 2 : 1, 0);
@@ -632,21 +630,25 @@ kv8_attn_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
           }
           if (!alive) break;
           tc_fence_after();
-          if (j >= 0) {
-            mma_o(t, o, j == 0);
-            if (t == nt - 1) commit_if(leader, &ctl.v_empty[o & 1u]);
-            if (j + 1 == n) commit_if(leader, &ctl.o_full[t]);
+          if (elect_one()) {
+            if (j >= 0) {
+              mma_o(t, o, j == 0);
+              if (t == nt - 1) mma_commit(su32(&ctl.v_empty[o & 1u]));
+              if (j + 1 == n) mma_commit(su32(&ctl.o_full[t]));
+            }
+            if (j + 1 < n) {
+              mma_s(t, s2);
+              if (t == nt - 1) mma_commit(su32(&ctl.k_empty[s2 & 1u]));
+            }
           }
-          if (j + 1 < n) {
-            mma_s(t, s2);
-            if (t == nt - 1) commit_if(leader, &ctl.k_empty[s2 & 1u]);
-          }
+          __syncwarp();
         }
       }
       it += n;
     } while (alive && warp_next(w, a));
     // nothing is in flight when tensor memory is freed
-    commit_if(leader, &ctl.done);
+    if (elect_one()) mma_commit(su32(&ctl.done));
+    __syncwarp();
     warp_wait(&ctl.done, 0u, status);
   }
   __syncwarp();
