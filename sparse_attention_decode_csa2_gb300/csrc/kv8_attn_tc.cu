@@ -15,19 +15,22 @@
 // Warp roles (512 threads):
 //   warps 0-3, 4-7  softmax of row tile 0, 1: a thread owns a row (a tensor-memory
 //                   lane), so row maxima and sums need no exchange.  The reference
-//                   maximum is lazy: it moves, and O is rescaled, only when a logit
-//                   passes it by more than 2^8 (weights stay below 2^15).  So the
-//                   weights are formed in one pass with the old reference, and only
-//                   a tile that passes it is looked through and formed again
+//                   maximum is lazy: weights are formed in one pass with the old
+//                   reference, which gives the key at the reference a weight of 2^7;
+//                   only where they grow past fp16's range (seen from their sums)
+//                   does it move, O is rescaled and the weights are formed again
 //   warps 8-11      dequantisers: E4M3 codes to fp16, 128-byte swizzled, double
 //                   buffered; keys that no row of the unit may see, and those of
 //                   pages outside the cache, become zeros
-//   warp 12         tensor memory; lane 0 issues every MMA
+//   warps 12, 14    issue the MMAs of row tile 0, 1 (12: tensor memory too).  An
+//                   issuing warp is held until the tensor pipe has room, so that one
+//                   warp would come late to every barrier: the second issuer took
+//                   a chunk of 4096 rows over 16K tokens (32 heads over 8, D = 128) from 825 to 787 us
 //   warp 13         loader: the block table and scales, and the codes of a tile's
 //                   pages into shared memory by bulk copies (through L2, where the
 //                   units of a sequence share them); a tile's K is requested while
 //                   its predecessor's V is converted and the reverse
-//   (warps 14, 15 only complete their warpgroup, for the register split)
+//   (warp 15 only completes its warpgroup, for the register split)
 // Measured before the loader had a warp of its own (the dequantisers looked up
 // pages and scales and loaded to registers): 6600 cycles a pair of tiles against
 // the 2048 of its MMAs, 3000 of them in those dependent loads.
@@ -42,7 +45,8 @@ namespace {
 using namespace kv8;
 using namespace tc;
 
-constexpr int kSoftWarps = 8, kDeqWarp0 = 8, kDeqWarps = 4, kMmaWarp = 12, kLoadWarp = 13;
+constexpr int kSoftWarps = 8, kDeqWarp0 = 8, kDeqWarps = 4, kMmaWarp = 12, kLoadWarp = 13,
+              kMmaWarp1 = 14;
 constexpr int kWarps = 16, kThreads = kWarps * 32;
 // Registers a thread after the roles part (four warpgroups, 512 in all: the 128
 // a thread of the launch): a softmax thread holds a row of P and a part of S.
@@ -50,7 +54,9 @@ constexpr int kSoftRegs = 184, kDeqRegs = 80, kMmaRegs = 64;
 static_assert(2 * kSoftRegs + kDeqRegs + kMmaRegs <= 512, "register split");
 constexpr int kUnit = 256;      // query rows of a unit
 constexpr int kTileE = 128;     // keys of a tile (and rows of a row tile)
-constexpr float kHeadroom = 7.0f, kLazy = 8.0f;  // log2: weights stay below 2^(7 + 8)
+// log2 of the weight at the reference, and the largest sum of 16 weights: no
+// weight is above it, which fp16 holds (65504)
+constexpr float kHeadroom = 7.0f, kMostSum = 57344.0f;
 constexpr uint32_t kAtom = 128 * 128;            // bytes: 128 rows of 64 fp16 channels
 
 template <int D>
@@ -73,7 +79,7 @@ struct Ctl {
   uint64_t q_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_full[2];
   uint64_t done;
   RangeSmem<kWarps> range;
-  Walk<kUnit, kTileE> walk[kLoadWarp + 1];  // each warp's own (kept out of registers)
+  Walk<kUnit, kTileE> walk[kMmaWarp1 + 1];  // each warp's own (kept out of registers)
   uint32_t tmem;
 };
 static_assert(sizeof(Ctl) <= 2048, "control block");
@@ -199,22 +205,23 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
       : "memory");
 }
 
+// 4 E4M3 codes -> fp16.
+__device__ __forceinline__ uint2 e4m3x4_to_f16x4(uint32_t x) {
+  uint2 r;
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(r.x), "=r"(r.y)
+      : "r"(x));
+  return r;
+}
+
 // 16 E4M3 codes -> fp16, into 16-byte chunks 2 c4, 2 c4 + 1 of key e of an atom.
-// swap: the second chunk first (the lanes of a warp that write another atom of the
-// same keys then meet other banks).
-__device__ __forceinline__ void put16(uint8_t* atom, int e, int c4, uint4 w, bool swap) {
-  const uint32_t x[4] = {swap ? w.z : w.x, swap ? w.w : w.y, swap ? w.x : w.z, swap ? w.y : w.w};
-  uint32_t o[8];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    o[2 * i] = e4m3x2_to_f16x2((uint16_t)(x[i] & 0xFFFFu));
-    o[2 * i + 1] = e4m3x2_to_f16x2((uint16_t)(x[i] >> 16));
-  }
+__device__ __forceinline__ void put16(uint8_t* atom, int e, int c4, uint4 w) {
   uint8_t* row = atom + (e >> 3) * 1024 + (e & 7) * 128;
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-    *reinterpret_cast<uint4*>(row + (((2 * c4 + (i ^ (int)swap)) ^ (e & 7)) << 4)) =
-        make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+  const uint2 a = e4m3x4_to_f16x4(w.x), b = e4m3x4_to_f16x4(w.y);
+  const uint2 c = e4m3x4_to_f16x4(w.z), d = e4m3x4_to_f16x4(w.w);
+  *reinterpret_cast<uint4*>(row + (((2 * c4) ^ (e & 7)) << 4)) = make_uint4(a.x, a.y, b.x, b.y);
+  *reinterpret_cast<uint4*>(row + (((2 * c4 + 1) ^ (e & 7)) << 4)) = make_uint4(c.x, c.y, d.x, d.y);
 }
 
 template <int D, bool kBf16>
@@ -244,20 +251,20 @@ kv8_attn_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
       mbar_init(su32(&ctl.p_full[i]), 4);
       mbar_init(su32(&ctl.k_full[i]), kDeqWarps);
       mbar_init(su32(&ctl.v_full[i]), kDeqWarps);
-      mbar_init(su32(&ctl.k_empty[i]), 1);
-      mbar_init(su32(&ctl.v_empty[i]), 1);
+      mbar_init(su32(&ctl.k_empty[i]), 2);
+      mbar_init(su32(&ctl.v_empty[i]), 2);
       mbar_init(su32(&ctl.s_full[i]), 1);
       mbar_init(su32(&ctl.o_full[i]), 1);
     }
-    mbar_init(su32(&ctl.done), 1);
+    mbar_init(su32(&ctl.done), 2);
     mbar_init(su32(&ctl.rk_full), 1);
     mbar_init(su32(&ctl.rv_full), 1);
     mbar_init(su32(&ctl.rk_empty), kDeqWarps);
     mbar_init(su32(&ctl.rv_empty), kDeqWarps);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  Walk<kUnit, kTileE>& w = ctl.walk[min(warp, kLoadWarp)];
-  if (warp <= kLoadWarp && lane == 0) w.start(a, rg);
+  Walk<kUnit, kTileE>& w = ctl.walk[min(warp, kMmaWarp1)];
+  if (warp <= kMmaWarp1 && lane == 0) w.start(a, rg);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -354,10 +361,55 @@ kv8_attn_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
         for (int half = 0; half < 2; ++half) {
           uint32_t p[32];
           float sum;
+          bool move = __any_sync(0xffffffffu, m_ref == -INFINITY);
           while (true) {
-            // the weights with the reference as it is; `top`: the largest exponent
+            if (move) {  // the reference moves to the half's largest logit where that is past it
+              float x = -INFINITY;
+#pragma unroll 1
+              for (int i = 0; i < 2; ++i) {
+                uint32_t y[32];
+                tmem_ld32(ts + 64 * half + 32 * i, y);
+                tmem_wait_ld32(y);
+#pragma unroll
+                for (int gi = 0; gi < 2; ++gi) {
+                  const float4 b = sc[4 * half + 2 * i + gi];
+                  float mx = __uint_as_float(y[16 * gi]);
+#pragma unroll
+                  for (int k = 1; k < 16; ++k) mx = fmaxf(mx, __uint_as_float(y[16 * gi + k]));
+                  x = fmaxf(x, fmaf(mx, fmaxf(crow * b.x, 1.17549435e-38f), b.y));
+                }
+              }
+              const float alpha = x > m_ref ? ex2(m_ref - x) : 1.0f;
+              m_ref = fmaxf(m_ref, x);
+              l *= alpha;
+              // S_t(j) is done, so O_t(j - 1), issued before it, is too
+              if (j > t0) {
+#pragma unroll 1
+                for (int i = 0; i < D; i += 16) {
+                  float o[16];
+                  tmem_ld16(to + i, o);
+                  tmem_wait_ld();
+#pragma unroll
+                  for (int k = 0; k < 16; ++k) o[k] *= alpha;
+                  tmem_st16(to + i, o);
+                }
+              }
+              if (half == 1) {  // the first half's weights had the old reference
+                const __half2 a2 = __float2half2_rn(alpha);
+                uint32_t y[32];
+                tmem_ld32(ts, y);
+                tmem_wait_ld32(y);
+#pragma unroll
+                for (int k = 0; k < 32; ++k) {
+                  const __half2 z = __hmul2(*reinterpret_cast<const __half2*>(&y[k]), a2);
+                  y[k] = *reinterpret_cast<const uint32_t*>(&z);
+                }
+                tmem_st32(ts, y);
+              }
+            }
+            // the weights with the reference as it is; `most`: the largest sum of a group
             const float base = (m_ref == -INFINITY ? 0.0f : m_ref) - kHeadroom;
-            float top = -INFINITY;
+            float most = 0.0f;
             sum = 0.0f;
             uint32_t s[2][32];
             tmem_ld32(ts + 64 * half, s[0]);
@@ -376,49 +428,20 @@ kv8_attn_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
                   const F2 y = fma2(
                       {__uint_as_float(x[16 * gi + k]), __uint_as_float(x[16 * gi + k + 1])}, {c, c},
                       {d, d});
-                  top = fmaxf(top, fmaxf(y.lo, y.hi));
                   const F2 w2 = {ex2(y.lo), ex2(y.hi)};
                   part[(k >> 1) & 1] = add2(part[(k >> 1) & 1], w2);
                   p[16 * i + 8 * gi + k / 2] = pack_f16(w2.lo, w2.hi);
                 }
                 const F2 both = add2(part[0], part[1]);
-                sum = fmaf(both.lo + both.hi, b.z, sum);
+                const float one = both.lo + both.hi;
+                most = fmaxf(most, one);
+                sum = fmaf(one, b.z, sum);
               }
             }
-            // again where this is a row's first visible key, or its reference is passed
-            if (!__any_sync(0xffffffffu, (m_ref == -INFINITY && top > -INFINITY) ||
-                                             top > kHeadroom + kLazy))
-              break;
-            const float x = top + base;  // the largest logit
-            float alpha = 1.0f;
-            if (x > m_ref + kLazy || m_ref == -INFINITY) {
-              alpha = x == -INFINITY ? 1.0f : ex2(m_ref - x);
-              m_ref = x;
-            }
-            l *= alpha;
-            // S_t(j) is done, so O_t(j - 1), issued before it, is too
-            if (j > t0) {
-#pragma unroll 1
-              for (int i = 0; i < D; i += 16) {
-                float o[16];
-                tmem_ld16(to + i, o);
-                tmem_wait_ld();
-#pragma unroll
-                for (int k = 0; k < 16; ++k) o[k] *= alpha;
-                tmem_st16(to + i, o);
-              }
-            }
-            if (half == 1) {  // the first half's weights had the old reference
-              const __half2 a2 = __float2half2_rn(alpha);
-              tmem_ld32(ts, s[0]);
-              tmem_wait_ld32(s[0]);
-#pragma unroll
-              for (int k = 0; k < 32; ++k) {
-                const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&s[0][k]), a2);
-                s[0][k] = *reinterpret_cast<const uint32_t*>(&y);
-              }
-              tmem_st32(ts, s[0]);
-            }
+            // a weight may leave fp16's range only in a group whose sum does: then the
+            // reference moves and the weights are formed again
+            if (!__any_sync(0xffffffffu, most > kMostSum)) break;
+            move = true;
           }
           l += sum;
           tmem_st32(ts + 32 * half, p);
@@ -477,11 +500,11 @@ kv8_attn_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
     // ================= dequantisers =================
     fewer_registers<kDeqRegs>();
     // a lane converts 16 channels (chunk c of the key's codes) of D / 16 lanes a
-    // key: it reads 16 contiguous bytes of a run, and writes two 16-byte chunks of
-    // atom c / 4
+    // key: it reads 16 bytes and writes two 16-byte chunks of atom c / 4.  The lanes
+    // of the second atom take the key beside (e ^ 1), so that the eight lanes of a
+    // phase meet the eight different 16-byte slots of the swizzle in both
     constexpr int kCh = D / 16, kKeys = 32 / kCh;  // lanes a key, keys an instruction
-    const int dw = warp - kDeqWarp0, c = lane % kCh, sub = lane / kCh;
-    const bool swap = c >= 4;
+    const int dw = warp - kDeqWarp0, c = lane % kCh, sub = (lane / kCh) ^ (c >> 2);
     do {
       const int t1 = w.t1, g0 = w.u.g0, lo = w.u.lo, hi = w.u.hi;
       for (int j = w.t0; j < t1; ++j, ++it) {
@@ -503,7 +526,7 @@ kv8_attn_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
             uint4 x = *reinterpret_cast<const uint4*>(raw + e * D + 16 * c);
             if (!clean && (key0 + e < lo || key0 + e >= hi || ctl.sc[it & 3][e >> 4].z == 0.0f))
               x = make_uint4(0, 0, 0, 0);
-            put16(to + (c >> 2) * kAtom, e, c & 3, x, swap);
+            put16(to + (c >> 2) * kAtom, e, c & 3, x);
           }
           warp_arrive(full + st);
           if (lane == 0) mbar_arrive(su32(bars + 1));
@@ -583,66 +606,64 @@ kv8_attn_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
     if (ks_out > 0) warp_wait(&ctl.rk_full, (ks_out - 1) & 1u, status);
     if (vs_out > 0) warp_wait(&ctl.rv_full, (vs_out - 1) & 1u, status);
   }
-  if (warp == kMmaWarp) {
-    // ================= MMA issuer =================
+  if (warp == kMmaWarp || warp == kMmaWarp1) {
+    // ================= MMA issuers =================
     const uint32_t id_s = idesc_f16(kTileE, false);
     const uint32_t id_o = idesc_f16(D, false) | (1u << 16);  // B (V) MN-major
-    const uint32_t sb = su32(smem);
-    const uint64_t dq = sw128_desc(sb + L::q, 16, 1024);
+    const int t = warp == kMmaWarp ? 0 : 1;                  // row tile
+    const uint32_t sb = su32(smem), ts = tm_s + t * 128, to = tm_o + t * D;
+    const uint64_t dq = sw128_desc(sb + L::q + t * L::tile, 16, 1024);
     const uint64_t dk = sw128_desc(sb + L::k, 16, 1024);
     const uint64_t dv = sw128_desc(sb + L::v, kAtom, 1024);
-    uint32_t cnt = 0, units = 0;  // bit t: parity of row tile t's softmax tiles, of its units
-    auto mma_s = [&](int t, uint32_t i) {
-      const uint64_t qa = dq + t * (L::tile >> 4), kb = dk + (i & 1u) * (L::tile >> 4);
-      const uint32_t d = tm_s + t * 128;
-#pragma unroll
-      for (int x = 0; x < D / 16; ++x) {  // 16 channels: 32 bytes of atom x / 4
-        const uint32_t off = ((x >> 2) * kAtom + (x & 3) * 32) >> 4;
-        mma_f16(d, qa + off, kb + off, id_s, x != 0);
-      }
-      mma_commit(su32(&ctl.s_full[t]));
-    };
-    auto mma_o = [&](int t, uint32_t i, bool first) {
-      const uint64_t vb = dv + (i & 1u) * (L::tile >> 4);
-      const uint32_t d = tm_o + t * D, p = tm_s + t * 128;
-#pragma unroll
-      for (int x = 0; x < kTileE / 16; ++x)  // 16 keys: 8 columns of P, 2048 bytes of V
-        mma_f16_ta(d, p + 8 * x, vb + x * (2048 >> 4), id_o, x != 0 || !first);
-    };
+    uint32_t cnt = 0, units = 0;
     do {
-      const int nt = __shfl_sync(0xffffffffu, w.rows(a.G) > 128 ? 2 : 1, 0);
-      const int n = __shfl_sync(0xffffffffu, w.t1 - w.t0, 0);
+      const int n = w.t1 - w.t0;
+      const bool mine = t == 0 || w.rows(a.G) > 128;  // else the unit has one row tile
+      if (mine) {
+        alive = warp_wait(&ctl.q_full[t], units & 1u, status);
+        ++units;
+      }
       // S_t(0) of the unit, then for each tile j of keys O_t(j) and S_t(j + 1)
 #pragma unroll 1
       for (int j = -1; j < n && alive; ++j) {
         const uint32_t o = it + j, s2 = o + 1;  // tiles of the CTA: of O, of S
         if (j >= 0) alive = warp_wait(&ctl.v_full[o & 1u], (o >> 1) & 1u, status);
         if (alive && j + 1 < n) alive = warp_wait(&ctl.k_full[s2 & 1u], (s2 >> 1) & 1u, status);
-#pragma unroll 1
-        for (int t = 0; t < nt && alive; ++t) {
-          // P_t(j) is written and O_t rescaled; before the first tile: Q_t is written
-          if (j >= 0) {
-            alive = warp_wait(&ctl.p_full[t], (cnt >> t) & 1u, status);
-            cnt ^= 1u << t;
-          } else {
-            alive = warp_wait(&ctl.q_full[t], (units >> t) & 1u, status);
-            units ^= 1u << t;
-          }
-          if (!alive) break;
-          tc_fence_after();
-          if (elect_one()) {
-            if (j >= 0) {
-              mma_o(t, o, j == 0);
-              if (t == nt - 1) mma_commit(su32(&ctl.v_empty[o & 1u]));
-              if (j + 1 == n) mma_commit(su32(&ctl.o_full[t]));
-            }
-            if (j + 1 < n) {
-              mma_s(t, s2);
-              if (t == nt - 1) mma_commit(su32(&ctl.k_empty[s2 & 1u]));
-            }
+        if (!mine) {  // only releases the tiles
+          if (alive && lane == 0) {
+            if (j >= 0) mbar_arrive(su32(&ctl.v_empty[o & 1u]));
+            if (j + 1 < n) mbar_arrive(su32(&ctl.k_empty[s2 & 1u]));
           }
           __syncwarp();
+          continue;
         }
+        if (alive && j >= 0) {  // P_t(j) is written and O_t rescaled
+          alive = warp_wait(&ctl.p_full[t], cnt & 1u, status);
+          ++cnt;
+        }
+        if (!alive) break;
+        tc_fence_after();
+        if (elect_one()) {
+          if (j >= 0) {
+            const uint64_t vb = dv + (o & 1u) * (L::tile >> 4);
+#pragma unroll
+            for (int x = 0; x < kTileE / 16; ++x)  // 16 keys: 8 columns of P, 2048 bytes of V
+              mma_f16_ta(to, ts + 8 * x, vb + x * (2048 >> 4), id_o, x != 0 || j != 0);
+            mma_commit(su32(&ctl.v_empty[o & 1u]));
+            if (j + 1 == n) mma_commit(su32(&ctl.o_full[t]));
+          }
+          if (j + 1 < n) {
+            const uint64_t kb = dk + (s2 & 1u) * (L::tile >> 4);
+#pragma unroll
+            for (int x = 0; x < D / 16; ++x) {  // 16 channels: 32 bytes of atom x / 4
+              const uint32_t off = ((x >> 2) * kAtom + (x & 3) * 32) >> 4;
+              mma_f16(ts, dq + off, kb + off, id_s, x != 0);
+            }
+            mma_commit(su32(&ctl.s_full[t]));
+            mma_commit(su32(&ctl.k_empty[s2 & 1u]));
+          }
+        }
+        __syncwarp();
       }
       it += n;
     } while (alive && warp_next(w, a));
