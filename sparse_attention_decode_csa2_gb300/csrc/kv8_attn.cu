@@ -51,6 +51,8 @@ struct Cfg {
   static constexpr int unit = 16 * kRg;                    // query rows
   static constexpr int kgs = kWarps / kRg;                 // key groups
   static constexpr int granule = kgs * kTileKeys;          // keys
+  // a unit's queries and output take about as long as 128 keys
+  using Work = Shape<unit, granule, kRg>;
   static constexpr int stages = (D == 128 ? 3 : 4) * kRg;
   static constexpr int tile = kTileKeys * D;               // bytes of K (or V) of a stage
   static constexpr int stage = 2 * tile;
@@ -125,7 +127,7 @@ kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a) {
   const int kg = warp / kRg, rq = warp % kRg;  // key group, row group
   pdl_trigger();
   if (blockIdx.x == 0) kv8_check_batch(a.c);
-  const Range rg = find_range<C::unit, C::granule, kWarps>(a, blockIdx.x, gridDim.x, rsm);
+  const Range rg = find_range<typename C::Work, kWarps>(a, blockIdx.x, gridDim.x, rsm);
   if (rg.s < 0) return;
 
   uint8_t* ring = smem + kg * (C::stages * C::stage);
@@ -135,8 +137,8 @@ kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a) {
   float* part =
       reinterpret_cast<float*>(a.scratch) + (size_t)blockIdx.x * 2 * part_floats(C::unit, D);
 
-  Walk<C::unit, C::granule> w;
-  w.start(a, rg);
+  Walk<typename C::Work> w;
+  if (!w.start(a, rg)) return;
   do {
     const int i0 = w.first_row(), nrow = w.rows(a.G);
 
@@ -463,7 +465,7 @@ template <int D, int kRg, bool kBf16>
 __global__ void __launch_bounds__(kThreads)
 kv8_merge_kernel(const __grid_constant__ Kv8AttnArgs a, int workers) {
   using C = Cfg<D, kRg>;
-  merge_parts<C::unit, C::granule, kWarps, D, kBf16>(a, workers, kHeadroom);
+  merge_parts<typename C::Work, kWarps, D, kBf16>(a, workers, kHeadroom);
 }
 
 template <int D>

@@ -57,6 +57,7 @@ constexpr int kTileE = 128;     // keys of a tile (and rows of a row tile)
 // log2 of the weight at the reference, and the largest sum of 16 weights: no
 // weight is above it, which fp16 holds (65504)
 constexpr float kHeadroom = 7.0f, kMostSum = 57344.0f;
+using Work = Shape<kUnit, kTileE, 2>;
 constexpr uint32_t kAtom = 128 * 128;            // bytes: 128 rows of 64 fp16 channels
 
 template <int D>
@@ -79,7 +80,7 @@ struct Ctl {
   uint64_t q_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_full[2];
   uint64_t done;
   RangeSmem<kWarps> range;
-  Walk<kUnit, kTileE> walk[kMmaWarp1 + 1];  // each warp's own (kept out of registers)
+  Walk<Work> walk[kMmaWarp1 + 1];  // each warp's own (kept out of registers)
   uint32_t tmem;
 };
 static_assert(sizeof(Ctl) <= 2048, "control block");
@@ -89,7 +90,7 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int32_
 }
 
 // The warp's walk to its next unit (one lane moves it).
-__device__ __forceinline__ bool warp_next(Walk<kUnit, kTileE>& w, const Kv8AttnArgs& a) {
+__device__ __forceinline__ bool warp_next(Walk<Work>& w, const Kv8AttnArgs& a) {
   __syncwarp();
   bool more = false;
   if ((threadIdx.x & 31) == 0) more = w.next(a);
@@ -236,9 +237,12 @@ kv8_attn_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
   int32_t* status = a.c.status;
   pdl_trigger();
   if (blockIdx.x == 0) kv8_check_batch(a.c);
-  const Range rg =
-      find_range<kUnit, kTileE, kWarps>(a, blockIdx.x, gridDim.x, ctl.range);
+  const Range rg = find_range<Work, kWarps>(a, blockIdx.x, gridDim.x, ctl.range);
   if (rg.s < 0) return;
+  Walk<Work>& w = ctl.walk[min(warp, kMmaWarp1)];
+  bool any = false;
+  if (warp <= kMmaWarp1 && lane == 0) any = w.start(a, rg);
+  if (!__syncthreads_or(any)) return;  // the range ends within a unit's fixed cost
 
   if (warp == kMmaWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
@@ -263,8 +267,6 @@ kv8_attn_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
     mbar_init(su32(&ctl.rv_empty), kDeqWarps);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  Walk<kUnit, kTileE>& w = ctl.walk[min(warp, kMmaWarp1)];
-  if (warp <= kMmaWarp1 && lane == 0) w.start(a, rg);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -282,60 +284,74 @@ kv8_attn_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
     uint8_t* qt = smem + L::q + t * L::tile;
     const int qr = row & 127;
     uint32_t cnt = 0, units = 0;
-    do {
-      const int i0 = w.first_row(), nrow = w.rows(a.G), t0 = w.t0, t1 = w.t1;
-      if (t == 1 && nrow <= 128) {
-        it += t1 - t0;
-        continue;
+    // the unit's row of this thread
+    bool ok;
+    int64_t orow;       // of out, lse
+    float crow;         // logit factor, without the block's K scale
+    int rlo, rhi;       // tokens it sees
+    // To the next unit that has row tile t (`first`: this one, if it has it).
+    auto advance = [&](bool first) -> bool {
+      while (true) {
+        if (!first && !warp_next(w, a)) return false;
+        first = false;
+        if (t == 0 || w.rows(a.G) > 128) return true;
+        it += w.t1 - w.t0;
       }
-      // ---- this thread's row of Q, scaled to a largest magnitude in [1, 2) ----
-      const bool ok = row < nrow;
+    };
+    // The row of Q, scaled to a largest magnitude in [1, 2), into shared memory.
+    auto load_q = [&]() {
+      const int i0 = w.first_row();
+      ok = row < w.rows(a.G);
       const int tok = i0 + (ok ? row : 0) / a.G, head = w.h * a.G + (ok ? row % a.G : 0);
-      float crow = a.scale_log2;
-      {
-        const uint4* src = reinterpret_cast<const uint4*>(
-            static_cast<const uint16_t*>(a.q) + (int64_t)(w.d.row0 + tok) * a.q_stride +
-            (int64_t)head * D);
-        float down = 1.0f;
-        if (kBf16) {
-          float mx = 0.0f;
-#pragma unroll 4
-          for (int i = 0; i < D / 8; ++i) {
-            const uint4 x = ok ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
-            const uint32_t y[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const float2 f = pair_to_float2<true>(y[j]);
-              mx = fmaxf(mx, fmaxf(fabsf(f.x), fabsf(f.y)));
-            }
-          }
-          const int E = row_exponent(mx);
-          down = pow2f(-E);
-          crow *= pow2f(E);
-        }
-#pragma unroll 2
+      orow = (int64_t)(w.d.row0 + tok) * a.H + head;
+      const uint4* src = reinterpret_cast<const uint4*>(
+          static_cast<const uint16_t*>(a.q) + (int64_t)(w.d.row0 + tok) * a.q_stride +
+          (int64_t)head * D);
+      float down = 1.0f;
+      crow = a.scale_log2;
+      if (kBf16) {
+        float mx = 0.0f;
+#pragma unroll 8
         for (int i = 0; i < D / 8; ++i) {
           const uint4 x = ok ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
-          uint32_t y[4] = {x.x, x.y, x.z, x.w};
-          if (kBf16) {
+          const uint32_t y[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const float2 f = pair_to_float2<true>(y[j]);
-              y[j] = pack_f16(f.x * down, f.y * down);
-            }
+          for (int j = 0; j < 4; ++j) {
+            const float2 f = pair_to_float2<true>(y[j]);
+            mx = fmaxf(mx, fmaxf(fabsf(f.x), fabsf(f.y)));
           }
-          *reinterpret_cast<uint4*>(qt + sw128_off(qr, 8 * i, kAtom)) =
-              make_uint4(y[0], y[1], y[2], y[3]);
         }
+        const int E = row_exponent(mx);
+        down = pow2f(-E);
+        crow *= pow2f(E);
+      }
+#pragma unroll 4
+      for (int i = 0; i < D / 8; ++i) {
+        const uint4 x = ok ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+        uint32_t y[4] = {x.x, x.y, x.z, x.w};
+        if (kBf16) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float2 f = pair_to_float2<true>(y[j]);
+            y[j] = pack_f16(f.x * down, f.y * down);
+          }
+        }
+        *reinterpret_cast<uint4*>(qt + sw128_off(qr, 8 * i, kAtom)) =
+            make_uint4(y[0], y[1], y[2], y[3]);
       }
       warp_arrive(&ctl.q_full[t]);
-      int rlo = w.u.lo, rhi = w.u.hi;
+      rlo = w.u.lo;
+      rhi = w.u.hi;
       if (a.causal && ok) {
         const int64_t p = (int64_t)w.d.len - w.d.n + tok;
         rhi = (int)max((int64_t)0, min((int64_t)w.u.hi, p + 1));
         if (a.window > 0) rlo = (int)max((int64_t)rlo, p - a.window + 1);
       }
-
+    };
+    bool have = advance(true);
+    if (have) load_q();
+    while (have) {
+      const int t0 = w.t0, t1 = w.t1;
       float m_ref = -INFINITY, l = 0.0f;
       for (int j = t0, key0 = (w.u.g0 + t0) * kTileE; j < t1; ++j, ++it, ++cnt, key0 += kTileE) {
         if (!warp_wait(&ctl.s_full[t], cnt & 1u, status)) {
@@ -449,16 +465,21 @@ kv8_attn_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
         tmem_wait_st();
         warp_arrive(&ctl.p_full[t]);
       }
-      if (!alive || !warp_wait(&ctl.o_full[t], units & 1u, status)) {
+      if (!alive) break;
+      // the next unit's Q (every S_t of this one is done): its first product runs
+      // while this unit's output is written
+      const bool whole = w.whole(), out_ok = ok;
+      const int64_t out_row = orow;
+      have = advance(false);
+      if (have) load_q();
+      if (!warp_wait(&ctl.o_full[t], units & 1u, status)) {
         alive = false;
         break;
       }
       ++units;
       tc_fence_after();
       // ---- output, or a part of it ----
-      const bool whole = w.whole();
       const float inv = !whole ? 1.0f : l == 0.0f ? 0.0f : 1.0f / l;  // no visible token: zeros
-      const int64_t orow = (int64_t)(w.d.row0 + tok) * a.H + head;
       float* part = reinterpret_cast<float*>(a.scratch) +
                     ((size_t)blockIdx.x * 2 + (t0 == 0 ? 1 : 0)) * part_floats(kUnit, D);
 #pragma unroll 1
@@ -466,9 +487,9 @@ kv8_attn_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
         uint32_t o[32];
         tmem_ld32(to + i, o);
         tmem_wait_ld();
-        if (!ok) continue;
+        if (!out_ok) continue;
         if (whole) {
-          uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + orow * D + i);
+          uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + out_row * D + i);
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             uint32_t y[4];
@@ -485,17 +506,17 @@ kv8_attn_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
             dst[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
         }
       }
-      if (ok) {
+      if (out_ok) {
         if (whole) {
           if (a.lse)
-            a.lse[orow] = l == 0.0f ? -INFINITY
+            a.lse[out_row] = l == 0.0f ? -INFINITY
                                     : ((m_ref == -INFINITY ? 0.0f : m_ref) - kHeadroom + __log2f(l)) * kLn2;
         } else {
           part[kUnit * D + row] = m_ref;
           part[kUnit * D + kUnit + row] = l;
         }
       }
-    } while (warp_next(w, a));
+    }
   } else if (warp < kMmaWarp) {
     // ================= dequantisers =================
     fewer_registers<kDeqRegs>();
@@ -683,7 +704,7 @@ kv8_attn_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
 template <int D, bool kBf16>
 __global__ void __launch_bounds__(128)
 kv8_merge_tc_kernel(const __grid_constant__ Kv8AttnArgs a, int workers) {
-  merge_parts<kUnit, kTileE, 4, D, kBf16>(a, workers, kHeadroom);
+  merge_parts<Work, 4, D, kBf16>(a, workers, kHeadroom);
 }
 
 template <int D, bool kBf16>

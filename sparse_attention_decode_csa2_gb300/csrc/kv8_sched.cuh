@@ -2,7 +2,9 @@
 // (sequence, block of up to kUnit query rows = tokens x G heads, KV head); its
 // keys are cut into granules.  The batch's granules, in the order (sequence,
 // block, head, key), are dealt to the grid's CTAs ("workers") as equal
-// contiguous ranges.  Everything is computed on the device from kv_len and cu:
+// contiguous ranges.  What a unit costs beside its keys (its queries, its output)
+// counts as kCost granules before its first: without them a worker with many
+// short units took twice the mean (prompts through a window of 1024).  Everything is computed on the device from kv_len and cu:
 // there is no host plan, nothing to keep up to date, no CTA for tokens that a
 // sequence does not have, and a captured graph follows the lengths.
 #pragma once
@@ -19,7 +21,14 @@ struct Dims {
   int tpu, nm;            // tokens of a block of rows, blocks
 };
 
-template <int kUnit>
+// What the kernels of one kind share: query rows of a unit, keys of a granule, a
+// unit's fixed cost in granules.
+template <int kUnit_, int kGranule_, int kCost_>
+struct Shape {
+  static constexpr int kUnit = kUnit_, kGranule = kGranule_, kCost = kCost_;
+};
+
+template <class Sh>
 __device__ __forceinline__ Dims seq_dims(const Kv8AttnArgs& a, int s) {
   const Kv8Seq q = kv8_seq(a.c, s);
   Dims d;
@@ -27,7 +36,7 @@ __device__ __forceinline__ Dims seq_dims(const Kv8AttnArgs& a, int s) {
   d.row0 = q.row0;
   d.len = q.len;
   d.cap = (int)min((int64_t)q.len, (int64_t)a.c.max_pages << a.c.page_shift);
-  d.tpu = kUnit / a.G;
+  d.tpu = Sh::kUnit / a.G;
   d.nm = (q.n + d.tpu - 1) / d.tpu;
   return d;
 }
@@ -37,7 +46,7 @@ struct Span {
   int lo, hi, g0, ng;
 };
 
-template <int kGranule>
+template <class Sh>
 __device__ __forceinline__ Span unit_span(const Kv8AttnArgs& a, const Dims& d, int m) {
   Span u;
   u.lo = 0;
@@ -49,23 +58,23 @@ __device__ __forceinline__ Span unit_span(const Kv8AttnArgs& a, const Dims& d, i
     if (a.window > 0) u.lo = (int)max((int64_t)0, p0 - a.window + 1);
   }
   if (u.lo > u.hi) u.lo = u.hi;
-  u.g0 = u.lo / kGranule;
-  u.ng = max(1, (u.hi + kGranule - 1) / kGranule - u.g0);  // one at least: it writes the rows
+  u.g0 = u.lo / Sh::kGranule;
+  u.ng = max(1, (u.hi + Sh::kGranule - 1) / Sh::kGranule - u.g0);  // one at least: it writes the rows
   return u;
 }
 
-// A worker's range [w0, w1) of the batch's granules and where it starts:
-// granule t0 of unit (s, m, h).  s < 0: no range.
+// A worker's range [w0, w1) of the batch's granules (fixed costs included) and
+// where it starts: place c0 of unit (s, m, h).  s < 0: no range.
 struct Range {
   int64_t w0, w1, total;
   int workers;  // workers that have a range (no more than there are granules)
-  int s, m, h, t0;
+  int s, m, h, c0;
 };
 
 template <int kWarps>
 struct RangeSmem {
   int64_t warp_sum[kWarps];
-  int s, m, h, t0;
+  int s, m, h, c0;
 };
 
 // Sums one value per lane of each warp; every lane gets the warp's total.
@@ -86,7 +95,7 @@ __device__ __forceinline__ int64_t warp_scan(int64_t x, int lane) {  // inclusiv
 // All threads of the block.  A warp takes a contiguous share of the sequences,
 // 32 at a time: a lane per sequence where the sequences have one block of rows,
 // else the lanes go over a sequence's blocks together.
-template <int kUnit, int kGranule, int kWarps>
+template <class Sh, int kWarps>
 __device__ Range find_range(const Kv8AttnArgs& a, int worker, int workers,
                             RangeSmem<kWarps>& sm) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -94,12 +103,12 @@ __device__ Range find_range(const Kv8AttnArgs& a, int worker, int workers,
   const int s0 = min(a.c.S, warp * per), s1 = min(a.c.S, s0 + per);
   // granules of the blocks of sequence s, every KV head
   auto lane_work = [&](const Dims& d) -> int64_t {  // a lane's sequence with one block (or none)
-    return d.nm == 1 ? (int64_t)unit_span<kGranule>(a, d, 0).ng * a.c.H_kv : 0;
+    return d.nm == 1 ? (int64_t)(unit_span<Sh>(a, d, 0).ng + Sh::kCost) * a.c.H_kv : 0;
   };
   auto warp_work = [&](const Dims& d) -> int64_t {  // the warp's sequence, any number of blocks
-    if (!a.causal) return (int64_t)d.nm * unit_span<kGranule>(a, d, 0).ng * a.c.H_kv;
+    if (!a.causal) return (int64_t)d.nm * (unit_span<Sh>(a, d, 0).ng + Sh::kCost) * a.c.H_kv;
     int64_t w = 0;
-    for (int m = lane; m < d.nm; m += 32) w += unit_span<kGranule>(a, d, m).ng;
+    for (int m = lane; m < d.nm; m += 32) w += unit_span<Sh>(a, d, m).ng + Sh::kCost;
     return warp_total(w) * a.c.H_kv;
   };
   // work of sequence base + lane (0 past s1)
@@ -107,13 +116,13 @@ __device__ Range find_range(const Kv8AttnArgs& a, int worker, int workers,
     const int s = base + lane;
     Dims d;
     d.nm = 0;
-    if (s < s1) d = seq_dims<kUnit>(a, s);
+    if (s < s1) d = seq_dims<Sh>(a, s);
     int64_t w = lane_work(d);
     uint32_t big = __ballot_sync(0xffffffffu, d.nm > 1);
     while (big) {
       const int l = __ffs(big) - 1;
       big &= big - 1;
-      const int64_t x = warp_work(seq_dims<kUnit>(a, base + l));
+      const int64_t x = warp_work(seq_dims<Sh>(a, base + l));
       if (lane == l) w = x;
     }
     return w;
@@ -152,10 +161,10 @@ __device__ Range find_range(const Kv8AttnArgs& a, int worker, int workers,
         const int l = __ffs(past) - 1;
         const int s = b + l;
         int64_t rem = r.w0 - at - __shfl_sync(0xffffffffu, inc - w, l);
-        const Dims d = seq_dims<kUnit>(a, s);
+        const Dims d = seq_dims<Sh>(a, s);
         // the block of rows: 32 at a time
         for (int m0 = 0; m0 < d.nm; m0 += 32) {
-          const int ng = m0 + lane < d.nm ? unit_span<kGranule>(a, d, m0 + lane).ng : 0;
+          const int ng = m0 + lane < d.nm ? unit_span<Sh>(a, d, m0 + lane).ng + Sh::kCost : 0;
           const int64_t x = (int64_t)ng * a.c.H_kv, xi = warp_scan(x, lane);
           const uint32_t pm = __ballot_sync(0xffffffffu, rem < xi);
           if (pm) {
@@ -166,7 +175,7 @@ __device__ Range find_range(const Kv8AttnArgs& a, int worker, int workers,
               sm.s = s;
               sm.m = m0 + k;
               sm.h = (int)(rem / n);
-              sm.t0 = (int)(rem % n);
+              sm.c0 = (int)(rem % n);
             }
             break;
           }
@@ -181,49 +190,56 @@ __device__ Range find_range(const Kv8AttnArgs& a, int worker, int workers,
   r.s = sm.s;
   r.m = sm.m;
   r.h = sm.h;
-  r.t0 = sm.t0;
+  r.c0 = sm.c0;
   return r;
 }
 
-// Walks the units of a range: unit (s, m, h), granules [t0, t1) of its span.
-template <int kUnit, int kGranule>
+// Walks the units of a range that it has granules of: unit (s, m, h), granules
+// [t0, t1) of its span.
+template <class Sh>
 struct Walk {
   int s, m, h, t0, t1;
-  int64_t pos, end;  // granules of the batch: the unit's t0, the range's end
+  int64_t pos, end;  // the batch's places: of the unit, of the range's end
   Dims d;
   Span u;
 
-  __device__ __forceinline__ void start(const Kv8AttnArgs& a, const Range& r) {
+  // To the range's first unit; false if it has none.
+  __device__ __forceinline__ bool start(const Kv8AttnArgs& a, const Range& r) {
     s = r.s;
     m = r.m;
     h = r.h;
-    t0 = r.t0;
-    pos = r.w0;
     end = r.w1;
-    d = seq_dims<kUnit>(a, s);
-    u = unit_span<kGranule>(a, d, m);
-    t1 = (int)min((int64_t)u.ng, t0 + (end - pos));
+    d = seq_dims<Sh>(a, s);
+    u = unit_span<Sh>(a, d, m);
+    pos = r.w0 - r.c0;
+    return clip(r.c0) || next(a);
   }
   // To the next unit of the range; false at its end.
   __device__ __forceinline__ bool next(const Kv8AttnArgs& a) {
-    pos += t1 - t0;
-    if (pos >= end) return false;
-    t0 = 0;
-    if (++h == a.c.H_kv) {
-      h = 0;
-      if (++m < d.nm) {
-        u = unit_span<kGranule>(a, d, m);
-      } else {
-        m = 0;
-        do {
-          if (++s >= a.c.S) return false;
-          d = seq_dims<kUnit>(a, s);
-        } while (d.nm == 0);
-        u = unit_span<kGranule>(a, d, 0);
+    while (true) {
+      pos += u.ng + Sh::kCost;
+      if (pos >= end) return false;
+      if (++h == a.c.H_kv) {
+        h = 0;
+        if (++m < d.nm) {
+          u = unit_span<Sh>(a, d, m);
+        } else {
+          m = 0;
+          do {
+            if (++s >= a.c.S) return false;
+            d = seq_dims<Sh>(a, s);
+          } while (d.nm == 0);
+          u = unit_span<Sh>(a, d, 0);
+        }
       }
+      if (clip(0)) return true;
     }
-    t1 = (int)min((int64_t)u.ng, t0 + (end - pos));
-    return true;
+  }
+  // The unit's granules from place c0 to the range's end; false if none.
+  __device__ __forceinline__ bool clip(int c0) {
+    t0 = max(0, c0 - Sh::kCost);
+    t1 = (int)min((int64_t)u.ng, end - pos - Sh::kCost);
+    return t1 > t0;
   }
   __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == u.ng; }
   __device__ __forceinline__ int first_row() const { return m * d.tpu; }  // its first token's row
@@ -274,23 +290,20 @@ __device__ __forceinline__ int row_exponent(float mx) {
 // part ends worker x's range, every gridDim.y-th group of its rows.  The
 // ranges depend on kv_len and cu alone, which were there before the kernel
 // whose parts are joined: only the parts are waited for.
-template <int kUnit, int kGranule, int kWarps, int D, bool kBf16>
+template <class Sh, int kWarps, int D, bool kBf16>
 __device__ __forceinline__ void merge_parts(const Kv8AttnArgs& a, int workers, float headroom) {
   __shared__ RangeSmem<kWarps> rsm;
-  const Range rg = find_range<kUnit, kGranule, kWarps>(a, blockIdx.x, workers, rsm);
-  if (rg.s < 0) {
-    pdl_wait();
-    return;
-  }
-  Walk<kUnit, kGranule> w;
-  w.start(a, rg);
-  while (w.pos + (w.t1 - w.t0) < w.end && w.next(a)) {
-  }
+  constexpr int kUnit = Sh::kUnit;
+  const Range rg = find_range<Sh, kWarps>(a, blockIdx.x, workers, rsm);
+  Walk<Sh> w;
+  bool cut = rg.s >= 0 && w.start(a, rg);
+  if (cut)  // only the range's last unit can be cut at its end
+    while (!(cut = w.t0 == 0 && w.t1 < w.u.ng) && w.next(a)) {
+    }
   pdl_wait();
-  if (w.t0 != 0 || w.t1 == w.u.ng) return;  // not cut here, or it began before this worker
-  // the unit is granules [pos, pos + ng): its parts are those of the workers up
-  // to the one that holds the last of them
-  const int64_t end = w.pos + w.u.ng;
+  if (!cut) return;  // none is, or it began before this worker
+  // the unit's parts are those of the workers up to the one that has its last granule
+  const int64_t end = w.pos + Sh::kCost + w.u.ng;
   const int last = (int)((end * rg.workers - 1) / rg.total);
   constexpr int kTpr = D / 4, kRowsPer = kWarps * 32 / kTpr;
   const float* base = reinterpret_cast<const float*>(a.scratch);
