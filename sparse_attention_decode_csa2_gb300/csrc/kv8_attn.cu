@@ -11,13 +11,13 @@
 // instructions (fp16 in, fp32 accumulate) therefore form q . codes with only
 // fp32 rounding.  The block scales enter in the exponent: with K scale ks and V
 // scale vs of key j's block,
-//   s_j = scale log2(e) ks (q . kcode_j) + log2(vs),   w_j = 2^(s_j - max s + 15),
+//   s_j = scale log2(e) ks (q . kcode_j) + log2(vs),   w_j = 2^(s_j - ref + 7),
 //   out = sum_j w_j vcode_j / sum_j (w_j / vs),
-// so every weight is at most 2^15 whatever the scales, and applying both scales
-// costs one fused multiply-add.  The weights are rounded to fp16 as the operand
-// of the second product (2^-11 relative; the factor 2^15 keeps weights down to
-// 2^-29 of the largest normal, so that a long tail of small ones is not lost);
-// sums and maxima are fp32.
+// with a reference near the largest s, so the weights fit fp16 whatever the
+// scales, and applying both scales costs one fused multiply-add.  The weights are
+// rounded to fp16 as the operand of the second product (2^-11 relative; the
+// factor 2^7 keeps those of 2^-21 and more of the reference normal, so that a long
+// tail of small ones is not lost); sums and maxima are fp32.
 //
 // Work split.  The units' keys are cut into granules of 128 keys and the whole
 // batch's granules are dealt to the grid's CTAs as equal contiguous ranges
@@ -26,12 +26,18 @@
 // parts of a unit that is cut go to scratch (at most two per CTA) and the merge
 // kernel joins them in order, so results do not depend on timing.
 //
-// A warp takes 32 keys of a granule through its own ring of shared-memory
-// stages (16-byte asynchronous copies, swizzled), with no barrier between warps:
-// K fragments are plain 16-byte shared loads (the channel order of the
+// A group of warps takes 32 keys at a time through its own ring of shared-memory
+// stages (16-byte asynchronous copies, swizzled); groups do not wait for one
+// another.  K fragments are plain 16-byte shared loads (the channel order of the
 // contraction is permuted so that a lane's 16 bytes are its four k-steps), V
-// fragments come from transposing matrix loads of byte pairs, both converted in
-// registers (E4M3 -> fp16 is one instruction for two values).
+// fragments come from transposing matrix loads of bytes, whose four bytes are a
+// lane's keys of a k-step when S's columns are permuted to match; both are
+// converted in registers (E4M3 -> fp16 is one instruction for two values).
+//
+// The running maximum is lazy: weights are formed with the old one, which gives
+// the key at the reference a weight of 2^7, and only where a sum of them leaves
+// fp16's range (seen from the sums that are needed anyway) does it move and O is
+// rescaled.
 #include "kv8_sched.cuh"
 
 namespace csa2 {
@@ -42,26 +48,29 @@ using namespace kv8;
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kTileKeys = 32;
-constexpr float kHeadroom = 15.0f;  // log2 of the largest weight
+// log2 of the weight at the reference, and the largest sum of eight weights: no
+// weight is above it, which fp16 holds (65504)
+constexpr float kHeadroom = 7.0f, kMostSum = 57344.0f;
 
-// kRg warps share a tile's keys, 16 query rows each; 4 / kRg groups of warps
-// have rings of their own.  The ring of a CTA has the same size for every kRg.
-template <int D, int kRg>
+// A warp has kMt matrix tiles of 16 query rows; kRg warps share a tile's keys, and
+// 4 / kRg groups of warps have rings of their own.
+template <int D, int kMt, int kRg>
 struct Cfg {
-  static constexpr int unit = 16 * kRg;                    // query rows
+  static constexpr int unit = 16 * kMt * kRg;              // query rows
   static constexpr int kgs = kWarps / kRg;                 // key groups
   static constexpr int granule = kgs * kTileKeys;          // keys
   // a unit's queries and output take about as long as 128 keys
   using Work = Shape<unit, granule, kRg>;
-  static constexpr int stages = (D == 128 ? 3 : 4) * kRg;
+  static constexpr int stages = kRg == 1 ? (D == 128 ? 3 : 4) : (D == 128 ? 5 : 8);
   static constexpr int tile = kTileKeys * D;               // bytes of K (or V) of a stage
   static constexpr int stage = 2 * tile;
   static constexpr int ring = kgs * stages * stage;
   static constexpr int scales = kgs * stages * 16;         // ks, vs of two 16-key halves
-  static constexpr int smem = ring + scales;
-  static constexpr int ctas = D == 128 ? 2 : 3;            // per SM
-  static_assert(ring >= kWarps * 16 * D * 4, "the merge of the warps reuses the ring");
-  static_assert(stages <= 16, "two bits a stage in a word");
+  // kMt > 1: the fragments of Q (in registers otherwise)
+  static constexpr int q = kMt > 1 ? unit * D * 2 : 0;
+  static constexpr int smem = ring + scales + q;
+  static constexpr int ctas = D == 64 && kMt == 1 ? 3 : 2;  // per SM
+  static_assert(ring >= kgs * unit * D * 4, "the join of the key groups reuses the ring");
 };
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
@@ -91,19 +100,87 @@ __device__ __forceinline__ void mma16816(float* c, const uint32_t* x, uint32_t b
 }
 
 // Byte offset of 16-byte chunk ch of key r in a tile: 128-byte lines, chunks
-// exclusive-or'ed with the line so that eight lanes reading one chunk of eight
-// keys, or all chunks of two keys, meet eight different banks.
+// exclusive-or'ed so that eight lanes that read one chunk of eight keys, or all
+// chunks of the two neighbouring keys of a quarter-warp, meet different banks.
 template <int D>
 __device__ __forceinline__ uint32_t tile_off(int r, int ch) {
-  if (D == 128) return (uint32_t)(r * 128 + ((ch ^ (r & 7)) << 4));
-  return (uint32_t)((r >> 1) * 128 + (((((r & 1) << 2) | ch) ^ ((r >> 1) & 7)) << 4));
+  if (D == 128) return (uint32_t)(r * 128 + ((ch ^ ((r & 1) << 2) ^ ((r >> 1) & 3)) << 4));
+  return (uint32_t)((r >> 1) * 128 + (((((r & 1) << 2) | ch) ^ ((r >> 1) & 3)) << 4));
 }
-// Key of column n of an 8-key matrix: at D = 128 two neighbouring columns are
-// four keys apart, so that a quarter-warp's two keys swizzle to different halves
-// of a line.
-template <int D>
-__device__ __forceinline__ int key_of(int n) {
-  return D == 128 ? (n >> 1) | ((n & 1) << 2) : n;
+// Key of column n of 8-key matrix nt of a tile: columns 2c, 2c + 1 of matrices
+// 2b, 2b + 1 are keys 16 b + 4 c .. + 3, the four bytes that a transposing matrix
+// load of V gives lane c.
+__device__ __forceinline__ int key_of(int nt, int n) {
+  return (nt >> 1) * 16 + (n >> 1) * 4 + (nt & 1) * 2 + (n & 1);
+}
+
+// 4 E4M3 codes -> fp16.
+__device__ __forceinline__ uint2 e4m3x4_to_f16x4(uint32_t x) {
+  uint2 r;
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(r.x), "=r"(r.y)
+      : "r"(x));
+  return r;
+}
+
+// Fragments of 16 rows of Q (this lane: rows row, row + 8 of the unit, where
+// ok): k-step 4 j + i contracts channels 64 j + 16 c + 4 i .. + 3.  bf16 rows are
+// scaled to a largest magnitude in [1, 2); crow: the rows' logit factors.
+template <int D, bool kBf16>
+__device__ __forceinline__ void load_q(const Kv8AttnArgs& a, int row0, int head0, int row, int nrow,
+                                       int c, uint32_t (*qf)[4], float* crow) {
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
+    const int rr = row + 8 * r;
+    const bool ok = rr < nrow;
+    const int tok = (ok ? rr : 0) / a.G, head = head0 + (ok ? rr % a.G : 0);
+    const uint32_t* src = reinterpret_cast<const uint32_t*>(
+        static_cast<const uint16_t*>(a.q) + (int64_t)(row0 + tok) * a.q_stride + (int64_t)head * D);
+    uint32_t x[D / 64][8];
+#pragma unroll
+    for (int j = 0; j < D / 64; ++j) {
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        const uint4 t = ok ? __ldg(reinterpret_cast<const uint4*>(src + 32 * j + 8 * c + 4 * hf))
+                           : make_uint4(0, 0, 0, 0);
+        x[j][4 * hf] = t.x;
+        x[j][4 * hf + 1] = t.y;
+        x[j][4 * hf + 2] = t.z;
+        x[j][4 * hf + 3] = t.w;
+      }
+    }
+    crow[r] = a.scale_log2;
+    if (kBf16) {
+      float mx = 0.0f;
+#pragma unroll
+      for (int j = 0; j < D / 64; ++j)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float2 f = pair_to_float2<true>(x[j][i]);
+          mx = fmaxf(mx, fmaxf(fabsf(f.x), fabsf(f.y)));
+        }
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+      const int E = row_exponent(mx);
+      const float down = pow2f(-E);
+      crow[r] *= pow2f(E);
+#pragma unroll
+      for (int j = 0; j < D / 64; ++j)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float2 f = pair_to_float2<true>(x[j][i]);
+          x[j][i] = pack_f16(f.x * down, f.y * down);
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < D / 64; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        qf[4 * j + i][r] = x[j][2 * i];
+        qf[4 * j + i][2 + r] = x[j][2 * i + 1];
+      }
+  }
 }
 
 // The warps of key group kg.
@@ -115,16 +192,17 @@ __device__ __forceinline__ void group_sync(int kg) {
     asm volatile("bar.sync %0, %1;" ::"r"(1 + kg), "n"(kRg * 32) : "memory");
 }
 
-template <int D, int kRg, bool kBf16>
-__global__ void __launch_bounds__(kThreads, Cfg<D, kRg>::ctas)
+template <int D, int kMt, int kRg, bool kBf16>
+__global__ void __launch_bounds__(kThreads, Cfg<D, kMt, kRg>::ctas)
 kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a) {
-  using C = Cfg<D, kRg>;
+  using C = Cfg<D, kMt, kRg>;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ RangeSmem<kWarps> rsm;
   __shared__ float row_max[C::kgs][C::unit], row_sum[C::kgs][C::unit];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, c = lane & 3;
   const int kg = warp / kRg, rq = warp % kRg;  // key group, row group
+  const int wrow = rq * 16 * kMt;              // the warp's first row
   pdl_trigger();
   if (blockIdx.x == 0) kv8_check_batch(a.c);
   const Range rg = find_range<typename C::Work, kWarps>(a, blockIdx.x, gridDim.x, rsm);
@@ -132,6 +210,7 @@ kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a) {
 
   uint8_t* ring = smem + kg * (C::stages * C::stage);
   float* ring_scale = reinterpret_cast<float*>(smem + C::ring) + kg * (C::stages * 4);
+  uint4* qs = reinterpret_cast<uint4*>(smem + C::ring + C::scales);  // [matrix tile][k-step][lane]
   const uint32_t ring_u = smem_u32(ring), scale_u = smem_u32(ring_scale);
   const int page_mask = (1 << a.c.page_shift) - 1;
   float* part =
@@ -141,82 +220,71 @@ kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a) {
   if (!w.start(a, rg)) return;
   do {
     const int i0 = w.first_row(), nrow = w.rows(a.G);
+    // ---- Q ----
+    uint32_t qf[kMt == 1 ? D / 16 : 1][4];
+    float crow[kMt][2];
+    if constexpr (kMt == 1) {
+      load_q<D, kBf16>(a, w.d.row0 + i0, w.h * a.G, wrow + g, nrow, c, qf, crow[0]);
+    } else {
+      if (warp < C::unit / 16) {
+        uint32_t f[D / 16][4];
+        float cr[2];
+        load_q<D, kBf16>(a, w.d.row0 + i0, w.h * a.G, warp * 16 + g, nrow, c, f, cr);
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k)
+          qs[(warp * (D / 16) + k) * 32 + lane] = make_uint4(f[k][0], f[k][1], f[k][2], f[k][3]);
+        if (c == 0) {
+          row_sum[0][warp * 16 + g] = cr[0];
+          row_sum[0][warp * 16 + g + 8] = cr[1];
+        }
+      }
+      __syncthreads();
+#pragma unroll
+      for (int mt = 0; mt < kMt; ++mt) {
+        crow[mt][0] = row_sum[0][wrow + 16 * mt + g];
+        crow[mt][1] = row_sum[0][wrow + 16 * mt + g + 8];
+      }
+      __syncthreads();  // row_sum is written again at the unit's end
+    }
+    // tokens a row sees, and those that every row of the warp sees
+    int rlo[kMt][2], rhi[kMt][2];
+    int all_lo = w.u.lo, all_hi = w.u.hi;
+#pragma unroll
+    for (int mt = 0; mt < kMt; ++mt)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const int row = wrow + 16 * mt + g + 8 * r;
+        rlo[mt][r] = w.u.lo;
+        rhi[mt][r] = w.u.hi;
+        if (a.causal && row < nrow) {
+          const int64_t p = (int64_t)w.d.len - w.d.n + i0 + row / a.G;
+          rhi[mt][r] = (int)max((int64_t)0, min((int64_t)w.u.hi, p + 1));
+          if (a.window > 0) rlo[mt][r] = (int)max((int64_t)w.u.lo, p - a.window + 1);
+        }
+        all_lo = max(all_lo, rlo[mt][r]);
+        all_hi = min(all_hi, rhi[mt][r]);
+      }
+    all_lo = __reduce_max_sync(0xffffffffu, all_lo);
+    all_hi = __reduce_min_sync(0xffffffffu, all_hi);
 
-    // ---- this lane's two rows of Q (g and g + 8) ----
-    uint32_t qf[D / 16][4];
-    float crow[2];       // logit factor of the row, without the block's K scale
-    int rlo[2], rhi[2];  // tokens the row sees
+    float o[kMt][D / 8][4];
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const int row = rq * 16 + g + 8 * r;
-      const bool ok = row < nrow;
-      const int tok = i0 + (ok ? row : 0) / a.G, head = w.h * a.G + (ok ? row % a.G : 0);
-      const uint32_t* src = reinterpret_cast<const uint32_t*>(
-          static_cast<const uint16_t*>(a.q) + (int64_t)(w.d.row0 + tok) * a.q_stride +
-          (int64_t)head * D);
-      uint32_t x[D / 64][8];
+    for (int mt = 0; mt < kMt; ++mt)
 #pragma unroll
-      for (int j = 0; j < D / 64; ++j) {
+      for (int i = 0; i < D / 8; ++i) o[mt][i][0] = o[mt][i][1] = o[mt][i][2] = o[mt][i][3] = 0.0f;
+    float mrow[kMt][2], lrow[kMt][2];
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          const uint4 t = ok ? __ldg(reinterpret_cast<const uint4*>(src + 32 * j + 8 * c + 4 * hf))
-                             : make_uint4(0, 0, 0, 0);
-          x[j][4 * hf] = t.x;
-          x[j][4 * hf + 1] = t.y;
-          x[j][4 * hf + 2] = t.z;
-          x[j][4 * hf + 3] = t.w;
-        }
-      }
-      crow[r] = a.scale_log2;
-      if (kBf16) {
-        float mx = 0.0f;
-#pragma unroll
-        for (int j = 0; j < D / 64; ++j)
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float2 f = pair_to_float2<true>(x[j][i]);
-            mx = fmaxf(mx, fmaxf(fabsf(f.x), fabsf(f.y)));
-          }
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        const int E = row_exponent(mx);
-        const float down = pow2f(-E);
-        crow[r] *= pow2f(E);
-#pragma unroll
-        for (int j = 0; j < D / 64; ++j)
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float2 f = pair_to_float2<true>(x[j][i]);
-            x[j][i] = pack_f16(f.x * down, f.y * down);
-          }
-      }
-      // k-step 4 j + i contracts channels 64 j + 16 c + 4 i .. + 3
-#pragma unroll
-      for (int j = 0; j < D / 64; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          qf[4 * j + i][r] = x[j][2 * i];
-          qf[4 * j + i][2 + r] = x[j][2 * i + 1];
-        }
-      rlo[r] = w.u.lo;
-      rhi[r] = w.u.hi;
-      if (a.causal && ok) {
-        const int64_t p = (int64_t)w.d.len - w.d.n + tok;
-        rhi[r] = (int)max((int64_t)0, min((int64_t)w.u.hi, p + 1));
-        if (a.window > 0) rlo[r] = (int)max((int64_t)rlo[r], p - a.window + 1);
-      }
+    for (int mt = 0; mt < kMt; ++mt) {
+      mrow[mt][0] = mrow[mt][1] = -INFINITY;
+      lrow[mt][0] = lrow[mt][1] = 0.0f;
     }
 
-    float o[D / 8][4];
-#pragma unroll
-    for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
-    float mrow[2] = {-INFINITY, -INFINITY}, lrow[2] = {0.0f, 0.0f};
-
     const int32_t* table = a.c.table + (int64_t)w.s * a.c.max_pages;
-    // page ids of a tile's two 16-key halves (one page where pages are longer);
-    // -1: nothing of the half is seen, or the entry is outside the cache
+    const int key_first = w.u.g0 * C::granule + kg * kTileKeys;  // of granule 0 of the span
+    // page id of this lane's 16-key half of a tile (lanes 0-15, 16-31); -1: nothing
+    // of the half is seen, or the entry is outside the cache
     auto tile_page = [&](int t) -> int {
-      const int key = (w.u.g0 + t) * C::granule + kg * kTileKeys + (lane & 16);
+      const int key = key_first + t * C::granule + (lane & 16);
       int p = -1;
       if (t < w.t1 && key < w.u.hi && key + 16 > w.u.lo) {
         p = table[key >> a.c.page_shift];
@@ -227,50 +295,62 @@ kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a) {
       }
       return p;
     };
-    auto load_tile = [&](int t, int pid) {
-      const int st = (t - w.t0) % C::stages;
-      const int p0 = __shfl_sync(0xffffffffu, pid, 0), p1 = __shfl_sync(0xffffffffu, pid, 16);
-      if (t < w.t1) {
-        const int key0 = (w.u.g0 + t) * C::granule + kg * kTileKeys;
-        const uint32_t kd = ring_u + st * C::stage, vd = kd + C::tile;
-        constexpr int kCh = D / 16;              // 16-byte chunks per key
-        constexpr int kPerIt = 32 / kCh;         // keys per instruction
-        constexpr int kMine = kTileKeys / kRg;   // keys that this warp copies
+    // A tile's copies into stage st.  A half is 16 * D contiguous bytes of a page;
+    // with two warps a group each takes a half.
+    auto load_tile = [&](int t, int st, int pid) {
+      constexpr int kCh = D / 16, kPerIt = 32 / kCh;  // chunks a key, keys an instruction
+      constexpr int kIts = 16 / kPerIt;               // instructions a half
+      const int key0 = key_first + t * C::granule;
+      const uint32_t kd = ring_u + st * C::stage, vd = kd + C::tile;
 #pragma unroll
-        for (int it = 0; it < kMine / kPerIt; ++it) {
-          const int r = rq * kMine + it * kPerIt + lane / kCh, ch = lane % kCh;
-          const int key = key0 + r;
-          const int p = r < 16 ? p0 : p1;
-          const bool ok = p >= 0 && key >= w.u.lo && key < w.u.hi;
-          const int64_t off =
-              ok ? ((((int64_t)p * a.c.H_kv + w.h) << a.c.page_shift) + (key & page_mask)) * D + ch * 16
-                 : 0;
-          const uint32_t so = tile_off<D>(r, ch);
-          copy16(kd + so, a.c.k + off, ok);
-          copy16(vd + so, a.c.v + off, ok);
+      for (int i = 0; i < 2 / kRg; ++i) {
+        const int hf = kRg == 1 ? i : rq;
+        const int p = __shfl_sync(0xffffffffu, pid, 16 * hf);
+        if (t >= w.t1) continue;
+        const int first = key0 + 16 * hf;
+        const int64_t off =
+            ((((int64_t)max(p, 0) * a.c.H_kv + w.h) << a.c.page_shift) + (first & page_mask)) * D +
+            lane * 16;
+        const uint8_t *ksrc = a.c.k + off, *vsrc = a.c.v + off;
+        if (p >= 0 && first >= w.u.lo && first + 16 <= w.u.hi) {
+#pragma unroll
+          for (int it = 0; it < kIts; ++it) {
+            const uint32_t so = tile_off<D>(16 * hf + it * kPerIt + lane / kCh, lane % kCh);
+            copy16(kd + so, ksrc + it * 512, true);
+            copy16(vd + so, vsrc + it * 512, true);
+          }
+        } else {  // keys that no row sees, or without a page, are zeros
+#pragma unroll
+          for (int it = 0; it < kIts; ++it) {
+            const int r = it * kPerIt + lane / kCh;
+            const bool ok = p >= 0 && first + r >= w.u.lo && first + r < w.u.hi;
+            const uint32_t so = tile_off<D>(16 * hf + r, lane % kCh);
+            copy16(kd + so, ksrc + it * 512, ok);
+            copy16(vd + so, vsrc + it * 512, ok);
+          }
         }
-        if (rq == 0 && lane < 4) {  // ks of half 0, 1, vs of half 0, 1
-          const int p = (lane & 1) ? p1 : p0;
-          const bool ok = p >= 0;
-          const int64_t off = ok ? (int64_t)p * a.c.H_kv + w.h : 0;
-          copy4(scale_u + (st * 4 + lane) * 4, ((lane & 2) ? a.c.v_scale : a.c.k_scale) + off, ok);
-        }
+      }
+      if (rq == 0) {  // ks of half 0, 1, vs of half 0, 1 (zeros: no page)
+        const int p = __shfl_sync(0xffffffffu, pid, (lane & 1) * 16);
+        if (lane < 4 && t < w.t1)
+          copy4(scale_u + (st * 4 + lane) * 4,
+                ((lane & 2) ? a.c.v_scale : a.c.k_scale) +
+                    (p >= 0 ? (int64_t)p * a.c.H_kv + w.h : 0),
+                p >= 0);
       }
       copy_commit();
     };
 
     int pid_next = tile_page(w.t0);
-    uint32_t live = 0;  // two bits per stage: its halves hold a page
-#pragma unroll
+#pragma unroll 1
     for (int i = 0; i < C::stages - 1; ++i) {
       const int pid = pid_next;
       pid_next = tile_page(w.t0 + i + 1);
-      load_tile(w.t0 + i, pid);
-      const uint32_t b = __ballot_sync(0xffffffffu, pid >= 0);
-      live |= ((b & 1u) | ((b >> 15) & 2u)) << (2 * i);
+      load_tile(w.t0 + i, i, pid);
     }
+    int st = 0;
+#pragma unroll 1
     for (int t = w.t0; t < w.t1; ++t) {
-      const int rel = t - w.t0, st = rel % C::stages;
       copy_wait<C::stages - 2>();
       // the group's copies of tile t are there, and it is done with tile t - 1,
       // whose stage takes the next copies
@@ -278,114 +358,157 @@ kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a) {
       {
         const int pid = pid_next;
         pid_next = tile_page(t + C::stages);
-        load_tile(t + C::stages - 1, pid);
-        const int ns = (rel + C::stages - 1) % C::stages;
-        const uint32_t b = __ballot_sync(0xffffffffu, pid >= 0);
-        live = (live & ~(3u << (2 * ns))) | (((b & 1u) | ((b >> 15) & 2u)) << (2 * ns));
+        load_tile(t + C::stages - 1, st == 0 ? C::stages - 1 : st - 1, pid);
       }
-      const uint32_t halves = (live >> (2 * st)) & 3u;
-      if (halves != 0) {
-        const uint8_t* kt = ring + st * C::stage;
-        const uint32_t vt = ring_u + st * C::stage + C::tile;
-        const int key0 = (w.u.g0 + t) * C::granule + kg * kTileKeys;
-        // ---- S = Q K^T ----
-        float sc[4][4];
+      const float4 bs = *reinterpret_cast<const float4*>(ring_scale + st * 4);
+      const uint8_t* kt = ring + st * C::stage;
+      const uint32_t vt = ring_u + st * C::stage + C::tile;
+      if (++st == C::stages) st = 0;
+      if (bs.z == 0.0f && bs.w == 0.0f) continue;
+      const int key0 = key_first + t * C::granule;
+      // ---- S = Q K^T ----
+      float sc[kMt][4][4];
 #pragma unroll
-        for (int nt = 0; nt < 4; ++nt) {
-          sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.0f;
-          const int r = nt * 8 + key_of<D>(g);
+      for (int mt = 0; mt < kMt; ++mt)
 #pragma unroll
-          for (int j = 0; j < D / 64; ++j) {
-            const uint4 b = *reinterpret_cast<const uint4*>(kt + tile_off<D>(r, 4 * j + c));
-            const uint32_t bw[4] = {b.x, b.y, b.z, b.w};
+        for (int nt = 0; nt < 4; ++nt) sc[mt][nt][0] = sc[mt][nt][1] = sc[mt][nt][2] = sc[mt][nt][3] = 0.0f;
+#pragma unroll
+      for (int j = 0; j < D / 64; ++j) {
+        uint4 qv[kMt][4];
+        if constexpr (kMt > 1) {
+#pragma unroll
+          for (int mt = 0; mt < kMt; ++mt)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-              mma16816(sc[nt], qf[4 * j + i], e4m3x2_to_f16x2((uint16_t)(bw[i] & 0xFFFFu)),
-                       e4m3x2_to_f16x2((uint16_t)(bw[i] >> 16)));
-          }
+              qv[mt][i] = qs[((rq * kMt + mt) * (D / 16) + 4 * j + i) * 32 + lane];
         }
-        // ---- block scales, masks, running maximum ----
-        const float4 bs = *reinterpret_cast<const float4*>(ring_scale + st * 4);
-        const float ks[2] = {bs.x, bs.y};
-        const float lv[2] = {(halves & 1u) ? __log2f(bs.z) : 0.0f, (halves & 2u) ? __log2f(bs.w) : 0.0f};
-        const float rv[2] = {(halves & 1u) ? 1.0f / bs.z : 0.0f, (halves & 2u) ? 1.0f / bs.w : 0.0f};
-        float tmax[2] = {-INFINITY, -INFINITY};
-        const bool whole = halves == 3u && key0 >= max(rlo[0], rlo[1]) &&
-                           key0 + kTileKeys <= min(rhi[0], rhi[1]);
 #pragma unroll
         for (int nt = 0; nt < 4; ++nt) {
-          const int hf = nt >> 1;
+          const uint4 b = *reinterpret_cast<const uint4*>(kt + tile_off<D>(key_of(nt, g), 4 * j + c));
+          const uint32_t bw[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int r = e >> 1;
-            float x = fmaf(sc[nt][e], crow[r] * ks[hf], lv[hf]);
-            if (!whole) {
-              const int key = key0 + nt * 8 + key_of<D>(2 * c + (e & 1));
-              if (key < rlo[r] || key >= rhi[r] || !((halves >> hf) & 1u)) x = -INFINITY;
+          for (int i = 0; i < 4; ++i) {
+            const uint2 f = e4m3x4_to_f16x4(bw[i]);
+            if constexpr (kMt == 1) {
+              mma16816(sc[0][nt], qf[4 * j + i], f.x, f.y);
+            } else {
+#pragma unroll
+              for (int mt = 0; mt < kMt; ++mt) {
+                const uint32_t x[4] = {qv[mt][i].x, qv[mt][i].y, qv[mt][i].z, qv[mt][i].w};
+                mma16816(sc[mt][nt], x, f.x, f.y);
+              }
             }
-            sc[nt][e] = x;
-            tmax[r] = fmaxf(tmax[r], x);
           }
         }
-        float alpha[2], mu[2];
+      }
+      // ---- masks ----
+      const bool half0 = bs.z != 0.0f, half1 = bs.w != 0.0f;
+      if (!(half0 && half1 && key0 >= all_lo && key0 + kTileKeys <= all_hi)) {
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          float x = tmax[r];
-          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
-          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-          const float m = fmaxf(mrow[r], x), z = m == -INFINITY ? 0.0f : m;
-          mu[r] = z - kHeadroom;
-          alpha[r] = ex2(mrow[r] - z);
-          mrow[r] = m;
-        }
-        // ---- weights ----
-        float ls[2][2] = {};
-        uint32_t pf[2][4];
+        for (int mt = 0; mt < kMt; ++mt)
 #pragma unroll
-        for (int nt = 0; nt < 4; ++nt) {
-          float p[4];
+          for (int nt = 0; nt < 4; ++nt)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            p[e] = ex2(sc[nt][e] - mu[e >> 1]);
-            ls[nt >> 1][e >> 1] += p[e];
+            for (int e = 0; e < 4; ++e) {
+              const int key = key0 + key_of(nt, 2 * c + (e & 1));
+              if (key < rlo[mt][e >> 1] || key >= rhi[mt][e >> 1] || !(nt < 2 ? half0 : half1))
+                sc[mt][nt][e] = -INFINITY;
+            }
+      }
+      // ---- weights ----
+      const float lv[2] = {half0 ? __log2f(bs.z) : 0.0f, half1 ? __log2f(bs.w) : 0.0f};
+      const float rv[2] = {half0 ? 1.0f / bs.z : 0.0f, half1 ? 1.0f / bs.w : 0.0f};
+      // exponents: the logit in powers of two plus log2 of the V scale.  (Subtracting
+      // the reference from the rounded exponent, not inside the fused multiply-add,
+      // makes the reference's own weight exact however large the logits are.)
+#pragma unroll
+      for (int mt = 0; mt < kMt; ++mt)
+#pragma unroll
+        for (int nt = 0; nt < 4; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            sc[mt][nt][e] = fmaf(sc[mt][nt][e],
+                                 fmaxf(crow[mt][e >> 1] * (nt < 2 ? bs.x : bs.y), 1.17549435e-38f),
+                                 lv[nt >> 1]);
+      uint32_t pf[kMt][2][4];
+      float ls[kMt][2][2];  // sums [row][half]
+      bool fresh = false;
+#pragma unroll
+      for (int mt = 0; mt < kMt; ++mt) fresh |= mrow[mt][0] == -INFINITY || mrow[mt][1] == -INFINITY;
+      bool move = __any_sync(0xffffffffu, fresh);
+#pragma unroll 1
+      for (int pass = 0; pass < 2; ++pass) {
+        if (move) {  // the reference moves to the tile's largest exponent where that is past it
+#pragma unroll
+          for (int mt = 0; mt < kMt; ++mt) {
+            float alpha[2];
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              float x = -INFINITY;
+#pragma unroll
+              for (int nt = 0; nt < 4; ++nt)
+                x = fmaxf(x, fmaxf(sc[mt][nt][2 * r], sc[mt][nt][2 * r + 1]));
+              x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+              x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+              alpha[r] = x > mrow[mt][r] ? ex2(mrow[mt][r] - x) : 1.0f;
+              mrow[mt][r] = fmaxf(mrow[mt][r], x);
+              lrow[mt][r] *= alpha[r];
+            }
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) {
+              o[mt][i][0] *= alpha[0];
+              o[mt][i][1] *= alpha[0];
+              o[mt][i][2] *= alpha[1];
+              o[mt][i][3] *= alpha[1];
+            }
           }
-          pf[nt >> 1][(nt & 1) * 2] = pack_f16(p[0], p[1]);
-          pf[nt >> 1][(nt & 1) * 2 + 1] = pack_f16(p[2], p[3]);
         }
+        float most = 0.0f;
+#pragma unroll
+        for (int mt = 0; mt < kMt; ++mt)
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const float base = (mrow[mt][r] == -INFINITY ? 0.0f : mrow[mt][r]) - kHeadroom;
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+              float p[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                p[i] = ex2(sc[mt][2 * hf + (i >> 1)][2 * r + (i & 1)] - base);
+              ls[mt][r][hf] = (p[0] + p[1]) + (p[2] + p[3]);
+              most = fmaxf(most, ls[mt][r][hf]);
+              pf[mt][hf][r] = pack_f16(p[0], p[1]);
+              pf[mt][hf][2 + r] = pack_f16(p[2], p[3]);
+            }
+          }
+        // a weight may leave fp16's range only where a sum does, and only with a
+        // reference that has not moved
+        if (move || !__any_sync(0xffffffffu, most > kMostSum)) break;
+        move = true;
+      }
+#pragma unroll
+      for (int mt = 0; mt < kMt; ++mt)
 #pragma unroll
         for (int r = 0; r < 2; ++r)
-          lrow[r] = fmaf(lrow[r], alpha[r], fmaf(ls[0][r], rv[0], ls[1][r] * rv[1]));
-        if (__any_sync(0xffffffffu, alpha[0] != 1.0f || alpha[1] != 1.0f)) {
+          lrow[mt][r] = fmaf(ls[mt][r][0], rv[0], fmaf(ls[mt][r][1], rv[1], lrow[mt][r]));
+      // ---- O += P V ----
 #pragma unroll
-          for (int i = 0; i < D / 8; ++i) {
-            o[i][0] *= alpha[0];
-            o[i][1] *= alpha[0];
-            o[i][2] *= alpha[1];
-            o[i][3] *= alpha[1];
-          }
-        }
-        // ---- O += P V ----
+      for (int kk = 0; kk < 2; ++kk) {
+        const int r = kk * 16 + (lane & 15);
 #pragma unroll
-        for (int kk = 0; kk < 2; ++kk) {
-          const int r = kk * 16 + ((lane >> 3) & 1) * 8 + key_of<D>(lane & 7);
+        for (int cb = 0; cb < D / 16; cb += 2) {
+          // two 16-key x 16-channel blocks: v[2 b + e] holds keys 4c .. 4c + 3 of
+          // channel 16 (cb + b) + 8 e + g
+          uint32_t v[4];
+          asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0,%1,%2,%3}, [%4];"
+                       : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                       : "r"(vt + tile_off<D>(r, cb + (lane >> 4)))
+                       : "memory");
 #pragma unroll
-          for (int cb = 0; cb < D / 16; cb += 2) {
-            uint32_t v[4];
-            asm volatile(
-                "ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-                : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
-                : "r"(vt + tile_off<D>(r, cb + (lane >> 4)))
-                : "memory");
+          for (int b = 0; b < 4; ++b) {
+            const uint2 f = e4m3x4_to_f16x4(v[b]);
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
-              // bytes (key, channel): (2c, 2g) (2c, 2g+1) (2c+1, 2g) (2c+1, 2g+1)
-              const uint32_t x0 = __byte_perm(v[2 * b], 0, 0x3120);
-              const uint32_t x1 = __byte_perm(v[2 * b + 1], 0, 0x3120);
-              mma16816(o[2 * (cb + b)], pf[kk], e4m3x2_to_f16x2((uint16_t)(x0 & 0xFFFFu)),
-                       e4m3x2_to_f16x2((uint16_t)(x1 & 0xFFFFu)));
-              mma16816(o[2 * (cb + b) + 1], pf[kk], e4m3x2_to_f16x2((uint16_t)(x0 >> 16)),
-                       e4m3x2_to_f16x2((uint16_t)(x1 >> 16)));
-            }
+            for (int mt = 0; mt < kMt; ++mt) mma16816(o[mt][2 * cb + b], pf[mt][kk], f.x, f.y);
           }
         }
       }
@@ -394,34 +517,37 @@ kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a) {
 
     // ---- join the key groups ----
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      lrow[r] += __shfl_xor_sync(0xffffffffu, lrow[r], 1);
-      lrow[r] += __shfl_xor_sync(0xffffffffu, lrow[r], 2);
-      if (c == 0) {
-        row_max[kg][rq * 16 + g + 8 * r] = mrow[r];
-        row_sum[kg][rq * 16 + g + 8 * r] = lrow[r];
+    for (int mt = 0; mt < kMt; ++mt)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        lrow[mt][r] += __shfl_xor_sync(0xffffffffu, lrow[mt][r], 1);
+        lrow[mt][r] += __shfl_xor_sync(0xffffffffu, lrow[mt][r], 2);
+        if (c == 0) {
+          row_max[kg][wrow + 16 * mt + g + 8 * r] = mrow[mt][r];
+          row_sum[kg][wrow + 16 * mt + g + 8 * r] = lrow[mt][r];
+        }
       }
-    }
     __syncthreads();  // every warp is done with its ring
     float* obuf = reinterpret_cast<float*>(smem);  // [key group][row][D]
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const int row = rq * 16 + g + 8 * r;
-      float m = row_max[0][row];
+    for (int mt = 0; mt < kMt; ++mt)
 #pragma unroll
-      for (int i = 1; i < C::kgs; ++i) m = fmaxf(m, row_max[i][row]);
-      const float f = ex2(mrow[r] - (m == -INFINITY ? 0.0f : m));
-      float* dst = obuf + ((size_t)kg * C::unit + row) * D;
+      for (int r = 0; r < 2; ++r) {
+        const int row = wrow + 16 * mt + g + 8 * r;
+        float m = row_max[0][row];
 #pragma unroll
-      for (int cb = 0; cb < D / 16; ++cb)
-        *reinterpret_cast<float4*>(dst + 16 * cb + 4 * c) =
-            make_float4(o[2 * cb][2 * r] * f, o[2 * cb + 1][2 * r] * f, o[2 * cb][2 * r + 1] * f,
-                        o[2 * cb + 1][2 * r + 1] * f);
-    }
+        for (int i = 1; i < C::kgs; ++i) m = fmaxf(m, row_max[i][row]);
+        const float f = ex2(mrow[mt][r] - (m == -INFINITY ? 0.0f : m));
+        float* dst = obuf + ((size_t)kg * C::unit + row) * D + 2 * c;
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i)
+          *reinterpret_cast<float2*>(dst + 8 * i) =
+              make_float2(o[mt][i][2 * r] * f, o[mt][i][2 * r + 1] * f);
+      }
     __syncthreads();
     float* pw = part + (w.t0 == 0 ? part_floats(C::unit, D) : 0);
     constexpr int kTpr = D / 4;  // threads per row
-#pragma unroll
+#pragma unroll 4
     for (int i = 0; i < C::unit * kTpr / kThreads; ++i) {
       const int row = (i * kThreads + tid) / kTpr, ch = (tid % kTpr) * 4;
       float m = row_max[0][row];
@@ -461,39 +587,32 @@ kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a) {
   } while (w.next(a));
 }
 
-template <int D, int kRg, bool kBf16>
+template <int D, int kMt, int kRg, bool kBf16>
 __global__ void __launch_bounds__(kThreads)
 kv8_merge_kernel(const __grid_constant__ Kv8AttnArgs a, int workers) {
-  using C = Cfg<D, kRg>;
+  using C = Cfg<D, kMt, kRg>;
   merge_parts<typename C::Work, kWarps, D, kBf16>(a, workers, kHeadroom);
 }
 
-template <int D>
-int grid_workers() {
-  return device_sm_count() * Cfg<D, 1>::ctas;
-}
-
-template <int D, int kRg, bool kBf16>
+template <int D, int kMt, int kRg, bool kBf16>
 cudaError_t attn_t(const Kv8AttnArgs& a, cudaStream_t stream) {
-  using C = Cfg<D, kRg>;
-  cudaError_t e = cudaFuncSetAttribute(kv8_attn_kernel<D, kRg, kBf16>,
+  using C = Cfg<D, kMt, kRg>;
+  cudaError_t e = cudaFuncSetAttribute(kv8_attn_kernel<D, kMt, kRg, kBf16>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, C::smem);
   if (e != cudaSuccess) return e;
-  const int workers = grid_workers<D>();
-  kv8_attn_kernel<D, kRg, kBf16><<<workers, kThreads, C::smem, stream>>>(a);
+  const int workers = device_sm_count() * C::ctas;
+  kv8_attn_kernel<D, kMt, kRg, kBf16><<<workers, kThreads, C::smem, stream>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   constexpr int kRowsPer = kThreads / (D / 4);
-  return launch_kernel(kv8_merge_kernel<D, kRg, kBf16>, dim3(workers, C::unit / kRowsPer),
+  return launch_kernel(kv8_merge_kernel<D, kMt, kRg, kBf16>, dim3(workers, C::unit / kRowsPer),
                        dim3(kThreads), 0, stream, /*pdl=*/true, a, workers);
 }
 
 template <int D, bool kBf16>
-cudaError_t attn_rows(const Kv8AttnArgs& a, int row_groups, cudaStream_t stream) {
-  switch (row_groups) {
-    case 1: return attn_t<D, 1, kBf16>(a, stream);
-    case 2: return attn_t<D, 2, kBf16>(a, stream);
-    default: return attn_t<D, 4, kBf16>(a, stream);
-  }
+cudaError_t attn_rows(const Kv8AttnArgs& a, int64_t rows, cudaStream_t stream) {
+  if (rows <= 16) return attn_t<D, 1, 1, kBf16>(a, stream);
+  if (rows <= 32) return attn_t<D, 2, 1, kBf16>(a, stream);
+  return attn_t<D, 2, 2, kBf16>(a, stream);
 }
 
 // Query rows of a KV head per sequence, on average.
@@ -506,19 +625,17 @@ int64_t mean_rows(int S, int T, int G) {
 size_t kv8_attn_scratch_bytes(int S, int T, int H, int H_kv, int D) {
   if (D != 64 && D != 128) return 0;
   if (mean_rows(S, T, H / H_kv) > 64) return kv8_attn_tc_scratch_bytes(D);
-  const int workers = D == 128 ? grid_workers<128>() : grid_workers<64>();
-  return align_up((size_t)workers * 2 * part_floats(64, D) * 4, 256);
+  return align_up((size_t)device_sm_count() * 3 * 2 * part_floats(64, D) * 4, 256);
 }
 
 cudaError_t launch_kv8_attn(const Kv8AttnArgs& a, int type, cudaStream_t stream) {
   const int64_t rows = mean_rows(a.c.S, a.c.T, a.G);
   if (rows > 64) return launch_kv8_attn_tc(a, type, stream);
-  const int rg = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
   if (a.c.D == 128)
-    return type == CSA2_BF16 ? attn_rows<128, true>(a, rg, stream)
-                             : attn_rows<128, false>(a, rg, stream);
-  return type == CSA2_BF16 ? attn_rows<64, true>(a, rg, stream)
-                           : attn_rows<64, false>(a, rg, stream);
+    return type == CSA2_BF16 ? attn_rows<128, true>(a, rows, stream)
+                             : attn_rows<128, false>(a, rows, stream);
+  return type == CSA2_BF16 ? attn_rows<64, true>(a, rows, stream)
+                           : attn_rows<64, false>(a, rows, stream);
 }
 
 }  // namespace csa2

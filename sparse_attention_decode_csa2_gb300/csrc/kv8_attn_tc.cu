@@ -57,6 +57,10 @@ constexpr int kTileE = 128;     // keys of a tile (and rows of a row tile)
 // log2 of the weight at the reference, and the largest sum of 16 weights: no
 // weight is above it, which fp16 holds (65504)
 constexpr float kHeadroom = 7.0f, kMostSum = 57344.0f;
+// The largest reference with which exponents are formed by one fused
+// multiply-add: its rounding is then at most 2^-8 of a power of two, that of the
+// logits themselves.
+constexpr float kFused = 65536.0f;
 using Work = Shape<kUnit, kTileE, 2>;
 constexpr uint32_t kAtom = 128 * 128;            // bytes: 128 rows of 64 fp16 channels
 
@@ -375,59 +379,13 @@ kv8_attn_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
         // instruction cache, and unrolled it misses)
 #pragma unroll 1
         for (int half = 0; half < 2; ++half) {
-          uint32_t p[32];
-          float sum;
-          bool move = __any_sync(0xffffffffu, m_ref == -INFINITY);
-          while (true) {
-            if (move) {  // the reference moves to the half's largest logit where that is past it
-              float x = -INFINITY;
-#pragma unroll 1
-              for (int i = 0; i < 2; ++i) {
-                uint32_t y[32];
-                tmem_ld32(ts + 64 * half + 32 * i, y);
-                tmem_wait_ld32(y);
-#pragma unroll
-                for (int gi = 0; gi < 2; ++gi) {
-                  const float4 b = sc[4 * half + 2 * i + gi];
-                  float mx = __uint_as_float(y[16 * gi]);
-#pragma unroll
-                  for (int k = 1; k < 16; ++k) mx = fmaxf(mx, __uint_as_float(y[16 * gi + k]));
-                  x = fmaxf(x, fmaf(mx, fmaxf(crow * b.x, 1.17549435e-38f), b.y));
-                }
-              }
-              const float alpha = x > m_ref ? ex2(m_ref - x) : 1.0f;
-              m_ref = fmaxf(m_ref, x);
-              l *= alpha;
-              // S_t(j) is done, so O_t(j - 1), issued before it, is too
-              if (j > t0) {
-#pragma unroll 1
-                for (int i = 0; i < D; i += 16) {
-                  float o[16];
-                  tmem_ld16(to + i, o);
-                  tmem_wait_ld();
-#pragma unroll
-                  for (int k = 0; k < 16; ++k) o[k] *= alpha;
-                  tmem_st16(to + i, o);
-                }
-              }
-              if (half == 1) {  // the first half's weights had the old reference
-                const __half2 a2 = __float2half2_rn(alpha);
-                uint32_t y[32];
-                tmem_ld32(ts, y);
-                tmem_wait_ld32(y);
-#pragma unroll
-                for (int k = 0; k < 32; ++k) {
-                  const __half2 z = __hmul2(*reinterpret_cast<const __half2*>(&y[k]), a2);
-                  y[k] = *reinterpret_cast<const uint32_t*>(&z);
-                }
-                tmem_st32(ts, y);
-              }
-            }
-            // the weights with the reference as it is; `most`: the largest sum of a group
-            const float base = (m_ref == -INFINITY ? 0.0f : m_ref) - kHeadroom;
-            float most = 0.0f;
-            sum = 0.0f;
-            uint32_t s[2][32];
+          // with a reference (and logits small enough for the fused form below to be
+          // as exact as they are): the weights in one pass
+          bool slow = __any_sync(0xffffffffu, !(fabsf(m_ref) <= kFused));
+          if (!slow) {
+            uint32_t p[32], s[2][32];
+            const float base = m_ref - kHeadroom;
+            float sum = 0.0f, most = 0.0f;  // `most`: the largest sum of a group
             tmem_ld32(ts + 64 * half, s[0]);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
@@ -454,13 +412,83 @@ kv8_attn_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
                 sum = fmaf(one, b.z, sum);
               }
             }
-            // a weight may leave fp16's range only in a group whose sum does: then the
-            // reference moves and the weights are formed again
-            if (!__any_sync(0xffffffffu, most > kMostSum)) break;
-            move = true;
+            // a weight may leave fp16's range only in a group whose sum does
+            slow = __any_sync(0xffffffffu, most > kMostSum);
+            if (!slow) {
+              l += sum;
+              tmem_st32(ts + 32 * half, p);
+            }
           }
-          l += sum;
-          tmem_st32(ts + 32 * half, p);
+          if (slow) {  // the reference moves to the half's largest exponent where that is past it
+            float x = -INFINITY;
+#pragma unroll 1
+            for (int i = 0; i < 2; ++i) {
+              uint32_t y[32];
+              tmem_ld32(ts + 64 * half + 32 * i, y);
+              tmem_wait_ld32(y);
+#pragma unroll
+              for (int gi = 0; gi < 2; ++gi) {
+                const float4 b = sc[4 * half + 2 * i + gi];
+                float mx = __uint_as_float(y[16 * gi]);
+#pragma unroll
+                for (int k = 1; k < 16; ++k) mx = fmaxf(mx, __uint_as_float(y[16 * gi + k]));
+                x = fmaxf(x, fmaf(mx, fmaxf(crow * b.x, 1.17549435e-38f), b.y));
+              }
+            }
+            const float alpha = x > m_ref ? ex2(m_ref - x) : 1.0f;
+            m_ref = fmaxf(m_ref, x);
+            l *= alpha;
+            // S_t(j) is done, so O_t(j - 1), issued before it, is too
+            if (j > t0) {
+#pragma unroll 1
+              for (int i = 0; i < D; i += 16) {
+                float o[16];
+                tmem_ld16(to + i, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int k = 0; k < 16; ++k) o[k] *= alpha;
+                tmem_st16(to + i, o);
+              }
+            }
+            if (half == 1) {  // the first half's weights had the old reference
+              const __half2 a2 = __float2half2_rn(alpha);
+              uint32_t y[32];
+              tmem_ld32(ts, y);
+              tmem_wait_ld32(y);
+#pragma unroll
+              for (int k = 0; k < 32; ++k) {
+                const __half2 z = __hmul2(*reinterpret_cast<const __half2*>(&y[k]), a2);
+                y[k] = *reinterpret_cast<const uint32_t*>(&z);
+              }
+              tmem_st32(ts, y);
+            }
+            // the weights, the reference subtracted from the rounded exponent: its own
+            // weight is exact however large the logits are.  P's columns are those of
+            // keys that have been read
+            const float base = (m_ref == -INFINITY ? 0.0f : m_ref) - kHeadroom;
+#pragma unroll 1
+            for (int i = 0; i < 2; ++i) {
+              uint32_t y[32];
+              float p[16];
+              tmem_ld32(ts + 64 * half + 32 * i, y);
+              tmem_wait_ld32(y);
+#pragma unroll
+              for (int gi = 0; gi < 2; ++gi) {
+                const float4 b = sc[4 * half + 2 * i + gi];
+                const float c = fmaxf(crow * b.x, 1.17549435e-38f);
+                float one = 0.0f;
+#pragma unroll
+                for (int k = 0; k < 16; k += 2) {
+                  const float w0 = ex2(fmaf(__uint_as_float(y[16 * gi + k]), c, b.y) - base);
+                  const float w1 = ex2(fmaf(__uint_as_float(y[16 * gi + k + 1]), c, b.y) - base);
+                  one += w0 + w1;
+                  p[8 * gi + k / 2] = __uint_as_float(pack_f16(w0, w1));
+                }
+                l = fmaf(one, b.z, l);
+              }
+              tmem_st16(ts + 32 * half + 16 * i, p);
+            }
+          }
         }
         tmem_wait_st();
         warp_arrive(&ctl.p_full[t]);

@@ -333,6 +333,31 @@ def test_attn_queries_of_extreme_magnitude(C):
     assert (np.abs(lse[1:].double().cpu().numpy() - ref[1]) <= tol_l).all()
 
 
+def test_attn_prompt_queries_of_extreme_magnitude(C):
+    # as above for prompts: logits of 1e30 (only the largest token counts), 1e5, 1e-30 and 0
+    n, D = 80, 128
+    w = World(C, 47, [300] * 3, 1, D, 64).fill()
+    q = _q(w.rng, 3 * n, 2, D, BF16)
+    q[:n:2] *= 1e30
+    q[1:n:2] *= 1e5
+    q[n:2 * n:2] *= 1e-30
+    q[n + 1:2 * n:2] = 0
+    cache, batch = w.cache(), w.batch(3 * n)
+    out, lse = C.kv8_attn(q.cuda(), cache, batch)
+    assert torch.isfinite(out).all() and torch.isfinite(lse).all()
+    V = R.gather(w.v, w.vs, w.table[0], 0, 300, 64)[:, 0]
+    z = R.gather(w.k, w.ks, w.table[0], 0, 300, 64)[:, 0] @ q[:n].double().numpy().transpose(0, 2, 1)  # [n][300][2]
+    for i in range(0, n, 2):
+        for h in range(2):
+            best = z[i, :300 - n + i + 1, h].argmax()
+            assert torch.equal(out[i, h].cpu(), torch.from_numpy(V[best]).to(BF16)), (i, h)
+    ref = R.attention(q[n:].double().numpy(), (w.k, w.v, w.ks, w.vs), w.table[1:], [300] * 2,
+                      R.rows_of(2 * n, 2, None), 64, True, 0, 1 / math.sqrt(D))
+    tol_o, tol_l = R.attention_bounds(*ref, D, 300, BF16)
+    assert (np.abs(out[n:].double().cpu().numpy() - ref[0]) <= tol_o).all()
+    assert (np.abs(lse[n:].double().cpu().numpy() - ref[1]) <= tol_l).all()
+
+
 def test_attn_a_long_tail_of_small_weights_is_not_lost(C):
     # one token with weight near 1 and 4096 tokens 2^-20 below it that all share a direction
     D, L = 64, 4097
