@@ -561,7 +561,7 @@ class Kv8Cache:
         self.n_pages, self.kv_heads, self.page, self.dim = k.shape
         self.k_scale = _out(k_scale, k.shape[:2], torch.float32, "k_scale")
         self.v_scale = _out(v_scale, k.shape[:2], torch.float32, "v_scale")
-        self.device = k.device
+        self.device, self.index = k.device, k.device.index
         _same_device(self.device, v=v, k_scale=k_scale, v_scale=v_scale)
         self._c = Csa2Kv8Cache(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), self.n_pages,
                                self.kv_heads, self.page, self.dim)
@@ -591,7 +591,7 @@ class Kv8Batch:
         self.seqs, self.n_rows = S, int(n_rows)
         if self.n_rows < 0 or (cu_rows is None and self.n_rows % max(1, S)):
             raise ValueError(f"{n_rows} rows are no equal shares of {S} sequences")
-        self.device = block_table.device
+        self.device, self.index = block_table.device, block_table.device.index
         _same_device(self.device, kv_len=kv_len, cu_rows=cu_rows)
         self._c = Csa2Kv8Batch(_ptr(block_table), _ptr(kv_len), _ptr(cu_rows), S, self.n_rows, W)
         self._ref = ctypes.byref(self._c)
@@ -603,32 +603,38 @@ def _same_device(device, **tensors) -> None:
             raise ValueError(f"{name} is on {t.device}, not on {device}")
 
 
-def _kv8_rows(t: torch.Tensor, rows: int, heads: Optional[int], dim: int, device, name: str) -> int:
+def _kv8_rows(t: torch.Tensor, rows: int, heads: Optional[int], cache: Kv8Cache, name: str) -> int:
     """Checks [rows][heads][dim] whose tokens may be strided; returns the token stride."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor (there is no CPU path)")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, not on {device}")
-    sh = t.shape
-    if t.dim() != 3 or sh[0] != rows or sh[2] != dim or (heads is not None and sh[1] != heads):
-        raise ValueError(f"{name} must be [{rows}][{heads if heads is not None else 'H'}][{dim}], "
-                         f"got {tuple(sh)}")
-    s0, s1, s2 = t.stride()
-    dense = sh[1] * dim
-    if s2 != 1 or (s1 != dim and sh[1] > 1):
+    if t.get_device() != cache.index:
+        raise ValueError(f"{name} is on {t.device}, not on {cache.device}")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must have three dimensions, got {tuple(t.shape)}")
+    (n, h, d), (s0, s1, s2) = t.shape, t.stride()
+    if n != rows or d != cache.dim or (heads is not None and h != heads):
+        raise ValueError(f"{name} must be [{rows}][{heads if heads is not None else 'H'}]"
+                         f"[{cache.dim}], got {tuple(t.shape)}")
+    if s2 != 1 or (s1 != d and h > 1):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
-    if rows > 1 and s0 < dense:
+    if rows <= 1:
+        return h * d
+    if s0 < h * d:
         raise ValueError(f"{name}: tokens must not overlap")
-    return s0 if rows > 1 else dense
+    return s0
 
 
-def _kv8_call(device, where: str, fn, *args) -> None:
+# (the current stream's handle without a Stream object around it: 0.1 against 3 us a call)
+_raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+
+
+def _kv8_call(index: int, where: str, fn, *args) -> None:
     # the kernels run on the tensors' device, on its current stream
-    if torch.cuda.current_device() == device.index:
-        code = fn(*args, _stream())
+    if _current_device() == index:
+        code = fn(*args, _raw_stream(index))
     else:
-        with torch.cuda.device(device):
-            code = fn(*args, _stream())
+        with torch.cuda.device(index):
+            code = fn(*args, _raw_stream(index))
     if code:
         _check(code, where)
 
@@ -644,12 +650,11 @@ def make_kv8_workspace(cache: Kv8Cache, batch: Kv8Batch, heads: int = 0) -> torc
 
 def _kv8_ws(cache: Kv8Cache, batch: Kv8Batch, heads: int,
             ws: Optional[torch.Tensor]) -> torch.Tensor:
-    if batch.device != cache.device:
+    if batch.index != cache.index:
         raise ValueError(f"the batch is on {batch.device}, the cache on {cache.device}")
     if ws is None:
         return make_kv8_workspace(cache, batch, heads)
-    _dev(ws, torch.uint8, "ws")
-    if ws.device != cache.device:
+    if _dev(ws, torch.uint8, "ws").get_device() != cache.index:
         raise ValueError(f"ws is on {ws.device}, not on {cache.device}")
     return ws
 
@@ -661,9 +666,9 @@ def kv8_append(cache: Kv8Cache, batch: Kv8Batch, k: torch.Tensor, v: torch.Tenso
     ws = _kv8_ws(cache, batch, 0, ws)
     if k.dtype not in _KV8_TYPES or v.dtype != k.dtype:
         raise ValueError(f"k and v must both be bf16, fp16 or fp32, got {k.dtype} and {v.dtype}")
-    ks = _kv8_rows(k, batch.n_rows, cache.kv_heads, cache.dim, cache.device, "k")
-    vs = _kv8_rows(v, batch.n_rows, cache.kv_heads, cache.dim, cache.device, "v")
-    _kv8_call(cache.device, "csa2_kv8_append", lib.csa2_kv8_append, cache._ref, batch._ref,
+    ks = _kv8_rows(k, batch.n_rows, cache.kv_heads, cache, "k")
+    vs = _kv8_rows(v, batch.n_rows, cache.kv_heads, cache, "v")
+    _kv8_call(cache.index, "csa2_kv8_append", lib.csa2_kv8_append, cache._ref, batch._ref,
               k.data_ptr(), v.data_ptr(), _KV8_TYPES[k.dtype], ks, vs, ws.data_ptr(), ws.numel())
 
 
@@ -677,12 +682,13 @@ def kv8_read(cache: Kv8Cache, batch: Kv8Batch, dtype: torch.dtype = torch.bfloat
     shape = (batch.n_rows, cache.kv_heads, cache.dim)
     if out_k is None:
         out_k = torch.empty(shape, dtype=dtype, device=cache.device)
+    else:
+        _same_device(cache.device, out_k=_out(out_k, shape, dtype, "out_k"))
     if out_v is None:
         out_v = torch.empty(shape, dtype=dtype, device=cache.device)
-    _out(out_k, shape, dtype, "out_k")
-    _out(out_v, shape, dtype, "out_v")
-    _same_device(cache.device, out_k=out_k, out_v=out_v)
-    _kv8_call(cache.device, "csa2_kv8_read", lib.csa2_kv8_read, cache._ref, batch._ref,
+    else:
+        _same_device(cache.device, out_v=_out(out_v, shape, dtype, "out_v"))
+    _kv8_call(cache.index, "csa2_kv8_read", lib.csa2_kv8_read, cache._ref, batch._ref,
               out_k.data_ptr(), out_v.data_ptr(), _KV8_TYPES[dtype], ws.data_ptr(), ws.numel())
     return out_k, out_v
 
@@ -697,20 +703,20 @@ def kv8_attn(q: torch.Tensor, cache: Kv8Cache, batch: Kv8Batch, causal: bool = T
     allocated here)."""
     if q.dtype not in (torch.bfloat16, torch.float16):
         raise ValueError(f"q must be bf16 or fp16, got {q.dtype}")
-    qs = _kv8_rows(q, batch.n_rows, None, cache.dim, cache.device, "q")
+    qs = _kv8_rows(q, batch.n_rows, None, cache, "q")
     T, H, D = q.shape
     ws = _kv8_ws(cache, batch, H, ws)
     if softmax_scale is None:
         softmax_scale = 1.0 / math.sqrt(D)
     if out is None:
-        out = torch.empty((T, H, D), dtype=q.dtype, device=q.device)
+        out = torch.empty((T, H, D), dtype=q.dtype, device=cache.device)
     else:
         _same_device(q.device, out=_out(out, (T, H, D), q.dtype, "out"))
     if lse is not None:
         _same_device(q.device, lse=_out(lse, (T, H), torch.float32, "lse"))
     elif want_lse:
-        lse = torch.empty((T, H), dtype=torch.float32, device=q.device)
-    _kv8_call(cache.device, "csa2_kv8_attn", lib.csa2_kv8_attn, q.data_ptr(), _KV8_TYPES[q.dtype],
+        lse = torch.empty((T, H), dtype=torch.float32, device=cache.device)
+    _kv8_call(cache.index, "csa2_kv8_attn", lib.csa2_kv8_attn, q.data_ptr(), _KV8_TYPES[q.dtype],
               qs, H, cache._ref, batch._ref, 1 if causal else 0, window, softmax_scale,
               out.data_ptr(), _ptr(lse), ws.data_ptr(), ws.numel())
     return out, lse

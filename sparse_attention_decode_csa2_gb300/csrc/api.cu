@@ -586,6 +586,7 @@ csa2_status csa2_kv8_attn(const void* q, int type, int64_t q_stride, int H,
   a.lse = lse;
   a.causal = causal ? 1 : 0;
   a.window = window;
+  a.uncut = 0;
   a.scale_log2 = softmax_scale * 1.44269504088896340736f;
   a.scratch = reinterpret_cast<uint8_t*>(ws) + kStatusBytes;
   return check_launch(launch_kv8_attn(a, type, stream));

@@ -29,23 +29,21 @@ struct Kv8Seq {
   bool bad;
 };
 
-__device__ __forceinline__ Kv8Seq kv8_seq(const Kv8Args& a, int s) {
+// From its entries cu[s], cu[s + 1] (with cu) and kv_len[s].
+__device__ __forceinline__ Kv8Seq kv8_seq_of(const Kv8Args& a, int r0, int r1, int len) {
   Kv8Seq q;
-  if (a.cu) {
-    const int r0 = a.cu[s], r1 = a.cu[s + 1];
-    q.bad = r0 < 0 || r1 < r0 || r1 > a.T;
-    q.row0 = q.bad ? 0 : r0;
-    q.n = q.bad ? 0 : r1 - r0;
-  } else {
-    q.n = a.T / a.S;
-    q.row0 = s * q.n;
-    q.bad = false;
-  }
-  q.len = a.kv_len[s];
+  q.bad = r0 < 0 || r1 < r0 || r1 > a.T;
+  q.row0 = q.bad ? 0 : r0;
+  q.n = q.bad ? 0 : r1 - r0;
   // a length past the block table: the tokens the table has no entry for are skipped
-  q.bad = q.bad || q.len < 0 || q.len > (int)((int64_t)a.max_pages << a.page_shift);
-  if (q.len < 0) q.len = 0;
+  q.bad = q.bad || len < 0 || len > (int)((int64_t)a.max_pages << a.page_shift);
+  q.len = len < 0 ? 0 : len;
   return q;
+}
+__device__ __forceinline__ Kv8Seq kv8_seq(const Kv8Args& a, int s) {
+  const int n = a.T / a.S;
+  return a.cu ? kv8_seq_of(a, a.cu[s], a.cu[s + 1], a.kv_len[s])
+              : kv8_seq_of(a, s * n, s * n + n, a.kv_len[s]);
 }
 
 // Raises the bad-index bit if any sequence's entries make no sense (one
@@ -90,9 +88,16 @@ struct Kv8AttnArgs {
   void* out;           // [T][H][D], q's type
   float* lse;          // [T][H] or null
   int H, G, causal, window;
+  int uncut;           // every unit is one worker's: no parts, no merge kernel
   float scale_log2;    // softmax scale * log2(e)
   uint8_t* scratch;    // kv8_attn_scratch_bytes(...)
 };
+
+// Tokens that a row can see at most, from what the host knows.
+inline int64_t kv8_most_tokens(const Kv8AttnArgs& a) {
+  const int64_t table = (int64_t)a.c.max_pages << a.c.page_shift;
+  return a.window > 0 && a.window < table ? a.window : table;
+}
 
 size_t kv8_attn_scratch_bytes(int S, int T, int H, int H_kv, int D);
 // The kernels for many query rows per sequence (chosen by launch_kv8_attn).

@@ -204,7 +204,6 @@ kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a) {
   const int kg = warp / kRg, rq = warp % kRg;  // key group, row group
   const int wrow = rq * 16 * kMt;              // the warp's first row
   pdl_trigger();
-  if (blockIdx.x == 0) kv8_check_batch(a.c);
   const Range rg = find_range<typename C::Work, kWarps>(a, blockIdx.x, gridDim.x, rsm);
   if (rg.s < 0) return;
 
@@ -602,7 +601,7 @@ cudaError_t attn_t(const Kv8AttnArgs& a, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   const int workers = device_sm_count() * C::ctas;
   kv8_attn_kernel<D, kMt, kRg, kBf16><<<workers, kThreads, C::smem, stream>>>(a);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  if ((e = cudaGetLastError()) != cudaSuccess || a.uncut) return e;
   constexpr int kRowsPer = kThreads / (D / 4);
   return launch_kernel(kv8_merge_kernel<D, kMt, kRg, kBf16>, dim3(workers, C::unit / kRowsPer),
                        dim3(kThreads), 0, stream, /*pdl=*/true, a, workers);
@@ -614,6 +613,9 @@ cudaError_t attn_rows(const Kv8AttnArgs& a, int64_t rows, cudaStream_t stream) {
   if (rows <= 32) return attn_t<D, 2, 1, kBf16>(a, stream);
   return attn_t<D, 2, 2, kBf16>(a, stream);
 }
+
+// Units of up to so many keys are not cut.
+constexpr int64_t kUncut = 512, kUncutTc = 512;
 
 // Query rows of a KV head per sequence, on average.
 int64_t mean_rows(int S, int T, int G) {
@@ -628,8 +630,11 @@ size_t kv8_attn_scratch_bytes(int S, int T, int H, int H_kv, int D) {
   return align_up((size_t)device_sm_count() * 3 * 2 * part_floats(64, D) * 4, 256);
 }
 
-cudaError_t launch_kv8_attn(const Kv8AttnArgs& a, int type, cudaStream_t stream) {
+cudaError_t launch_kv8_attn(const Kv8AttnArgs& args, int type, cudaStream_t stream) {
+  Kv8AttnArgs a = args;
   const int64_t rows = mean_rows(a.c.S, a.c.T, a.G);
+  // cutting a unit of a few tiles gains less than the merge kernel takes
+  a.uncut = kv8_most_tokens(a) <= (rows > 64 ? kUncutTc : kUncut);
   if (rows > 64) return launch_kv8_attn_tc(a, type, stream);
   if (a.c.D == 128)
     return type == CSA2_BF16 ? attn_rows<128, true>(a, rows, stream)

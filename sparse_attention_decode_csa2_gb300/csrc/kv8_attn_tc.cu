@@ -240,7 +240,6 @@ kv8_attn_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   int32_t* status = a.c.status;
   pdl_trigger();
-  if (blockIdx.x == 0) kv8_check_batch(a.c);
   const Range rg = find_range<Work, kWarps>(a, blockIdx.x, gridDim.x, ctl.range);
   if (rg.s < 0) return;
   Walk<Work>& w = ctl.walk[min(warp, kMmaWarp1)];
@@ -743,7 +742,7 @@ cudaError_t attn_tc_t(const Kv8AttnArgs& a, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   const int workers = device_sm_count();
   kv8_attn_tc_kernel<D, kBf16><<<workers, kThreads, L::alloc, stream>>>(a);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  if ((e = cudaGetLastError()) != cudaSuccess || a.uncut) return e;
   return launch_kernel(kv8_merge_tc_kernel<D, kBf16>, dim3(workers, 8), dim3(128), 0, stream,
                        /*pdl=*/true, a, workers);
 }

@@ -12,10 +12,14 @@
 // rounded again (exact except where a code becomes subnormal).  A step that
 // writes a page's first token starts the scale anew, whatever the page held.
 //
-// One team of threads (a warp for a few rows per sequence, else a block of
-// 256) owns the rows of one (sequence, page, head) of K or V: it reads them
-// once into registers, reduces absmax, settles the scale and stores the codes.
-// No two teams touch the same block, so there are no atomics.
+// One team of threads (a warp for small blocks or a few rows per sequence, else
+// 128) owns the rows of one (sequence, page, head) of K or V: it reads them once
+// into registers, reduces absmax, settles the scale and stores the codes.  No two
+// teams touch the same block, so there are no atomics.  The team first follows a
+// chain of dependent loads (sequence, page, rows), so what bounds the writer of
+// prompts is how many rows the resident teams hold in flight: 128 threads with
+// four 32-byte pieces each keep a page of 64 rows of 128 channels in 64 registers
+// a thread, eight teams to an SM.
 #include <cuda_bf16.h>
 
 #include "kv8.cuh"
@@ -23,7 +27,8 @@
 namespace csa2 {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kTeamBig = 128;             // threads of a team (and of its block)
+constexpr int kBlockSmall = 256;          // threads of a block of warp teams
 constexpr int kEMin = -100, kEMax = 120;  // scale exponents
 
 template <typename T>
@@ -133,35 +138,43 @@ struct Slot {
 __device__ __forceinline__ Slot find_slot(const Kv8Args& a, int64_t slot) {
   Slot r;
   if (a.cu) {
-    // last s with clamp(cu[s]) / page + 2 s <= slot, 32 candidates a round
-    // (every lane of a warp has the same slot)
+    // last s with clamp(cu[s]) / page + 2 s <= slot, 32 candidates a round (every
+    // lane of a warp has the same slot); the last round has the sequence's entries
     const int lane = threadIdx.x & 31;
-    int lo = 0, hi = a.S;  // key(lo) <= slot (key(0) >= 0 is checked below)
-    while (hi - lo > 1) {
-      const int step = (hi - lo + 31) / 32;
-      const int c = lo + (lane + 1) * step;
+    int lo = 0, hi = a.S, step;
+    do {
+      step = (hi - lo + 31) / 32;
+      const int c = lo + lane * step;
+      int cu = 0, next = 0, len = 0;
       bool le = false;
       if (c < hi) {
-        const int cu = min(max(a.cu[c], 0), a.T);
-        le = ((int64_t)(cu >> a.page_shift) + 2 * (int64_t)c) <= slot;
+        cu = a.cu[c];
+        if (step == 1) {
+          next = a.cu[c + 1];
+          len = a.kv_len[c];
+        }
+        le = lane == 0 || ((int64_t)(min(max(cu, 0), a.T) >> a.page_shift) + 2 * (int64_t)c) <= slot;
       }
-      const uint32_t m = __ballot_sync(0xffffffffu, le);
-      const int k = m == 0 ? 0 : 32 - __clz(m);  // highest candidate that is not past the slot
-      const int nlo = lo + k * step;
-      hi = min(hi, nlo + step);
-      lo = nlo;
-    }
+      const int k = 31 - __clz(__ballot_sync(0xffffffffu, le));  // the highest that is not past the slot
+      lo += k * step;
+      hi = min(hi, lo + step);
+      if (step == 1) {
+        cu = __shfl_sync(0xffffffffu, cu, k);
+        next = __shfl_sync(0xffffffffu, next, k);
+        len = __shfl_sync(0xffffffffu, len, k);
+        r.q = kv8_seq_of(a, cu, next, len);
+        const int64_t j = slot - ((int64_t)(min(max(cu, 0), a.T) >> a.page_shift) + 2 * (int64_t)lo);
+        r.j = j < 0 || j > INT32_MAX ? INT32_MAX : (int)j;
+      }
+    } while (step > 1);
     r.s = lo;
-    const int cu = min(max(a.cu[lo], 0), a.T);
-    const int64_t j = slot - ((int64_t)(cu >> a.page_shift) + 2 * (int64_t)lo);
-    r.j = j < 0 || j > INT32_MAX ? INT32_MAX : (int)j;
   } else {
     const int64_t page = (int64_t)1 << a.page_shift;
     const int64_t per = ((int64_t)(a.T / a.S) + page - 2) / page + 1;
     r.s = (int)(slot / per);
     r.j = (int)(slot % per);
+    r.q = kv8_seq(a, r.s);
   }
-  r.q = kv8_seq(a, r.s);
   const int cap = (int)min((int64_t)r.q.len, (int64_t)a.max_pages << a.page_shift);
   const int64_t first = (int64_t)r.q.len - r.q.n;  // token of the sequence's row 0
   const int p0 = first < 0 ? 0 : (int)first;
@@ -173,6 +186,11 @@ __device__ __forceinline__ Slot find_slot(const Kv8Args& a, int64_t slot) {
   r.rows = r.q.n > 0 && r.col < a.max_pages && hi > lo ? (int)(hi - lo) : 0;
   r.row = r.q.row0 + (int)(lo - first);
   return r;
+}
+
+template <int kTeam>
+constexpr int block_of() {
+  return kTeam == 32 ? kBlockSmall : kTeam;
 }
 
 template <int kTeam>
@@ -189,13 +207,15 @@ __device__ __forceinline__ float team_max(float x, float* red) {
 }
 
 template <typename T, int kTeam>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(block_of<kTeam>(), (kTeam == 32 ? 4 : 8) / (sizeof(T) / 2))
 kv8_append_kernel(const __grid_constant__ Kv8Args a, const T* __restrict__ k,
                   const T* __restrict__ v, int64_t k_stride, int64_t v_stride, int64_t items) {
-  __shared__ float red[kThreads / 32];
-  if (blockIdx.x == 0) kv8_check_batch(a);
-  const int64_t item = (int64_t)blockIdx.x * (kThreads / kTeam) + threadIdx.x / kTeam;
-  if (item >= items) return;
+  __shared__ float red[kTeam / 32];
+  const int64_t item = (int64_t)blockIdx.x * (block_of<kTeam>() / kTeam) + threadIdx.x / kTeam;
+  if (item >= items) {
+    kv8_check_batch(a);  // the threads behind the last item (there are some) look for bad entries
+    return;
+  }
   const int t = threadIdx.x % kTeam;
   const bool is_v = item & 1;
   const int h = (int)((item >> 1) % a.H_kv);
@@ -273,7 +293,8 @@ template <>
 __device__ __forceinline__ void store16<float>(float* p, const float* x) {
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    reinterpret_cast<float4*>(p)[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+    __stcs(reinterpret_cast<float4*>(p) + i,
+           make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]));
 }
 template <>
 __device__ __forceinline__ void store16<__half>(__half* p, const float* x) {
@@ -283,8 +304,8 @@ __device__ __forceinline__ void store16<__half>(__half* p, const float* x) {
     const __half2 h = __floats2half2_rn(x[2 * i], x[2 * i + 1]);
     w[i] = *reinterpret_cast<const uint32_t*>(&h);
   }
-  reinterpret_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-  reinterpret_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  __stcs(reinterpret_cast<uint4*>(p), make_uint4(w[0], w[1], w[2], w[3]));
+  __stcs(reinterpret_cast<uint4*>(p) + 1, make_uint4(w[4], w[5], w[6], w[7]));
 }
 template <>
 __device__ __forceinline__ void store16<__nv_bfloat16>(__nv_bfloat16* p, const float* x) {
@@ -294,20 +315,22 @@ __device__ __forceinline__ void store16<__nv_bfloat16>(__nv_bfloat16* p, const f
     const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
     w[i] = *reinterpret_cast<const uint32_t*>(&h);
   }
-  reinterpret_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-  reinterpret_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  __stcs(reinterpret_cast<uint4*>(p), make_uint4(w[0], w[1], w[2], w[3]));
+  __stcs(reinterpret_cast<uint4*>(p) + 1, make_uint4(w[4], w[5], w[6], w[7]));
 }
 
 // Values of the step's rows: code * scale, rounded once to T.  Teams and
 // items as the writer's; rows of tokens below zero, and of pages outside the
 // cache, read as zeros.
 template <typename T, int kTeam>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(block_of<kTeam>())
 kv8_read_kernel(const __grid_constant__ Kv8Args a, T* __restrict__ k, T* __restrict__ v,
                 int64_t items) {
-  if (blockIdx.x == 0) kv8_check_batch(a);
-  const int64_t item = (int64_t)blockIdx.x * (kThreads / kTeam) + threadIdx.x / kTeam;
-  if (item >= items) return;
+  const int64_t item = (int64_t)blockIdx.x * (block_of<kTeam>() / kTeam) + threadIdx.x / kTeam;
+  if (item >= items) {
+    kv8_check_batch(a);
+    return;
+  }
   const int t = threadIdx.x % kTeam;
   const bool is_v = item & 1;
   const int h = (int)((item >> 1) % a.H_kv);
@@ -343,10 +366,16 @@ kv8_read_kernel(const __grid_constant__ Kv8Args a, T* __restrict__ k, T* __restr
   }
 }
 
-// A warp per item where the sequences have few rows on average, else a block.
-constexpr int kFewRows = 8;
-
-inline bool few_rows(const Kv8Args& a) { return (int64_t)a.T <= (int64_t)kFewRows * a.S; }
+// A warp per item where a block's rows are few, or few of it are written: up to
+// four 16-value pieces a lane.
+inline bool small_items(const Kv8Args& a) {
+  const int64_t rows = ((int64_t)a.T + a.S - 1) / a.S, page = (int64_t)1 << a.page_shift;
+  return (rows < page ? rows : page) * (a.D / 16) <= 128;
+}
+// Blocks of a launch: the items', and one whose threads check the batch's entries.
+inline int64_t blocks_of(int64_t items, bool small) {
+  return (small ? (items + kBlockSmall / 32 - 1) / (kBlockSmall / 32) : items) + 1;
+}
 
 template <typename T>
 cudaError_t append_t(const Kv8Args& a, const void* k, const void* v, int64_t ks, int64_t vs,
@@ -354,15 +383,14 @@ cudaError_t append_t(const Kv8Args& a, const void* k, const void* v, int64_t ks,
   const int64_t items = slots_of(a.S, a.T, a.cu != nullptr, a.page_shift) * a.H_kv * 2;
   const T* kp = static_cast<const T*>(k);
   const T* vp = static_cast<const T*>(v);
-  if (few_rows(a)) {
-    const int64_t blocks = (items + 7) / 8;
-    if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
-    kv8_append_kernel<T, 32><<<(unsigned)blocks, kThreads, 0, stream>>>(a, kp, vp, ks, vs, items);
-  } else {
-    if (items > INT32_MAX) return cudaErrorInvalidConfiguration;
-    kv8_append_kernel<T, kThreads><<<(unsigned)items, kThreads, 0, stream>>>(a, kp, vp, ks, vs,
-                                                                            items);
-  }
+  const bool small = small_items(a);
+  const int64_t blocks = blocks_of(items, small);
+  if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
+  if (small)
+    kv8_append_kernel<T, 32><<<(unsigned)blocks, kBlockSmall, 0, stream>>>(a, kp, vp, ks, vs, items);
+  else
+    kv8_append_kernel<T, kTeamBig><<<(unsigned)blocks, kTeamBig, 0, stream>>>(a, kp, vp, ks, vs,
+                                                                              items);
   return cudaGetLastError();
 }
 
@@ -371,14 +399,13 @@ cudaError_t read_t(const Kv8Args& a, void* k, void* v, cudaStream_t stream) {
   const int64_t items = slots_of(a.S, a.T, a.cu != nullptr, a.page_shift) * a.H_kv * 2;
   T* kp = static_cast<T*>(k);
   T* vp = static_cast<T*>(v);
-  if (few_rows(a)) {
-    const int64_t blocks = (items + 7) / 8;
-    if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
-    kv8_read_kernel<T, 32><<<(unsigned)blocks, kThreads, 0, stream>>>(a, kp, vp, items);
-  } else {
-    if (items > INT32_MAX) return cudaErrorInvalidConfiguration;
-    kv8_read_kernel<T, kThreads><<<(unsigned)items, kThreads, 0, stream>>>(a, kp, vp, items);
-  }
+  const bool small = small_items(a);
+  const int64_t blocks = blocks_of(items, small);
+  if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
+  if (small)
+    kv8_read_kernel<T, 32><<<(unsigned)blocks, kBlockSmall, 0, stream>>>(a, kp, vp, items);
+  else
+    kv8_read_kernel<T, kTeamBig><<<(unsigned)blocks, kTeamBig, 0, stream>>>(a, kp, vp, items);
   return cudaGetLastError();
 }
 

@@ -63,6 +63,13 @@ __device__ __forceinline__ Span unit_span(const Kv8AttnArgs& a, const Dims& d, i
   return u;
 }
 
+// Places of a unit in the batch's order: its granules after its fixed cost, or one
+// where units are not cut.
+template <class Sh>
+__device__ __forceinline__ int unit_places(const Kv8AttnArgs& a, const Span& u) {
+  return a.uncut ? 1 : u.ng + Sh::kCost;
+}
+
 // A worker's range [w0, w1) of the batch's granules (fixed costs included) and
 // where it starts: place c0 of unit (s, m, h).  s < 0: no range.
 struct Range {
@@ -101,14 +108,15 @@ __device__ Range find_range(const Kv8AttnArgs& a, int worker, int workers,
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (a.c.S + kWarps - 1) / kWarps;
   const int s0 = min(a.c.S, warp * per), s1 = min(a.c.S, s0 + per);
+  bool bad = false;  // some sequence's entries make no sense
   // granules of the blocks of sequence s, every KV head
   auto lane_work = [&](const Dims& d) -> int64_t {  // a lane's sequence with one block (or none)
-    return d.nm == 1 ? (int64_t)(unit_span<Sh>(a, d, 0).ng + Sh::kCost) * a.c.H_kv : 0;
+    return d.nm == 1 ? (int64_t)unit_places<Sh>(a, unit_span<Sh>(a, d, 0)) * a.c.H_kv : 0;
   };
   auto warp_work = [&](const Dims& d) -> int64_t {  // the warp's sequence, any number of blocks
-    if (!a.causal) return (int64_t)d.nm * (unit_span<Sh>(a, d, 0).ng + Sh::kCost) * a.c.H_kv;
+    if (!a.causal) return (int64_t)d.nm * unit_places<Sh>(a, unit_span<Sh>(a, d, 0)) * a.c.H_kv;
     int64_t w = 0;
-    for (int m = lane; m < d.nm; m += 32) w += unit_span<Sh>(a, d, m).ng + Sh::kCost;
+    for (int m = lane; m < d.nm; m += 32) w += unit_places<Sh>(a, unit_span<Sh>(a, d, m));
     return warp_total(w) * a.c.H_kv;
   };
   // work of sequence base + lane (0 past s1)
@@ -116,7 +124,10 @@ __device__ Range find_range(const Kv8AttnArgs& a, int worker, int workers,
     const int s = base + lane;
     Dims d;
     d.nm = 0;
-    if (s < s1) d = seq_dims<Sh>(a, s);
+    if (s < s1) {
+      d = seq_dims<Sh>(a, s);
+      bad |= kv8_seq(a.c, s).bad;
+    }
     int64_t w = lane_work(d);
     uint32_t big = __ballot_sync(0xffffffffu, d.nm > 1);
     while (big) {
@@ -133,6 +144,7 @@ __device__ Range find_range(const Kv8AttnArgs& a, int worker, int workers,
     if (b == s0) first = w;
     mine += w;
   }
+  if (bad) set_status(a.c.status, kStatusBadIndex);
   mine = warp_total(mine);
   if (lane == 0) sm.warp_sum[warp] = mine;
   if (tid == 0) sm.s = -1;
@@ -164,7 +176,7 @@ __device__ Range find_range(const Kv8AttnArgs& a, int worker, int workers,
         const Dims d = seq_dims<Sh>(a, s);
         // the block of rows: 32 at a time
         for (int m0 = 0; m0 < d.nm; m0 += 32) {
-          const int ng = m0 + lane < d.nm ? unit_span<Sh>(a, d, m0 + lane).ng + Sh::kCost : 0;
+          const int ng = m0 + lane < d.nm ? unit_places<Sh>(a, unit_span<Sh>(a, d, m0 + lane)) : 0;
           const int64_t x = (int64_t)ng * a.c.H_kv, xi = warp_scan(x, lane);
           const uint32_t pm = __ballot_sync(0xffffffffu, rem < xi);
           if (pm) {
@@ -212,12 +224,12 @@ struct Walk {
     d = seq_dims<Sh>(a, s);
     u = unit_span<Sh>(a, d, m);
     pos = r.w0 - r.c0;
-    return clip(r.c0) || next(a);
+    return clip(a, r.c0) || next(a);
   }
   // To the next unit of the range; false at its end.
   __device__ __forceinline__ bool next(const Kv8AttnArgs& a) {
     while (true) {
-      pos += u.ng + Sh::kCost;
+      pos += unit_places<Sh>(a, u);
       if (pos >= end) return false;
       if (++h == a.c.H_kv) {
         h = 0;
@@ -232,11 +244,16 @@ struct Walk {
           u = unit_span<Sh>(a, d, 0);
         }
       }
-      if (clip(0)) return true;
+      if (clip(a, 0)) return true;
     }
   }
   // The unit's granules from place c0 to the range's end; false if none.
-  __device__ __forceinline__ bool clip(int c0) {
+  __device__ __forceinline__ bool clip(const Kv8AttnArgs& a, int c0) {
+    if (a.uncut) {
+      t0 = 0;
+      t1 = u.ng;
+      return true;
+    }
     t0 = max(0, c0 - Sh::kCost);
     t1 = (int)min((int64_t)u.ng, end - pos - Sh::kCost);
     return t1 > t0;
