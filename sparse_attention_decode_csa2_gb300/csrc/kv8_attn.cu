@@ -92,7 +92,7 @@ __device__ __forceinline__ void copy_wait() {
 }
 
 __device__ __forceinline__ void mma16816(float* c, const uint32_t* x, uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
       "{%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -124,33 +124,50 @@ __device__ __forceinline__ uint2 e4m3x4_to_f16x4(uint32_t x) {
   return r;
 }
 
-// Fragments of 16 rows of Q (this lane: rows row, row + 8 of the unit, where
-// ok): k-step 4 j + i contracts channels 64 j + 16 c + 4 i .. + 3.  bf16 rows are
-// scaled to a largest magnitude in [1, 2); crow: the rows' logit factors.
-template <int D, bool kBf16>
-__device__ __forceinline__ void load_q(const Kv8AttnArgs& a, int row0, int head0, int row, int nrow,
-                                       int c, uint32_t (*qf)[4], float* crow) {
+// 16 rows of Q as loaded: of this lane's rows row, row + 8 (where the unit has
+// them) channels 64 j + 16 c .. + 15.
+template <int D>
+struct QRows {
+  uint4 x[2][D / 64][2];
+};
+template <int D>
+__device__ __forceinline__ QRows<D> fetch_q(const Kv8AttnArgs& a, int row0, int head0, int row,
+                                            int nrow, int c) {
+  QRows<D> q;
 #pragma unroll
   for (int r = 0; r < 2; ++r) {
     const int rr = row + 8 * r;
     const bool ok = rr < nrow;
-    const int tok = (ok ? rr : 0) / a.G, head = head0 + (ok ? rr % a.G : 0);
-    const uint32_t* src = reinterpret_cast<const uint32_t*>(
+    const int tok = (ok ? rr : 0) / a.G, head = head0 + (ok ? rr - tok * a.G : 0);
+    const uint4* src = reinterpret_cast<const uint4*>(
         static_cast<const uint16_t*>(a.q) + (int64_t)(row0 + tok) * a.q_stride + (int64_t)head * D);
+#pragma unroll
+    for (int j = 0; j < D / 64; ++j)
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf)
+        q.x[r][j][hf] = ok ? __ldg(src + 8 * j + 2 * c + hf) : make_uint4(0, 0, 0, 0);
+  }
+  return q;
+}
+// Their fragments: k-step 4 j + i contracts channels 64 j + 16 c + 4 i .. + 3.
+// bf16 rows are scaled to a largest magnitude in [1, 2); crow: the rows' logit
+// factors.
+template <int D, bool kBf16>
+__device__ __forceinline__ void make_q(const QRows<D>& q, float scale, uint32_t (*qf)[4],
+                                       float* crow) {
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
     uint32_t x[D / 64][8];
 #pragma unroll
-    for (int j = 0; j < D / 64; ++j) {
+    for (int j = 0; j < D / 64; ++j)
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
-        const uint4 t = ok ? __ldg(reinterpret_cast<const uint4*>(src + 32 * j + 8 * c + 4 * hf))
-                           : make_uint4(0, 0, 0, 0);
-        x[j][4 * hf] = t.x;
-        x[j][4 * hf + 1] = t.y;
-        x[j][4 * hf + 2] = t.z;
-        x[j][4 * hf + 3] = t.w;
+        x[j][4 * hf] = q.x[r][j][hf].x;
+        x[j][4 * hf + 1] = q.x[r][j][hf].y;
+        x[j][4 * hf + 2] = q.x[r][j][hf].z;
+        x[j][4 * hf + 3] = q.x[r][j][hf].w;
       }
-    }
-    crow[r] = a.scale_log2;
+    crow[r] = scale;
     if (kBf16) {
       float mx = 0.0f;
 #pragma unroll
@@ -205,79 +222,27 @@ kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a) {
   const int wrow = rq * 16 * kMt;              // the warp's first row
   pdl_trigger();
   const Range rg = find_range<typename C::Work, kWarps>(a, blockIdx.x, gridDim.x, rsm);
-  if (rg.s < 0) return;
+  Cut cut{-1, 0, 0, 0};
+  Walk<typename C::Work> w;
+  if (rg.s < 0 || !w.start(a, rg, rsm)) {
+    if (tid == 0) write_cut(a, cut);
+    return;
+  }
 
   uint8_t* ring = smem + kg * (C::stages * C::stage);
   float* ring_scale = reinterpret_cast<float*>(smem + C::ring) + kg * (C::stages * 4);
   uint4* qs = reinterpret_cast<uint4*>(smem + C::ring + C::scales);  // [matrix tile][k-step][lane]
   const uint32_t ring_u = smem_u32(ring), scale_u = smem_u32(ring_scale);
   const int page_mask = (1 << a.c.page_shift) - 1;
-  float* part =
-      reinterpret_cast<float*>(a.scratch) + (size_t)blockIdx.x * 2 * part_floats(C::unit, D);
 
-  Walk<typename C::Work> w;
-  if (!w.start(a, rg)) return;
   do {
     const int i0 = w.first_row(), nrow = w.rows(a.G);
-    // ---- Q ----
-    uint32_t qf[kMt == 1 ? D / 16 : 1][4];
-    float crow[kMt][2];
-    if constexpr (kMt == 1) {
-      load_q<D, kBf16>(a, w.d.row0 + i0, w.h * a.G, wrow + g, nrow, c, qf, crow[0]);
-    } else {
-      if (warp < C::unit / 16) {
-        uint32_t f[D / 16][4];
-        float cr[2];
-        load_q<D, kBf16>(a, w.d.row0 + i0, w.h * a.G, warp * 16 + g, nrow, c, f, cr);
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k)
-          qs[(warp * (D / 16) + k) * 32 + lane] = make_uint4(f[k][0], f[k][1], f[k][2], f[k][3]);
-        if (c == 0) {
-          row_sum[0][warp * 16 + g] = cr[0];
-          row_sum[0][warp * 16 + g + 8] = cr[1];
-        }
-      }
-      __syncthreads();
-#pragma unroll
-      for (int mt = 0; mt < kMt; ++mt) {
-        crow[mt][0] = row_sum[0][wrow + 16 * mt + g];
-        crow[mt][1] = row_sum[0][wrow + 16 * mt + g + 8];
-      }
-      __syncthreads();  // row_sum is written again at the unit's end
-    }
-    // tokens a row sees, and those that every row of the warp sees
-    int rlo[kMt][2], rhi[kMt][2];
-    int all_lo = w.u.lo, all_hi = w.u.hi;
-#pragma unroll
-    for (int mt = 0; mt < kMt; ++mt)
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const int row = wrow + 16 * mt + g + 8 * r;
-        rlo[mt][r] = w.u.lo;
-        rhi[mt][r] = w.u.hi;
-        if (a.causal && row < nrow) {
-          const int64_t p = (int64_t)w.d.len - w.d.n + i0 + row / a.G;
-          rhi[mt][r] = (int)max((int64_t)0, min((int64_t)w.u.hi, p + 1));
-          if (a.window > 0) rlo[mt][r] = (int)max((int64_t)w.u.lo, p - a.window + 1);
-        }
-        all_lo = max(all_lo, rlo[mt][r]);
-        all_hi = min(all_hi, rhi[mt][r]);
-      }
-    all_lo = __reduce_max_sync(0xffffffffu, all_lo);
-    all_hi = __reduce_min_sync(0xffffffffu, all_hi);
-
-    float o[kMt][D / 8][4];
-#pragma unroll
-    for (int mt = 0; mt < kMt; ++mt)
-#pragma unroll
-      for (int i = 0; i < D / 8; ++i) o[mt][i][0] = o[mt][i][1] = o[mt][i][2] = o[mt][i][3] = 0.0f;
-    float mrow[kMt][2], lrow[kMt][2];
-#pragma unroll
-    for (int mt = 0; mt < kMt; ++mt) {
-      mrow[mt][0] = mrow[mt][1] = -INFINITY;
-      lrow[mt][0] = lrow[mt][1] = 0.0f;
-    }
-
+    // the unit's first loads, all in flight together: Q (ahead of the copies, which
+    // fill the memory's queues) and the first tiles' pages
+    QRows<D> qrows;
+    const int qtile = kMt == 1 ? rq : warp;  // the matrix tile of Q that this warp takes
+    if (qtile < C::unit / 16)
+      qrows = fetch_q<D>(a, w.d.row0 + i0, w.h * a.G, qtile * 16 + g, nrow, c);
     const int32_t* table = a.c.table + (int64_t)w.s * a.c.max_pages;
     const int key_first = w.u.g0 * C::granule + kg * kTileKeys;  // of granule 0 of the span
     // page id of this lane's 16-key half of a tile (lanes 0-15, 16-31); -1: nothing
@@ -340,13 +305,74 @@ kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a) {
       copy_commit();
     };
 
-    int pid_next = tile_page(w.t0);
-#pragma unroll 1
-    for (int i = 0; i < C::stages - 1; ++i) {
-      const int pid = pid_next;
-      pid_next = tile_page(w.t0 + i + 1);
-      load_tile(w.t0 + i, i, pid);
+    int pid_next;
+    {
+      int pid[C::stages];
+#pragma unroll
+      for (int i = 0; i < C::stages; ++i) pid[i] = tile_page(w.t0 + i);
+#pragma unroll
+      for (int i = 0; i < C::stages - 1; ++i) load_tile(w.t0 + i, i, pid[i]);
+      pid_next = pid[C::stages - 1];
     }
+    // ---- Q ----
+    uint32_t qf[kMt == 1 ? D / 16 : 1][4];
+    float crow[kMt][2];
+    if constexpr (kMt == 1) {
+      make_q<D, kBf16>(qrows, a.scale_log2, qf, crow[0]);
+    } else {
+      if (warp < C::unit / 16) {
+        uint32_t f[D / 16][4];
+        float cr[2];
+        make_q<D, kBf16>(qrows, a.scale_log2, f, cr);
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k)
+          qs[(warp * (D / 16) + k) * 32 + lane] = make_uint4(f[k][0], f[k][1], f[k][2], f[k][3]);
+        if (c == 0) {
+          row_sum[0][warp * 16 + g] = cr[0];
+          row_sum[0][warp * 16 + g + 8] = cr[1];
+        }
+      }
+      __syncthreads();
+#pragma unroll
+      for (int mt = 0; mt < kMt; ++mt) {
+        crow[mt][0] = row_sum[0][wrow + 16 * mt + g];
+        crow[mt][1] = row_sum[0][wrow + 16 * mt + g + 8];
+      }
+      __syncthreads();  // row_sum is written again at the unit's end
+    }
+    // tokens a row sees, and those that every row of the warp sees
+    int rlo[kMt][2], rhi[kMt][2];
+    int all_lo = w.u.lo, all_hi = w.u.hi;
+#pragma unroll
+    for (int mt = 0; mt < kMt; ++mt)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const int row = wrow + 16 * mt + g + 8 * r;
+        rlo[mt][r] = w.u.lo;
+        rhi[mt][r] = w.u.hi;
+        if (a.causal && row < nrow) {
+          const int64_t p = (int64_t)w.d.len - w.d.n + i0 + row / a.G;
+          rhi[mt][r] = (int)max((int64_t)0, min((int64_t)w.u.hi, p + 1));
+          if (a.window > 0) rlo[mt][r] = (int)max((int64_t)w.u.lo, p - a.window + 1);
+        }
+        all_lo = max(all_lo, rlo[mt][r]);
+        all_hi = min(all_hi, rhi[mt][r]);
+      }
+    all_lo = __reduce_max_sync(0xffffffffu, all_lo);
+    all_hi = __reduce_min_sync(0xffffffffu, all_hi);
+
+    float o[kMt][D / 8][4];
+#pragma unroll
+    for (int mt = 0; mt < kMt; ++mt)
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) o[mt][i][0] = o[mt][i][1] = o[mt][i][2] = o[mt][i][3] = 0.0f;
+    float mrow[kMt][2], lrow[kMt][2];
+#pragma unroll
+    for (int mt = 0; mt < kMt; ++mt) {
+      mrow[mt][0] = mrow[mt][1] = -INFINITY;
+      lrow[mt][0] = lrow[mt][1] = 0.0f;
+    }
+
     int st = 0;
 #pragma unroll 1
     for (int t = w.t0; t < w.t1; ++t) {
@@ -381,13 +407,15 @@ kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a) {
             for (int i = 0; i < 4; ++i)
               qv[mt][i] = qs[((rq * kMt + mt) * (D / 16) + 4 * j + i) * 32 + lane];
         }
+        uint4 b[4];
 #pragma unroll
-        for (int nt = 0; nt < 4; ++nt) {
-          const uint4 b = *reinterpret_cast<const uint4*>(kt + tile_off<D>(key_of(nt, g), 4 * j + c));
-          const uint32_t bw[4] = {b.x, b.y, b.z, b.w};
+        for (int nt = 0; nt < 4; ++nt)
+          b[nt] = *reinterpret_cast<const uint4*>(kt + tile_off<D>(key_of(nt, g), 4 * j + c));
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint2 f = e4m3x4_to_f16x4(bw[i]);
+        for (int i = 0; i < 4; ++i)  // (4 kMt independent products in a row)
+#pragma unroll
+          for (int nt = 0; nt < 4; ++nt) {
+            const uint2 f = e4m3x4_to_f16x4(i == 0 ? b[nt].x : i == 1 ? b[nt].y : i == 2 ? b[nt].z : b[nt].w);
             if constexpr (kMt == 1) {
               mma16816(sc[0][nt], qf[4 * j + i], f.x, f.y);
             } else {
@@ -398,7 +426,6 @@ kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a) {
               }
             }
           }
-        }
       }
       // ---- masks ----
       const bool half0 = bs.z != 0.0f, half1 = bs.w != 0.0f;
@@ -544,7 +571,7 @@ kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a) {
               make_float2(o[mt][i][2 * r] * f, o[mt][i][2 * r + 1] * f);
       }
     __syncthreads();
-    float* pw = part + (w.t0 == 0 ? part_floats(C::unit, D) : 0);
+    float* pw = scratch_part(a, gridDim.x, blockIdx.x, w.t0 == 0, C::unit, D);
     constexpr int kTpr = D / 4;  // threads per row
 #pragma unroll 4
     for (int i = 0; i < C::unit * kTpr / kThreads; ++i) {
@@ -583,7 +610,9 @@ kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a) {
       }
     }
     __syncthreads();  // the buffers are read before the next unit's copies
+    if (w.t0 == 0 && w.t1 < w.u.ng) cut = w.cut(a, rg);
   } while (w.next(a));
+  if (tid == 0) write_cut(a, cut);
 }
 
 template <int D, int kMt, int kRg, bool kBf16>
@@ -594,14 +623,17 @@ kv8_merge_kernel(const __grid_constant__ Kv8AttnArgs a, int workers) {
 }
 
 template <int D, int kMt, int kRg, bool kBf16>
-cudaError_t attn_t(const Kv8AttnArgs& a, cudaStream_t stream) {
+cudaError_t attn_t(const Kv8AttnArgs& args, cudaStream_t stream) {
   using C = Cfg<D, kMt, kRg>;
+  Kv8AttnArgs a = args;
+  a.tpu = C::unit / a.G;
   cudaError_t e = cudaFuncSetAttribute(kv8_attn_kernel<D, kMt, kRg, kBf16>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, C::smem);
   if (e != cudaSuccess) return e;
   const int workers = device_sm_count() * C::ctas;
-  kv8_attn_kernel<D, kMt, kRg, kBf16><<<workers, kThreads, C::smem, stream>>>(a);
-  if ((e = cudaGetLastError()) != cudaSuccess || a.uncut) return e;
+  e = launch_kernel(kv8_attn_kernel<D, kMt, kRg, kBf16>, dim3(workers), dim3(kThreads), C::smem,
+                    stream, /*pdl=*/false, a);
+  if (e != cudaSuccess || a.uncut) return e;
   constexpr int kRowsPer = kThreads / (D / 4);
   return launch_kernel(kv8_merge_kernel<D, kMt, kRg, kBf16>, dim3(workers, C::unit / kRowsPer),
                        dim3(kThreads), 0, stream, /*pdl=*/true, a, workers);
@@ -627,7 +659,7 @@ int64_t mean_rows(int S, int T, int G) {
 size_t kv8_attn_scratch_bytes(int S, int T, int H, int H_kv, int D) {
   if (D != 64 && D != 128) return 0;
   if (mean_rows(S, T, H / H_kv) > 64) return kv8_attn_tc_scratch_bytes(D);
-  return align_up((size_t)device_sm_count() * 3 * 2 * part_floats(64, D) * 4, 256);
+  return align_up(scratch_bytes(device_sm_count() * 3, 64, D), 256);
 }
 
 cudaError_t launch_kv8_attn(const Kv8AttnArgs& args, int type, cudaStream_t stream) {

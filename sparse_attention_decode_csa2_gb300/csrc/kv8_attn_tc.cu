@@ -83,7 +83,6 @@ struct Ctl {
   uint64_t rk_full, rk_empty, rv_full, rv_empty;  // the codes of a tile
   uint64_t q_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_full[2];
   uint64_t done;
-  RangeSmem<kWarps> range;
   Walk<Work> walk[kMmaWarp1 + 1];  // each warp's own (kept out of registers)
   uint32_t tmem;
 };
@@ -240,12 +239,16 @@ kv8_attn_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   int32_t* status = a.c.status;
   pdl_trigger();
-  const Range rg = find_range<Work, kWarps>(a, blockIdx.x, gridDim.x, ctl.range);
-  if (rg.s < 0) return;
+  // (in the loader's space, which is free until the roles part)
+  RangeSmem<kWarps>& rsm = *reinterpret_cast<RangeSmem<kWarps>*>(smem + L::rk);
+  const Range rg = find_range<Work, kWarps>(a, blockIdx.x, gridDim.x, rsm);
   Walk<Work>& w = ctl.walk[min(warp, kMmaWarp1)];
   bool any = false;
-  if (warp <= kMmaWarp1 && lane == 0) any = w.start(a, rg);
-  if (!__syncthreads_or(any)) return;  // the range ends within a unit's fixed cost
+  if (warp <= kMmaWarp1 && lane == 0 && rg.s >= 0) any = w.start(a, rg, rsm);
+  if (!__syncthreads_or(any)) {  // no range, or one that ends within a unit's fixed cost
+    if (tid == 0) write_cut(a, Cut{-1, 0, 0, 0});
+    return;
+  }
 
   if (warp == kMmaWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
@@ -507,8 +510,7 @@ kv8_attn_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
       tc_fence_after();
       // ---- output, or a part of it ----
       const float inv = !whole ? 1.0f : l == 0.0f ? 0.0f : 1.0f / l;  // no visible token: zeros
-      float* part = reinterpret_cast<float*>(a.scratch) +
-                    ((size_t)blockIdx.x * 2 + (t0 == 0 ? 1 : 0)) * part_floats(kUnit, D);
+      float* part = scratch_part(a, gridDim.x, blockIdx.x, t0 == 0, kUnit, D);
 #pragma unroll 1
       for (int i = 0; i < D; i += 32) {
         uint32_t o[32];
@@ -590,10 +592,12 @@ kv8_attn_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
     // lanes 0-7: a 16-key group of the tile each; the first of a page's groups
     // (a run) requests the page's codes
     const int page = 1 << a.c.page_shift, run = min(page, kTileE);
+    Cut cut{-1, 0, 0, 0};
     const uint32_t run_bytes = (uint32_t)(run * D);
     const bool leads = lane < 8 && (16 * lane) % run == 0;
     uint32_t ks_out = 0, vs_out = 0;  // tiles whose K, V have been requested
     do {
+      if (w.t0 == 0 && w.t1 < w.u.ng) cut = w.cut(a, rg);
       const int t1 = w.t1, g0 = w.u.g0, lo = w.u.lo, hi = w.u.hi, h = w.h;
       const int32_t* table = a.c.table + (int64_t)w.s * a.c.max_pages;
       // page of the lane's group in tile j: -1 where no key of its run is seen or the
@@ -650,6 +654,7 @@ kv8_attn_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
         next = find(j + 2);
       }
     } while (alive && warp_next(w, a));
+    if (lane == 0) write_cut(a, cut);
     // no copy is in flight when the CTA ends: the last ones are waited for
     if (ks_out > 0) warp_wait(&ctl.rk_full, (ks_out - 1) & 1u, status);
     if (vs_out > 0) warp_wait(&ctl.rv_full, (vs_out - 1) & 1u, status);
@@ -735,14 +740,17 @@ kv8_merge_tc_kernel(const __grid_constant__ Kv8AttnArgs a, int workers) {
 }
 
 template <int D, bool kBf16>
-cudaError_t attn_tc_t(const Kv8AttnArgs& a, cudaStream_t stream) {
+cudaError_t attn_tc_t(const Kv8AttnArgs& args, cudaStream_t stream) {
   using L = Lay<D>;
+  Kv8AttnArgs a = args;
+  a.tpu = kUnit / a.G;
   cudaError_t e = cudaFuncSetAttribute(kv8_attn_tc_kernel<D, kBf16>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, L::alloc);
   if (e != cudaSuccess) return e;
   const int workers = device_sm_count();
-  kv8_attn_tc_kernel<D, kBf16><<<workers, kThreads, L::alloc, stream>>>(a);
-  if ((e = cudaGetLastError()) != cudaSuccess || a.uncut) return e;
+  e = launch_kernel(kv8_attn_tc_kernel<D, kBf16>, dim3(workers), dim3(kThreads), L::alloc, stream,
+                    /*pdl=*/false, a);
+  if (e != cudaSuccess || a.uncut) return e;
   return launch_kernel(kv8_merge_tc_kernel<D, kBf16>, dim3(workers, 8), dim3(128), 0, stream,
                        /*pdl=*/true, a, workers);
 }
@@ -750,7 +758,7 @@ cudaError_t attn_tc_t(const Kv8AttnArgs& a, cudaStream_t stream) {
 }  // namespace
 
 size_t kv8_attn_tc_scratch_bytes(int D) {
-  return align_up((size_t)device_sm_count() * 2 * part_floats(kUnit, D) * 4, 256);
+  return align_up(scratch_bytes(device_sm_count(), kUnit, D), 256);
 }
 
 cudaError_t launch_kv8_attn_tc(const Kv8AttnArgs& a, int type, cudaStream_t stream) {

@@ -36,8 +36,8 @@ __device__ __forceinline__ Dims seq_dims(const Kv8AttnArgs& a, int s) {
   d.row0 = q.row0;
   d.len = q.len;
   d.cap = (int)min((int64_t)q.len, (int64_t)a.c.max_pages << a.c.page_shift);
-  d.tpu = Sh::kUnit / a.G;
-  d.nm = (q.n + d.tpu - 1) / d.tpu;
+  d.tpu = a.tpu;
+  d.nm = q.n <= d.tpu ? (q.n > 0 ? 1 : 0) : (q.n + d.tpu - 1) / d.tpu;
   return d;
 }
 
@@ -73,8 +73,9 @@ __device__ __forceinline__ int unit_places(const Kv8AttnArgs& a, const Span& u) 
 // A worker's range [w0, w1) of the batch's granules (fixed costs included) and
 // where it starts: place c0 of unit (s, m, h).  s < 0: no range.
 struct Range {
-  int64_t w0, w1, total;
-  int workers;  // workers that have a range (no more than there are granules)
+  int64_t w0, w1;
+  int64_t q;   // every worker has q places, the first r one more
+  int r;
   int s, m, h, c0;
 };
 
@@ -82,7 +83,20 @@ template <int kWarps>
 struct RangeSmem {
   int64_t warp_sum[kWarps];
   int s, m, h, c0;
+  Dims d;
+  Span u;
 };
+
+// (A 64-bit division takes some hundred cycles; the numbers are small but for
+// batches of billions of places.)
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
+// The worker that has place x.
+__device__ __forceinline__ int owner(const Range& r, int64_t x) {
+  const int64_t big = (int64_t)r.r * (r.q + 1);
+  return x < big ? (int)quotient(x, r.q + 1) : r.r + (int)quotient(x - big, r.q);
+}
 
 // Sums one value per lane of each warp; every lane gets the warp's total.
 __device__ __forceinline__ int64_t warp_total(int64_t x) {
@@ -156,13 +170,10 @@ __device__ Range find_range(const Kv8AttnArgs& a, int worker, int workers,
     total += sm.warp_sum[w];
   }
   Range r;
-  r.total = total;
-  r.workers = (int)min((int64_t)workers, total);
-  r.w0 = r.w1 = 0;
-  if (worker < r.workers) {
-    r.w0 = total * worker / r.workers;
-    r.w1 = total * (worker + 1) / r.workers;
-  }
+  r.q = quotient(total, workers);
+  r.r = (int)(total - r.q * workers);
+  r.w0 = worker * r.q + min(worker, r.r);
+  r.w1 = r.w0 + r.q + (worker < r.r ? 1 : 0);
   if (r.w0 < r.w1 && r.w0 >= base && r.w0 < base + mine) {  // this warp's sequences hold w0
     int64_t at = base;
     for (int b = s0; b < s1; b += 32) {
@@ -186,8 +197,10 @@ __device__ Range find_range(const Kv8AttnArgs& a, int worker, int workers,
             if (lane == 0) {
               sm.s = s;
               sm.m = m0 + k;
-              sm.h = (int)(rem / n);
-              sm.c0 = (int)(rem % n);
+              sm.h = (int)quotient(rem, n);
+              sm.c0 = (int)(rem - (int64_t)sm.h * n);
+              sm.d = d;
+              sm.u = unit_span<Sh>(a, d, m0 + k);
             }
             break;
           }
@@ -206,6 +219,15 @@ __device__ Range find_range(const Kv8AttnArgs& a, int worker, int workers,
   return r;
 }
 
+// Scratch: a record for each worker, then its parts of cut units, O [kUnit][D],
+// max [kUnit], sum [kUnit]: [0] a part that continues a unit, [1] one that starts
+// it.  The record of the worker that starts a cut unit says how to join it, so
+// that the merge kernel need not find its way again.
+struct Cut {
+  int last;  // the worker with the unit's last part; -1: this worker starts no cut unit
+  int token, head, rows;  // the unit's first row in q and out, its KV head's first query head
+};
+
 // Walks the units of a range that it has granules of: unit (s, m, h), granules
 // [t0, t1) of its span.
 template <class Sh>
@@ -216,13 +238,15 @@ struct Walk {
   Span u;
 
   // To the range's first unit; false if it has none.
-  __device__ __forceinline__ bool start(const Kv8AttnArgs& a, const Range& r) {
+  template <int kWarps>
+  __device__ __forceinline__ bool start(const Kv8AttnArgs& a, const Range& r,
+                                        const RangeSmem<kWarps>& sm) {
     s = r.s;
     m = r.m;
     h = r.h;
     end = r.w1;
-    d = seq_dims<Sh>(a, s);
-    u = unit_span<Sh>(a, d, m);
+    d = sm.d;
+    u = sm.u;
     pos = r.w0 - r.c0;
     return clip(a, r.c0) || next(a);
   }
@@ -258,6 +282,11 @@ struct Walk {
     t1 = (int)min((int64_t)u.ng, end - pos - Sh::kCost);
     return t1 > t0;
   }
+  // The record of a unit that this range starts and does not end.
+  __device__ __forceinline__ Cut cut(const Kv8AttnArgs& a, const Range& r) const {
+    const int64_t past = pos + unit_places<Sh>(a, u);  // the place behind its last
+    return Cut{owner(r, past - 1), d.row0 + first_row(), h * a.G, rows(a.G)};
+  }
   __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == u.ng; }
   __device__ __forceinline__ int first_row() const { return m * d.tpu; }  // its first token's row
   __device__ __forceinline__ int rows(int G) const {
@@ -265,10 +294,22 @@ struct Walk {
   }
 };
 
-// A part of a cut unit in scratch: O [kUnit][D], max [kUnit], sum [kUnit].  A
-// worker has two: [0] a part that continues a unit, [1] one that starts it.
 __host__ __device__ constexpr size_t part_floats(int unit, int D) {
   return (size_t)unit * D + 2 * (size_t)unit;
+}
+__host__ __device__ inline size_t scratch_bytes(int workers, int unit, int D) {
+  return align_up((size_t)workers * sizeof(Cut), 256) + (size_t)workers * 2 * part_floats(unit, D) * 4;
+}
+__device__ __forceinline__ float* scratch_part(const Kv8AttnArgs& a, int workers, int worker,
+                                               bool starts, int unit, int D) {
+  return reinterpret_cast<float*>(a.scratch + align_up((size_t)workers * sizeof(Cut), 256)) +
+         ((size_t)worker * 2 + (starts ? 1 : 0)) * part_floats(unit, D);
+}
+// One thread of a worker, once.
+__device__ __forceinline__ void write_cut(const Kv8AttnArgs& a, const Cut& c) {
+  if (!a.uncut)
+    *reinterpret_cast<int4*>(a.scratch + (size_t)blockIdx.x * sizeof(Cut)) =
+        make_int4(c.last, c.token, c.head, c.rows);
 }
 
 // 2^x by the hardware's approximation (relative error about 2^-22); results
@@ -303,36 +344,21 @@ __device__ __forceinline__ int row_exponent(float mx) {
   return mx > 0.0f ? max(-126, min(126, E)) : 0;
 }
 
-// Joins the parts of the cut units: block (x, y) takes the unit whose first
-// part ends worker x's range, every gridDim.y-th group of its rows.  The
-// ranges depend on kv_len and cu alone, which were there before the kernel
-// whose parts are joined: only the parts are waited for.
+// Joins the parts of the cut units: block (x, y) takes the unit that worker x
+// starts, every gridDim.y-th group of its rows.
 template <class Sh, int kWarps, int D, bool kBf16>
 __device__ __forceinline__ void merge_parts(const Kv8AttnArgs& a, int workers, float headroom) {
-  __shared__ RangeSmem<kWarps> rsm;
-  constexpr int kUnit = Sh::kUnit;
-  const Range rg = find_range<Sh, kWarps>(a, blockIdx.x, workers, rsm);
-  Walk<Sh> w;
-  bool cut = rg.s >= 0 && w.start(a, rg);
-  if (cut)  // only the range's last unit can be cut at its end
-    while (!(cut = w.t0 == 0 && w.t1 < w.u.ng) && w.next(a)) {
-    }
+  constexpr int kUnit = Sh::kUnit, kTpr = D / 4, kRowsPer = kWarps * 32 / kTpr;
   pdl_wait();
-  if (!cut) return;  // none is, or it began before this worker
-  // the unit's parts are those of the workers up to the one that has its last granule
-  const int64_t end = w.pos + Sh::kCost + w.u.ng;
-  const int last = (int)((end * rg.workers - 1) / rg.total);
-  constexpr int kTpr = D / 4, kRowsPer = kWarps * 32 / kTpr;
-  const float* base = reinterpret_cast<const float*>(a.scratch);
-  const size_t pf = part_floats(kUnit, D);
-  const int ch = (threadIdx.x % kTpr) * 4, nrow = w.rows(a.G);
+  const int4 cut = __ldcg(reinterpret_cast<const int4*>(a.scratch) + blockIdx.x);
+  const int last = cut.x, ch = (threadIdx.x % kTpr) * 4, nrow = last < 0 ? 0 : cut.w;
   for (int row = blockIdx.y * kRowsPer + threadIdx.x / kTpr; row < nrow;
        row += gridDim.y * kRowsPer) {
     float m = -INFINITY, l = 0.0f;
     float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 4
     for (int p = blockIdx.x; p <= last; ++p) {
-      const float* src = base + ((size_t)p * 2 + (p == (int)blockIdx.x ? 1 : 0)) * pf;
+      const float* src = scratch_part(a, workers, p, p == (int)blockIdx.x, kUnit, D);
       const float pm = __ldcg(src + kUnit * D + row), pl = __ldcg(src + kUnit * D + kUnit + row);
       const float4 y = __ldcg(reinterpret_cast<const float4*>(src + (size_t)row * D + ch));
       const float nm = fmaxf(m, pm), z = nm == -INFINITY ? 0.0f : nm;
@@ -345,8 +371,7 @@ __device__ __forceinline__ void merge_parts(const Kv8AttnArgs& a, int workers, f
       x.w = x.w * f0 + y.w * f1;
     }
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;  // no visible token: zeros
-    const int64_t orow =
-        (int64_t)(w.d.row0 + w.first_row() + row / a.G) * a.H + w.h * a.G + row % a.G;
+    const int64_t orow = (int64_t)(cut.y + row / a.G) * a.H + cut.z + row % a.G;
     *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + orow * D + ch) =
         make_uint2(pair_from_floats<kBf16>(x.x * inv, x.y * inv),
                    pair_from_floats<kBf16>(x.z * inv, x.w * inv));
