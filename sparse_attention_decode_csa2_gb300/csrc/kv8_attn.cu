@@ -70,7 +70,9 @@ struct Cfg {
   static constexpr int q = kMt > 1 ? unit * D * 2 : 0;
   static constexpr int smem = ring + scales + q;
   static constexpr int ctas = D == 64 && kMt == 1 ? 3 : 2;  // per SM
-  static_assert(ring >= kgs * unit * D * 4, "the join of the key groups reuses the ring");
+  // the join of the key groups uses kMt * kRg stages of each ring, the next unit's
+  // first tiles the others
+  static_assert(kMt * kRg * stage == unit * D * 4 && kMt * kRg < stages, "join");
 };
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
@@ -215,19 +217,17 @@ kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a) {
   using C = Cfg<D, kMt, kRg>;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ RangeSmem<kWarps> rsm;
-  __shared__ float row_max[C::kgs][C::unit], row_sum[C::kgs][C::unit];
+  __shared__ float row_max[C::kgs][C::unit], row_sum[C::kgs][C::unit], row_c[C::unit];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, c = lane & 3;
   const int kg = warp / kRg, rq = warp % kRg;  // key group, row group
   const int wrow = rq * 16 * kMt;              // the warp's first row
   pdl_trigger();
   const Range rg = find_range<typename C::Work, kWarps>(a, blockIdx.x, gridDim.x, rsm);
-  Cut cut{-1, 0, 0, 0};
-  Walk<typename C::Work> w;
-  if (rg.s < 0 || !w.start(a, rg, rsm)) {
-    if (tid == 0) write_cut(a, cut);
-    return;
-  }
+  if (tid == 0) write_cut(a, Cut{-1, 0, 0, 0});
+  __shared__ Walk<typename C::Work> walks[kWarps];
+  Walk<typename C::Work>& w = walks[warp];
+  if (!warp_start(w, a, rg, rsm)) return;
 
   uint8_t* ring = smem + kg * (C::stages * C::stage);
   float* ring_scale = reinterpret_cast<float*>(smem + C::ring) + kg * (C::stages * 4);
@@ -235,42 +235,43 @@ kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a) {
   const uint32_t ring_u = smem_u32(ring), scale_u = smem_u32(ring_scale);
   const int page_mask = (1 << a.c.page_shift) - 1;
 
-  do {
-    const int i0 = w.first_row(), nrow = w.rows(a.G);
-    // the unit's first loads, all in flight together: Q (ahead of the copies, which
-    // fill the memory's queues) and the first tiles' pages
-    QRows<D> qrows;
-    const int qtile = kMt == 1 ? rq : warp;  // the matrix tile of Q that this warp takes
-    if (qtile < C::unit / 16)
-      qrows = fetch_q<D>(a, w.d.row0 + i0, w.h * a.G, qtile * 16 + g, nrow, c);
-    const int32_t* table = a.c.table + (int64_t)w.s * a.c.max_pages;
-    const int key_first = w.u.g0 * C::granule + kg * kTileKeys;  // of granule 0 of the span
-    // page id of this lane's 16-key half of a tile (lanes 0-15, 16-31); -1: nothing
-    // of the half is seen, or the entry is outside the cache
-    auto tile_page = [&](int t) -> int {
-      const int key = key_first + t * C::granule + (lane & 16);
-      int p = -1;
-      if (t < w.t1 && key < w.u.hi && key + 16 > w.u.lo) {
-        p = table[key >> a.c.page_shift];
-        if (p < 0 || p >= a.c.n_pages) {
-          set_status(a.c.status, kStatusBadIndex);
-          p = -1;
-        }
+  // ---- the unit's tiles: pages, copies ----
+  constexpr int kJoin = kMt * kRg;  // stages of each ring that the join of the key groups uses
+  const int32_t* table;
+  int key_first;                    // the key group's first key of granule 0 of the span
+  int issue, slot = 0;              // the next tile to request (of the unit's), its stage
+  int pids, pids_next;              // pages of the requested block of 16 tiles and of the next
+  // page ids of tiles i .. i + 15 of the unit's: lane l has tile i + l % 16, its
+  // 16-key half l / 16; -1: nothing of the half is seen, or the entry is outside the cache
+  auto pages = [&](int i) -> int {
+    const int t = w.t0 + i + (lane & 15), key = key_first + t * C::granule + (lane & 16);
+    int p = -1;
+    if (t < w.t1 && key < w.u.hi && key + 16 > w.u.lo) {
+      p = table[key >> a.c.page_shift];
+      if (p < 0 || p >= a.c.n_pages) {
+        set_status(a.c.status, kStatusBadIndex);
+        p = -1;
       }
-      return p;
-    };
-    // A tile's copies into stage st.  A half is 16 * D contiguous bytes of a page;
-    // with two warps a group each takes a half.
-    auto load_tile = [&](int t, int st, int pid) {
-      constexpr int kCh = D / 16, kPerIt = 32 / kCh;  // chunks a key, keys an instruction
-      constexpr int kIts = 16 / kPerIt;               // instructions a half
+    }
+    return p;
+  };
+  // Requests the unit's next tile (an empty group of copies past its last).  A half
+  // is 16 * D contiguous bytes of a page; with two warps a group each takes a half.
+  auto request = [&]() {
+    constexpr int kCh = D / 16, kPerIt = 32 / kCh;  // chunks a key, keys an instruction
+    constexpr int kIts = 16 / kPerIt;               // instructions a half
+    if ((issue & 15) == 0 && issue > 0) {
+      pids = pids_next;
+      pids_next = pages(issue + 16);
+    }
+    const int t = w.t0 + issue;
+    if (t < w.t1) {
       const int key0 = key_first + t * C::granule;
-      const uint32_t kd = ring_u + st * C::stage, vd = kd + C::tile;
+      const uint32_t kd = ring_u + slot * C::stage, vd = kd + C::tile;
 #pragma unroll
       for (int i = 0; i < 2 / kRg; ++i) {
         const int hf = kRg == 1 ? i : rq;
-        const int p = __shfl_sync(0xffffffffu, pid, 16 * hf);
-        if (t >= w.t1) continue;
+        const int p = __shfl_sync(0xffffffffu, pids, (issue & 15) + 16 * hf);
         const int first = key0 + 16 * hf;
         const int64_t off =
             ((((int64_t)max(p, 0) * a.c.H_kv + w.h) << a.c.page_shift) + (first & page_mask)) * D +
@@ -295,25 +296,41 @@ kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a) {
         }
       }
       if (rq == 0) {  // ks of half 0, 1, vs of half 0, 1 (zeros: no page)
-        const int p = __shfl_sync(0xffffffffu, pid, (lane & 1) * 16);
-        if (lane < 4 && t < w.t1)
-          copy4(scale_u + (st * 4 + lane) * 4,
+        const int p = __shfl_sync(0xffffffffu, pids, (issue & 15) + (lane & 1) * 16);
+        if (lane < 4)
+          copy4(scale_u + (slot * 4 + lane) * 4,
                 ((lane & 2) ? a.c.v_scale : a.c.k_scale) +
                     (p >= 0 ? (int64_t)p * a.c.H_kv + w.h : 0),
                 p >= 0);
       }
-      copy_commit();
-    };
-
-    int pid_next;
-    {
-      int pid[C::stages];
-#pragma unroll
-      for (int i = 0; i < C::stages; ++i) pid[i] = tile_page(w.t0 + i);
-#pragma unroll
-      for (int i = 0; i < C::stages - 1; ++i) load_tile(w.t0 + i, i, pid[i]);
-      pid_next = pid[C::stages - 1];
     }
+    copy_commit();
+    ++issue;
+    if (++slot == C::stages) slot = 0;
+  };
+  auto open_unit = [&]() {
+    table = a.c.table + (int64_t)w.s * a.c.max_pages;
+    key_first = w.u.g0 * C::granule + kg * kTileKeys;
+    issue = 0;
+    pids = pages(0);
+    pids_next = pages(16);
+  };
+  const int qtile = kMt == 1 ? rq : warp;  // the matrix tile of Q that this warp takes
+  QRows<D> qrows;
+  auto fetch = [&]() {
+    if (qtile < C::unit / 16)
+      qrows = fetch_q<D>(a, w.d.row0 + w.first_row(), w.h * a.G, qtile * 16 + g, w.rows(a.G), c);
+  };
+
+  // the unit's first loads, all in flight together: Q ahead of the copies, which
+  // fill the memory's queues
+  fetch();
+  open_unit();
+#pragma unroll 1
+  for (int i = 0; i < C::stages - 1; ++i) request();
+  int st = 0;
+  while (true) {
+    const int i0 = w.first_row(), nrow = w.rows(a.G);
     // ---- Q ----
     uint32_t qf[kMt == 1 ? D / 16 : 1][4];
     float crow[kMt][2];
@@ -328,35 +345,31 @@ kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a) {
         for (int k = 0; k < D / 16; ++k)
           qs[(warp * (D / 16) + k) * 32 + lane] = make_uint4(f[k][0], f[k][1], f[k][2], f[k][3]);
         if (c == 0) {
-          row_sum[0][warp * 16 + g] = cr[0];
-          row_sum[0][warp * 16 + g + 8] = cr[1];
+          row_c[warp * 16 + g] = cr[0];
+          row_c[warp * 16 + g + 8] = cr[1];
         }
       }
       __syncthreads();
 #pragma unroll
       for (int mt = 0; mt < kMt; ++mt) {
-        crow[mt][0] = row_sum[0][wrow + 16 * mt + g];
-        crow[mt][1] = row_sum[0][wrow + 16 * mt + g + 8];
+        crow[mt][0] = row_c[wrow + 16 * mt + g];
+        crow[mt][1] = row_c[wrow + 16 * mt + g + 8];
       }
-      __syncthreads();  // row_sum is written again at the unit's end
     }
-    // tokens a row sees, and those that every row of the warp sees
-    int rlo[kMt][2], rhi[kMt][2];
+    // each row's token (rows that the unit does not have: its first row's), and the
+    // tokens [all_lo, all_hi) that every row of the warp sees
+    int rpos[kMt][2];
     int all_lo = w.u.lo, all_hi = w.u.hi;
 #pragma unroll
     for (int mt = 0; mt < kMt; ++mt)
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         const int row = wrow + 16 * mt + g + 8 * r;
-        rlo[mt][r] = w.u.lo;
-        rhi[mt][r] = w.u.hi;
-        if (a.causal && row < nrow) {
-          const int64_t p = (int64_t)w.d.len - w.d.n + i0 + row / a.G;
-          rhi[mt][r] = (int)max((int64_t)0, min((int64_t)w.u.hi, p + 1));
-          if (a.window > 0) rlo[mt][r] = (int)max((int64_t)w.u.lo, p - a.window + 1);
+        rpos[mt][r] = w.d.len - w.d.n + i0 + (row < nrow ? row / a.G : 0);
+        if (a.causal) {
+          all_hi = min(all_hi, rpos[mt][r] + 1);
+          if (a.window > 0) all_lo = max(all_lo, rpos[mt][r] - a.window + 1);
         }
-        all_lo = max(all_lo, rlo[mt][r]);
-        all_hi = min(all_hi, rhi[mt][r]);
       }
     all_lo = __reduce_max_sync(0xffffffffu, all_lo);
     all_hi = __reduce_min_sync(0xffffffffu, all_hi);
@@ -373,18 +386,13 @@ kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a) {
       lrow[mt][0] = lrow[mt][1] = 0.0f;
     }
 
-    int st = 0;
 #pragma unroll 1
     for (int t = w.t0; t < w.t1; ++t) {
       copy_wait<C::stages - 2>();
       // the group's copies of tile t are there, and it is done with tile t - 1,
       // whose stage takes the next copies
       group_sync<kRg>(kg);
-      {
-        const int pid = pid_next;
-        pid_next = tile_page(t + C::stages);
-        load_tile(t + C::stages - 1, st == 0 ? C::stages - 1 : st - 1, pid);
-      }
+      request();
       const float4 bs = *reinterpret_cast<const float4*>(ring_scale + st * 4);
       const uint8_t* kt = ring + st * C::stage;
       const uint32_t vt = ring_u + st * C::stage + C::tile;
@@ -436,8 +444,9 @@ kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a) {
           for (int nt = 0; nt < 4; ++nt)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const int key = key0 + key_of(nt, 2 * c + (e & 1));
-              if (key < rlo[mt][e >> 1] || key >= rhi[mt][e >> 1] || !(nt < 2 ? half0 : half1))
+              const int key = key0 + key_of(nt, 2 * c + (e & 1)), pos = rpos[mt][e >> 1];
+              if (key < w.u.lo || key >= w.u.hi || (a.causal && key > pos) ||
+                  (a.window > 0 && key <= pos - a.window) || !(nt < 2 ? half0 : half1))
                 sc[mt][nt][e] = -INFINITY;
             }
       }
@@ -540,42 +549,47 @@ kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a) {
       }
     }
     copy_wait<0>();
+    group_sync<kRg>(kg);  // the group is done with its ring
+
+    // ---- the next unit's first tiles, into the stages that the join leaves ----
+    const bool whole = w.whole(), starts = w.t0 == 0;
+    const int token0 = w.d.row0 + i0, head0 = w.h * a.G;
+    if (starts && !whole && tid == 0) write_cut(a, w.cut(a, rg));
+    const bool more = warp_next(w, a);
+    if (more) {
+      open_unit();
+      slot = st = kJoin;
+#pragma unroll 1
+      for (int i = 0; i < min(C::stages - kJoin, C::stages - 1); ++i) request();
+    }
 
     // ---- join the key groups ----
+    float* obuf = reinterpret_cast<float*>(ring);  // [row][D], of each key group
 #pragma unroll
     for (int mt = 0; mt < kMt; ++mt)
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         lrow[mt][r] += __shfl_xor_sync(0xffffffffu, lrow[mt][r], 1);
         lrow[mt][r] += __shfl_xor_sync(0xffffffffu, lrow[mt][r], 2);
-        if (c == 0) {
-          row_max[kg][wrow + 16 * mt + g + 8 * r] = mrow[mt][r];
-          row_sum[kg][wrow + 16 * mt + g + 8 * r] = lrow[mt][r];
-        }
-      }
-    __syncthreads();  // every warp is done with its ring
-    float* obuf = reinterpret_cast<float*>(smem);  // [key group][row][D]
-#pragma unroll
-    for (int mt = 0; mt < kMt; ++mt)
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
         const int row = wrow + 16 * mt + g + 8 * r;
-        float m = row_max[0][row];
+        if (c == 0) {
+          row_max[kg][row] = mrow[mt][r];
+          row_sum[kg][row] = lrow[mt][r];
+        }
+        float* dst = obuf + (size_t)row * D + 2 * c;
 #pragma unroll
-        for (int i = 1; i < C::kgs; ++i) m = fmaxf(m, row_max[i][row]);
-        const float f = ex2(mrow[mt][r] - (m == -INFINITY ? 0.0f : m));
-        float* dst = obuf + ((size_t)kg * C::unit + row) * D + 2 * c;
-#pragma unroll
-        for (int i = 0; i < D / 8; ++i)
-          *reinterpret_cast<float2*>(dst + 8 * i) =
-              make_float2(o[mt][i][2 * r] * f, o[mt][i][2 * r + 1] * f);
+        for (int i = 0; i < D / 8; ++i)  // (8-channel blocks exclusive-or'ed with the row: other banks)
+          *reinterpret_cast<float2*>(dst + 8 * (i ^ (row & 3))) =
+              make_float2(o[mt][i][2 * r], o[mt][i][2 * r + 1]);
       }
+    if (more) fetch();
     __syncthreads();
-    float* pw = scratch_part(a, gridDim.x, blockIdx.x, w.t0 == 0, C::unit, D);
+    float* pw = scratch_part(a, gridDim.x, blockIdx.x, starts, C::unit, D);
     constexpr int kTpr = D / 4;  // threads per row
 #pragma unroll 4
     for (int i = 0; i < C::unit * kTpr / kThreads; ++i) {
       const int row = (i * kThreads + tid) / kTpr, ch = (tid % kTpr) * 4;
+      if (row >= nrow) continue;
       float m = row_max[0][row];
 #pragma unroll
       for (int q = 1; q < C::kgs; ++q) m = fmaxf(m, row_max[q][row]);
@@ -584,18 +598,18 @@ kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a) {
       float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
       for (int q = 0; q < C::kgs; ++q) {
-        l = fmaf(row_sum[q][row], ex2(row_max[q][row] - mz), l);
-        const float4 y =
-            *reinterpret_cast<const float4*>(obuf + ((size_t)q * C::unit + row) * D + ch);
-        x.x += y.x;
-        x.y += y.y;
-        x.z += y.z;
-        x.w += y.w;
+        const float f = ex2(row_max[q][row] - mz);
+        l = fmaf(row_sum[q][row], f, l);
+        const float4 y = *reinterpret_cast<const float4*>(
+            smem + q * (C::stages * C::stage) + ((size_t)row * D + (ch ^ ((row & 3) * 8))) * 4);
+        x.x = fmaf(y.x, f, x.x);
+        x.y = fmaf(y.y, f, x.y);
+        x.z = fmaf(y.z, f, x.z);
+        x.w = fmaf(y.w, f, x.w);
       }
-      if (row >= nrow) continue;
-      if (w.whole()) {
+      if (whole) {
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;  // no visible token: zeros
-        const int64_t orow = (int64_t)(w.d.row0 + i0 + row / a.G) * a.H + w.h * a.G + row % a.G;
+        const int64_t orow = (int64_t)(token0 + row / a.G) * a.H + head0 + row % a.G;
         *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + orow * D + ch) =
             make_uint2(pair_from_floats<kBf16>(x.x * inv, x.y * inv),
                        pair_from_floats<kBf16>(x.z * inv, x.w * inv));
@@ -609,10 +623,11 @@ kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a) {
         }
       }
     }
-    __syncthreads();  // the buffers are read before the next unit's copies
-    if (w.t0 == 0 && w.t1 < w.u.ng) cut = w.cut(a, rg);
-  } while (w.next(a));
-  if (tid == 0) write_cut(a, cut);
+    if (!more) break;
+    __syncthreads();  // the joined stages may be written again
+#pragma unroll 1
+    for (int i = min(C::stages - kJoin, C::stages - 1); i < C::stages - 1; ++i) request();
+  }
 }
 
 template <int D, int kMt, int kRg, bool kBf16>

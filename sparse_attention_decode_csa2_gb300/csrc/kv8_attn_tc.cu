@@ -92,16 +92,6 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int32_
   return __all_sync(0xffffffffu, mbar_wait(su32(bar), parity, status));
 }
 
-// The warp's walk to its next unit (one lane moves it).
-__device__ __forceinline__ bool warp_next(Walk<Work>& w, const Kv8AttnArgs& a) {
-  __syncwarp();
-  bool more = false;
-  if ((threadIdx.x & 31) == 0) more = w.next(a);
-  more = __shfl_sync(0xffffffffu, more, 0);
-  __syncwarp();
-  return more;
-}
-
 template <int kRegs>
 __device__ __forceinline__ void more_registers() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
@@ -244,7 +234,7 @@ kv8_attn_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
   const Range rg = find_range<Work, kWarps>(a, blockIdx.x, gridDim.x, rsm);
   Walk<Work>& w = ctl.walk[min(warp, kMmaWarp1)];
   bool any = false;
-  if (warp <= kMmaWarp1 && lane == 0 && rg.s >= 0) any = w.start(a, rg, rsm);
+  if (warp <= kMmaWarp1) any = warp_start(w, a, rg, rsm);
   if (!__syncthreads_or(any)) {  // no range, or one that ends within a unit's fixed cost
     if (tid == 0) write_cut(a, Cut{-1, 0, 0, 0});
     return;
@@ -592,12 +582,12 @@ kv8_attn_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
     // lanes 0-7: a 16-key group of the tile each; the first of a page's groups
     // (a run) requests the page's codes
     const int page = 1 << a.c.page_shift, run = min(page, kTileE);
-    Cut cut{-1, 0, 0, 0};
+    if (lane == 0) write_cut(a, Cut{-1, 0, 0, 0});
     const uint32_t run_bytes = (uint32_t)(run * D);
     const bool leads = lane < 8 && (16 * lane) % run == 0;
     uint32_t ks_out = 0, vs_out = 0;  // tiles whose K, V have been requested
     do {
-      if (w.t0 == 0 && w.t1 < w.u.ng) cut = w.cut(a, rg);
+      if (w.t0 == 0 && w.t1 < w.u.ng && lane == 0) write_cut(a, w.cut(a, rg));
       const int t1 = w.t1, g0 = w.u.g0, lo = w.u.lo, hi = w.u.hi, h = w.h;
       const int32_t* table = a.c.table + (int64_t)w.s * a.c.max_pages;
       // page of the lane's group in tile j: -1 where no key of its run is seen or the
@@ -654,7 +644,6 @@ kv8_attn_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
         next = find(j + 2);
       }
     } while (alive && warp_next(w, a));
-    if (lane == 0) write_cut(a, cut);
     // no copy is in flight when the CTA ends: the last ones are waited for
     if (ks_out > 0) warp_wait(&ctl.rk_full, (ks_out - 1) & 1u, status);
     if (vs_out > 0) warp_wait(&ctl.rv_full, (vs_out - 1) & 1u, status);

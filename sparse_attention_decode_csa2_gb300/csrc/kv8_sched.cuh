@@ -305,11 +305,31 @@ __device__ __forceinline__ float* scratch_part(const Kv8AttnArgs& a, int workers
   return reinterpret_cast<float*>(a.scratch + align_up((size_t)workers * sizeof(Cut), 256)) +
          ((size_t)worker * 2 + (starts ? 1 : 0)) * part_floats(unit, D);
 }
-// One thread of a worker, once.
+// One thread of a worker (first a record without a unit, then the unit it starts).
 __device__ __forceinline__ void write_cut(const Kv8AttnArgs& a, const Cut& c) {
   if (!a.uncut)
     *reinterpret_cast<int4*>(a.scratch + (size_t)blockIdx.x * sizeof(Cut)) =
         make_int4(c.last, c.token, c.head, c.rows);
+}
+
+// A warp's walk in shared memory (kept out of registers): one lane moves it.
+template <class Sh, int kWarps>
+__device__ __forceinline__ bool warp_start(Walk<Sh>& w, const Kv8AttnArgs& a, const Range& r,
+                                           const RangeSmem<kWarps>& sm) {
+  bool any = false;
+  if ((threadIdx.x & 31) == 0 && r.s >= 0) any = w.start(a, r, sm);
+  any = __shfl_sync(0xffffffffu, any, 0);
+  __syncwarp();
+  return any;
+}
+template <class Sh>
+__device__ __forceinline__ bool warp_next(Walk<Sh>& w, const Kv8AttnArgs& a) {
+  __syncwarp();
+  bool more = false;
+  if ((threadIdx.x & 31) == 0) more = w.next(a);
+  more = __shfl_sync(0xffffffffu, more, 0);
+  __syncwarp();
+  return more;
 }
 
 // 2^x by the hardware's approximation (relative error about 2^-22); results
