@@ -587,6 +587,8 @@ csa2_status csa2_kv8_attn(const void* q, int type, int64_t q_stride, int H,
   a.causal = causal ? 1 : 0;
   a.window = window;
   a.uncut = 0;
+  a.tpu = 0;
+  a.g_inv = (65536 + a.G - 1) / a.G;
   a.scale_log2 = softmax_scale * 1.44269504088896340736f;
   a.scratch = reinterpret_cast<uint8_t*>(ws) + kStatusBytes;
   return check_launch(launch_kv8_attn(a, type, stream));

@@ -88,6 +88,7 @@ struct Kv8AttnArgs {
   void* out;           // [T][H][D], q's type
   float* lse;          // [T][H] or null
   int H, G, causal, window;
+  int g_inv;           // ceil(2^16 / G)
   int tpu;             // tokens of a unit's rows (the kernel's rows a unit / G)
   int uncut;           // every unit is one worker's: no parts, no merge kernel
   float scale_log2;    // softmax scale * log2(e)

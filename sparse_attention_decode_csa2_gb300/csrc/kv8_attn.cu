@@ -140,7 +140,7 @@ __device__ __forceinline__ QRows<D> fetch_q(const Kv8AttnArgs& a, int row0, int 
   for (int r = 0; r < 2; ++r) {
     const int rr = row + 8 * r;
     const bool ok = rr < nrow;
-    const int tok = (ok ? rr : 0) / a.G, head = head0 + (ok ? rr - tok * a.G : 0);
+    const int tok = over_g(a, ok ? rr : 0), head = head0 + (ok ? rr - tok * a.G : 0);
     const uint4* src = reinterpret_cast<const uint4*>(
         static_cast<const uint16_t*>(a.q) + (int64_t)(row0 + tok) * a.q_stride + (int64_t)head * D);
 #pragma unroll
@@ -225,8 +225,9 @@ kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a) {
   pdl_trigger();
   const Range rg = find_range<typename C::Work, kWarps>(a, blockIdx.x, gridDim.x, rsm);
   if (tid == 0) write_cut(a, Cut{-1, 0, 0, 0});
-  __shared__ Walk<typename C::Work> walks[kWarps];
-  Walk<typename C::Work>& w = walks[warp];
+  __shared__ Walk<typename C::Work> walks[kWarps][2];  // of the unit, and of the next
+  Walk<typename C::Work>& w = walks[warp][0];
+  Walk<typename C::Work>& ahead = walks[warp][1];
   if (!warp_start(w, a, rg, rsm)) return;
 
   uint8_t* ring = smem + kg * (C::stages * C::stage);
@@ -237,17 +238,17 @@ kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a) {
 
   // ---- the unit's tiles: pages, copies ----
   constexpr int kJoin = kMt * kRg;  // stages of each ring that the join of the key groups uses
-  const int32_t* table;
   int key_first;                    // the key group's first key of granule 0 of the span
-  int issue, slot = 0;              // the next tile to request (of the unit's), its stage
+  int issue = 0, slot = 0;            // the next tile to request (of the unit's), its stage
   int pids, pids_next;              // pages of the requested block of 16 tiles and of the next
   // page ids of tiles i .. i + 15 of the unit's: lane l has tile i + l % 16, its
   // 16-key half l / 16; -1: nothing of the half is seen, or the entry is outside the cache
-  auto pages = [&](int i) -> int {
-    const int t = w.t0 + i + (lane & 15), key = key_first + t * C::granule + (lane & 16);
+  auto pages = [&](const Walk<typename C::Work>& u, int i) -> int {
+    const int t = u.t0 + i + (lane & 15);
+    const int key = (u.u.g0 + t) * C::granule + kg * kTileKeys + (lane & 16);
     int p = -1;
-    if (t < w.t1 && key < w.u.hi && key + 16 > w.u.lo) {
-      p = table[key >> a.c.page_shift];
+    if (t < u.t1 && key < u.u.hi && key + 16 > u.u.lo) {
+      p = a.c.table[(int64_t)u.s * a.c.max_pages + (key >> a.c.page_shift)];
       if (p < 0 || p >= a.c.n_pages) {
         set_status(a.c.status, kStatusBadIndex);
         p = -1;
@@ -262,7 +263,7 @@ kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a) {
     constexpr int kIts = 16 / kPerIt;               // instructions a half
     if ((issue & 15) == 0 && issue > 0) {
       pids = pids_next;
-      pids_next = pages(issue + 16);
+      pids_next = pages(w, issue + 16);
     }
     const int t = w.t0 + issue;
     if (t < w.t1) {
@@ -308,12 +309,11 @@ kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a) {
     ++issue;
     if (++slot == C::stages) slot = 0;
   };
-  auto open_unit = [&]() {
-    table = a.c.table + (int64_t)w.s * a.c.max_pages;
+  auto open_unit = [&](int first_pages) {
     key_first = w.u.g0 * C::granule + kg * kTileKeys;
     issue = 0;
-    pids = pages(0);
-    pids_next = pages(16);
+    pids = first_pages;
+    pids_next = pages(w, 16);
   };
   const int qtile = kMt == 1 ? rq : warp;  // the matrix tile of Q that this warp takes
   QRows<D> qrows;
@@ -325,11 +325,15 @@ kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a) {
   // the unit's first loads, all in flight together: Q ahead of the copies, which
   // fill the memory's queues
   fetch();
-  open_unit();
+  open_unit(pages(w, 0));
 #pragma unroll 1
   for (int i = 0; i < C::stages - 1; ++i) request();
   int st = 0;
   while (true) {
+    // the next unit and its first pages, while this one's tiles arrive
+    if (lane == 0) ahead = w;
+    const bool more = warp_next(ahead, a);
+    const int pids_ahead = more ? pages(ahead, 0) : -1;
     const int i0 = w.first_row(), nrow = w.rows(a.G);
     // ---- Q ----
     uint32_t qf[kMt == 1 ? D / 16 : 1][4];
@@ -365,7 +369,7 @@ kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a) {
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         const int row = wrow + 16 * mt + g + 8 * r;
-        rpos[mt][r] = w.d.len - w.d.n + i0 + (row < nrow ? row / a.G : 0);
+        rpos[mt][r] = w.d.len - w.d.n + i0 + over_g(a, row < nrow ? row : 0);
         if (a.causal) {
           all_hi = min(all_hi, rpos[mt][r] + 1);
           if (a.window > 0) all_lo = max(all_lo, rpos[mt][r] - a.window + 1);
@@ -555,9 +559,11 @@ kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a) {
     const bool whole = w.whole(), starts = w.t0 == 0;
     const int token0 = w.d.row0 + i0, head0 = w.h * a.G;
     if (starts && !whole && tid == 0) write_cut(a, w.cut(a, rg));
-    const bool more = warp_next(w, a);
+    __syncwarp();
     if (more) {
-      open_unit();
+      if (lane == 0) w = ahead;
+      __syncwarp();
+      open_unit(pids_ahead);
       slot = st = kJoin;
 #pragma unroll 1
       for (int i = 0; i < min(C::stages - kJoin, C::stages - 1); ++i) request();
@@ -609,7 +615,7 @@ kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a) {
       }
       if (whole) {
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;  // no visible token: zeros
-        const int64_t orow = (int64_t)(token0 + row / a.G) * a.H + head0 + row % a.G;
+        const int64_t orow = out_row(a, token0, head0, row);
         *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + orow * D + ch) =
             make_uint2(pair_from_floats<kBf16>(x.x * inv, x.y * inv),
                        pair_from_floats<kBf16>(x.z * inv, x.w * inv));
@@ -634,7 +640,7 @@ template <int D, int kMt, int kRg, bool kBf16>
 __global__ void __launch_bounds__(kThreads)
 kv8_merge_kernel(const __grid_constant__ Kv8AttnArgs a, int workers) {
   using C = Cfg<D, kMt, kRg>;
-  merge_parts<typename C::Work, kWarps, D, kBf16>(a, workers, kHeadroom);
+  merge_parts<typename C::Work, D, kBf16>(a, workers, kHeadroom);
 }
 
 template <int D, int kMt, int kRg, bool kBf16>
@@ -649,8 +655,7 @@ cudaError_t attn_t(const Kv8AttnArgs& args, cudaStream_t stream) {
   e = launch_kernel(kv8_attn_kernel<D, kMt, kRg, kBf16>, dim3(workers), dim3(kThreads), C::smem,
                     stream, /*pdl=*/false, a);
   if (e != cudaSuccess || a.uncut) return e;
-  constexpr int kRowsPer = kThreads / (D / 4);
-  return launch_kernel(kv8_merge_kernel<D, kMt, kRg, kBf16>, dim3(workers, C::unit / kRowsPer),
+  return launch_kernel(kv8_merge_kernel<D, kMt, kRg, kBf16>, dim3(workers, merge_blocks<typename C::Work, D>(a)),
                        dim3(kThreads), 0, stream, /*pdl=*/true, a, workers);
 }
 
@@ -674,7 +679,7 @@ int64_t mean_rows(int S, int T, int G) {
 size_t kv8_attn_scratch_bytes(int S, int T, int H, int H_kv, int D) {
   if (D != 64 && D != 128) return 0;
   if (mean_rows(S, T, H / H_kv) > 64) return kv8_attn_tc_scratch_bytes(D);
-  return align_up(scratch_bytes(device_sm_count() * 3, 64, D), 256);
+  return align_up(scratch_bytes(device_sm_count() * 4, 64, D), 256);
 }
 
 cudaError_t launch_kv8_attn(const Kv8AttnArgs& args, int type, cudaStream_t stream) {

@@ -725,7 +725,7 @@ kv8_attn_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
 template <int D, bool kBf16>
 __global__ void __launch_bounds__(128)
 kv8_merge_tc_kernel(const __grid_constant__ Kv8AttnArgs a, int workers) {
-  merge_parts<Work, 4, D, kBf16>(a, workers, kHeadroom);
+  merge_parts<Work, D, kBf16>(a, workers, kHeadroom);
 }
 
 template <int D, bool kBf16>
@@ -740,7 +740,7 @@ cudaError_t attn_tc_t(const Kv8AttnArgs& args, cudaStream_t stream) {
   e = launch_kernel(kv8_attn_tc_kernel<D, kBf16>, dim3(workers), dim3(kThreads), L::alloc, stream,
                     /*pdl=*/false, a);
   if (e != cudaSuccess || a.uncut) return e;
-  return launch_kernel(kv8_merge_tc_kernel<D, kBf16>, dim3(workers, 8), dim3(128), 0, stream,
+  return launch_kernel(kv8_merge_tc_kernel<D, kBf16>, dim3(workers, merge_blocks<Work, D>(a)), dim3(128), 0, stream,
                        /*pdl=*/true, a, workers);
 }
 

@@ -364,40 +364,129 @@ __device__ __forceinline__ int row_exponent(float mx) {
   return mx > 0.0f ? max(-126, min(126, E)) : 0;
 }
 
+// row / G for row < 256, by the host's reciprocal ceil(2^16 / G): row times its
+// excess (below G) stays below 2^16.
+__device__ __forceinline__ int over_g(const Kv8AttnArgs& a, int row) {
+  return (row * a.g_inv) >> 16;
+}
+// Row of q, out and lse (token x H + head) of a unit's row.
+__device__ __forceinline__ int64_t out_row(const Kv8AttnArgs& a, int token, int head, int row) {
+  const int t = over_g(a, row);
+  return (int64_t)(token + t) * a.H + head + (row - t * a.G);
+}
+
 // Joins the parts of the cut units: block (x, y) takes the unit that worker x
-// starts, every gridDim.y-th group of its rows.
-template <class Sh, int kWarps, int D, bool kBf16>
+// starts, every gridDim.y-th group of its rows.  Few parts: a thread has four
+// channels of a row and goes through them.  Many (a long context with few units):
+// a warp has 32 channels of a row; its lanes share out the parts' maxima and sums,
+// 32 at a time, and four groups of eight lanes sum a quarter of the parts each, all
+// loads independent.  (A thread that goes through the parts takes 0.35 us a part;
+// for two parts of 256 rows the shared form takes twice as long as it.  No shared
+// memory: a block with some has its SM's memory divided anew, which waits for the
+// blocks of the attention and delays the next call's.)
+template <class Sh, int D>
+constexpr int merge_rows() {  // rows of a block of four warps
+  return 4 / (D / 32);
+}
+// Blocks for a worker's unit: a row group each for up to 16 rows.
+template <class Sh, int D>
+int merge_blocks(const Kv8AttnArgs& a) {
+  const int64_t most = a.c.cu ? Sh::kUnit : (int64_t)(a.c.T / a.c.S) * a.G;
+  const int rows = (int)(most < Sh::kUnit ? most : Sh::kUnit);
+  return ((rows < 16 ? rows : 16) + merge_rows<Sh, D>() - 1) / merge_rows<Sh, D>();
+}
+template <class Sh, int D, bool kBf16>
 __device__ __forceinline__ void merge_parts(const Kv8AttnArgs& a, int workers, float headroom) {
-  constexpr int kUnit = Sh::kUnit, kTpr = D / 4, kRowsPer = kWarps * 32 / kTpr;
+  constexpr int kUnit = Sh::kUnit, kRowsPer = merge_rows<Sh, D>();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, group = lane >> 3;
+  const int sub = warp / (D / 32), ch = (warp % (D / 32)) * 32 + (lane & 7) * 4;
   pdl_wait();
   const int4 cut = __ldcg(reinterpret_cast<const int4*>(a.scratch) + blockIdx.x);
-  const int last = cut.x, ch = (threadIdx.x % kTpr) * 4, nrow = last < 0 ? 0 : cut.w;
-  for (int row = blockIdx.y * kRowsPer + threadIdx.x / kTpr; row < nrow;
-       row += gridDim.y * kRowsPer) {
-    float m = -INFINITY, l = 0.0f;
-    float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-    for (int p = blockIdx.x; p <= last; ++p) {
-      const float* src = scratch_part(a, workers, p, p == (int)blockIdx.x, kUnit, D);
-      const float pm = __ldcg(src + kUnit * D + row), pl = __ldcg(src + kUnit * D + kUnit + row);
-      const float4 y = __ldcg(reinterpret_cast<const float4*>(src + (size_t)row * D + ch));
-      const float nm = fmaxf(m, pm), z = nm == -INFINITY ? 0.0f : nm;
-      const float f0 = ex2(m - z), f1 = ex2(pm - z);
-      m = nm;
-      l = l * f0 + pl * f1;
-      x.x = x.x * f0 + y.x * f1;
-      x.y = x.y * f0 + y.y * f1;
-      x.z = x.z * f0 + y.z * f1;
-      x.w = x.w * f0 + y.w * f1;
-    }
+  const int last = cut.x, nrow = last < 0 ? 0 : cut.w;
+  auto write = [&](int row, int c4, float4 x, float m, float l) {
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;  // no visible token: zeros
-    const int64_t orow = (int64_t)(cut.y + row / a.G) * a.H + cut.z + row % a.G;
-    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + orow * D + ch) =
+    const int64_t orow = out_row(a, cut.y, cut.z, row);
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + orow * D + c4) =
         make_uint2(pair_from_floats<kBf16>(x.x * inv, x.y * inv),
                    pair_from_floats<kBf16>(x.z * inv, x.w * inv));
-    if (a.lse && ch == 0)
+    if (a.lse && c4 == 0)
       a.lse[orow] =
           l == 0.0f ? -INFINITY : ((m == -INFINITY ? 0.0f : m) - headroom + __log2f(l)) * kLn2;
+  };
+  if (last - (int)blockIdx.x < 4) {
+    constexpr int kTpr = D / 4, kRows = 128 / kTpr;
+    const int c4 = (threadIdx.x % kTpr) * 4;
+    for (int row = blockIdx.y * kRows + threadIdx.x / kTpr; row < nrow; row += gridDim.y * kRows) {
+      float m = -INFINITY, l = 0.0f;
+      float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+      for (int p = blockIdx.x; p <= last; ++p) {
+        const float* src = scratch_part(a, workers, p, p == (int)blockIdx.x, kUnit, D);
+        const float pm = __ldcg(src + kUnit * D + row), pl = __ldcg(src + kUnit * D + kUnit + row);
+        const float4 y = __ldcg(reinterpret_cast<const float4*>(src + (size_t)row * D + c4));
+        const float nm = fmaxf(m, pm), z = nm == -INFINITY ? 0.0f : nm;
+        const float f0 = ex2(m - z), f1 = ex2(pm - z);
+        m = nm;
+        l = l * f0 + pl * f1;
+        x.x = x.x * f0 + y.x * f1;
+        x.y = x.y * f0 + y.y * f1;
+        x.z = x.z * f0 + y.z * f1;
+        x.w = x.w * f0 + y.w * f1;
+      }
+      write(row, c4, x, m, l);
+    }
+    return;
+  }
+  for (int row = blockIdx.y * kRowsPer + sub; row < nrow; row += gridDim.y * kRowsPer) {
+    float m = -INFINITY, l = 0.0f;
+    float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int p0 = blockIdx.x; p0 <= last; p0 += 32) {
+      const int n = min(32, last + 1 - p0);
+      auto part = [&](int i) {
+        return scratch_part(a, workers, p0 + i, p0 + i == (int)blockIdx.x, kUnit, D);
+      };
+      float pm = -INFINITY, pl = 0.0f;
+      if (lane < n) {
+        pm = __ldcg(part(lane) + kUnit * D + row);
+        pl = __ldcg(part(lane) + kUnit * D + kUnit + row);
+      }
+      float4 y[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int i = group + 4 * k;
+        y[k] = i < n ? __ldcg(reinterpret_cast<const float4*>(part(i) + (size_t)row * D + ch))
+                     : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      }
+      float top = fmaxf(m, pm);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const float z = top == -INFINITY ? 0.0f : top, old = ex2(m - z), f = ex2(pm - z);
+      float sum = f * pl;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      l = fmaf(l, old, sum);
+      m = top;
+      x.x *= old;
+      x.y *= old;
+      x.z *= old;
+      x.w *= old;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float g = __shfl_sync(0xffffffffu, f, group + 4 * k);
+        x.x = fmaf(y[k].x, g, x.x);
+        x.y = fmaf(y[k].y, g, x.y);
+        x.z = fmaf(y[k].z, g, x.z);
+        x.w = fmaf(y[k].w, g, x.w);
+      }
+    }
+#pragma unroll
+    for (int o = 8; o < 32; o <<= 1) {
+      x.x += __shfl_xor_sync(0xffffffffu, x.x, o);
+      x.y += __shfl_xor_sync(0xffffffffu, x.y, o);
+      x.z += __shfl_xor_sync(0xffffffffu, x.z, o);
+      x.w += __shfl_xor_sync(0xffffffffu, x.w, o);
+    }
+    if (group == 0) write(row, ch, x, m, l);
   }
 }
 
