@@ -52,27 +52,25 @@ constexpr int kTileKeys = 32;
 // weight is above it, which fp16 holds (65504)
 constexpr float kHeadroom = 7.0f, kMostSum = 57344.0f;
 
-// A warp has kMt matrix tiles of 16 query rows; kRg warps share a tile's keys, and
-// 4 / kRg groups of warps have rings of their own.
-template <int D, int kMt, int kRg>
+// A warp has kMt matrix tiles of 16 query rows, and its own keys and ring.
+template <int D, int kMt>
 struct Cfg {
-  static constexpr int unit = 16 * kMt * kRg;              // query rows
-  static constexpr int kgs = kWarps / kRg;                 // key groups
-  static constexpr int granule = kgs * kTileKeys;          // keys
+  static constexpr int unit = 16 * kMt;                    // query rows
+  static constexpr int granule = kWarps * kTileKeys;       // keys
   // a unit's queries and output take about as long as 128 keys
-  using Work = Shape<unit, granule, kRg>;
-  static constexpr int stages = kRg == 1 ? (D == 128 ? 3 : 4) : (D == 128 ? 5 : 8);
+  using Work = Shape<unit, granule, 1>;
+  static constexpr int stages = D == 128 ? 3 : 4;
   static constexpr int tile = kTileKeys * D;               // bytes of K (or V) of a stage
   static constexpr int stage = 2 * tile;
-  static constexpr int ring = kgs * stages * stage;
-  static constexpr int scales = kgs * stages * 16;         // ks, vs of two 16-key halves
+  static constexpr int ring = kWarps * stages * stage;
+  static constexpr int scales = kWarps * stages * 16;      // ks, vs of two 16-key halves
   // kMt > 1: the fragments of Q (in registers otherwise)
   static constexpr int q = kMt > 1 ? unit * D * 2 : 0;
   static constexpr int smem = ring + scales + q;
   static constexpr int ctas = D == 64 && kMt == 1 ? 3 : 2;  // per SM
-  // the join of the key groups uses kMt * kRg stages of each ring, the next unit's
-  // first tiles the others
-  static_assert(kMt * kRg * stage == unit * D * 4 && kMt * kRg < stages, "join");
+  // the join of the warps uses kMt stages of each ring, the next unit's first tiles
+  // the others
+  static_assert(kMt * stage == unit * D * 4 && kMt < stages, "join");
 };
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
@@ -202,26 +200,15 @@ __device__ __forceinline__ void make_q(const QRows<D>& q, float scale, uint32_t 
   }
 }
 
-// The warps of key group kg.
-template <int kRg>
-__device__ __forceinline__ void group_sync(int kg) {
-  if (kRg == 1)
-    __syncwarp();
-  else
-    asm volatile("bar.sync %0, %1;" ::"r"(1 + kg), "n"(kRg * 32) : "memory");
-}
-
-template <int D, int kMt, int kRg, bool kBf16>
-__global__ void __launch_bounds__(kThreads, Cfg<D, kMt, kRg>::ctas)
+template <int D, int kMt, bool kBf16>
+__global__ void __launch_bounds__(kThreads, Cfg<D, kMt>::ctas)
 kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a) {
-  using C = Cfg<D, kMt, kRg>;
+  using C = Cfg<D, kMt>;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ RangeSmem<kWarps> rsm;
-  __shared__ float row_max[C::kgs][C::unit], row_sum[C::kgs][C::unit], row_c[C::unit];
+  __shared__ float row_max[kWarps][C::unit], row_sum[kWarps][C::unit], row_c[C::unit];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, c = lane & 3;
-  const int kg = warp / kRg, rq = warp % kRg;  // key group, row group
-  const int wrow = rq * 16 * kMt;              // the warp's first row
   pdl_trigger();
   const Range rg = find_range<typename C::Work, kWarps>(a, blockIdx.x, gridDim.x, rsm);
   if (tid == 0) write_cut(a, Cut{-1, 0, 0, 0});
@@ -230,22 +217,22 @@ kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a) {
   Walk<typename C::Work>& ahead = walks[warp][1];
   if (!warp_start(w, a, rg, rsm)) return;
 
-  uint8_t* ring = smem + kg * (C::stages * C::stage);
-  float* ring_scale = reinterpret_cast<float*>(smem + C::ring) + kg * (C::stages * 4);
+  uint8_t* ring = smem + warp * (C::stages * C::stage);
+  float* ring_scale = reinterpret_cast<float*>(smem + C::ring) + warp * (C::stages * 4);
   uint4* qs = reinterpret_cast<uint4*>(smem + C::ring + C::scales);  // [matrix tile][k-step][lane]
   const uint32_t ring_u = smem_u32(ring), scale_u = smem_u32(ring_scale);
   const int page_mask = (1 << a.c.page_shift) - 1;
 
   // ---- the unit's tiles: pages, copies ----
-  constexpr int kJoin = kMt * kRg;  // stages of each ring that the join of the key groups uses
-  int key_first;                    // the key group's first key of granule 0 of the span
-  int issue = 0, slot = 0;            // the next tile to request (of the unit's), its stage
-  int pids, pids_next;              // pages of the requested block of 16 tiles and of the next
+  constexpr int kJoin = kMt;  // stages of each ring that the join of the warps uses
+  int key_first;              // the warp's first key of granule 0 of the span
+  int issue = 0, slot = 0;    // the next tile to request (of the unit's), its stage
+  int pids, pids_next;        // pages of the requested block of 16 tiles and of the next
   // page ids of tiles i .. i + 15 of the unit's: lane l has tile i + l % 16, its
   // 16-key half l / 16; -1: nothing of the half is seen, or the entry is outside the cache
   auto pages = [&](const Walk<typename C::Work>& u, int i) -> int {
     const int t = u.t0 + i + (lane & 15);
-    const int key = (u.u.g0 + t) * C::granule + kg * kTileKeys + (lane & 16);
+    const int key = (u.u.g0 + t) * C::granule + warp * kTileKeys + (lane & 16);
     int p = -1;
     if (t < u.t1 && key < u.u.hi && key + 16 > u.u.lo) {
       p = a.c.table[(int64_t)u.s * a.c.max_pages + (key >> a.c.page_shift)];
@@ -257,7 +244,7 @@ kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a) {
     return p;
   };
   // Requests the unit's next tile (an empty group of copies past its last).  A half
-  // is 16 * D contiguous bytes of a page; with two warps a group each takes a half.
+  // is 16 * D contiguous bytes of a page.
   auto request = [&]() {
     constexpr int kCh = D / 16, kPerIt = 32 / kCh;  // chunks a key, keys an instruction
     constexpr int kIts = 16 / kPerIt;               // instructions a half
@@ -270,8 +257,7 @@ kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a) {
       const int key0 = key_first + t * C::granule;
       const uint32_t kd = ring_u + slot * C::stage, vd = kd + C::tile;
 #pragma unroll
-      for (int i = 0; i < 2 / kRg; ++i) {
-        const int hf = kRg == 1 ? i : rq;
+      for (int hf = 0; hf < 2; ++hf) {
         const int p = __shfl_sync(0xffffffffu, pids, (issue & 15) + 16 * hf);
         const int first = key0 + 16 * hf;
         const int64_t off =
@@ -296,26 +282,25 @@ kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a) {
           }
         }
       }
-      if (rq == 0) {  // ks of half 0, 1, vs of half 0, 1 (zeros: no page)
-        const int p = __shfl_sync(0xffffffffu, pids, (issue & 15) + (lane & 1) * 16);
-        if (lane < 4)
-          copy4(scale_u + (slot * 4 + lane) * 4,
-                ((lane & 2) ? a.c.v_scale : a.c.k_scale) +
-                    (p >= 0 ? (int64_t)p * a.c.H_kv + w.h : 0),
-                p >= 0);
-      }
+      // ks of half 0, 1, vs of half 0, 1 (zeros: no page)
+      const int p = __shfl_sync(0xffffffffu, pids, (issue & 15) + (lane & 1) * 16);
+      if (lane < 4)
+        copy4(scale_u + (slot * 4 + lane) * 4,
+              ((lane & 2) ? a.c.v_scale : a.c.k_scale) +
+                  (p >= 0 ? (int64_t)p * a.c.H_kv + w.h : 0),
+              p >= 0);
     }
     copy_commit();
     ++issue;
     if (++slot == C::stages) slot = 0;
   };
   auto open_unit = [&](int first_pages) {
-    key_first = w.u.g0 * C::granule + kg * kTileKeys;
+    key_first = w.u.g0 * C::granule + warp * kTileKeys;
     issue = 0;
     pids = first_pages;
     pids_next = pages(w, 16);
   };
-  const int qtile = kMt == 1 ? rq : warp;  // the matrix tile of Q that this warp takes
+  const int qtile = kMt == 1 ? 0 : warp;  // the matrix tile of Q that this warp takes
   QRows<D> qrows;
   auto fetch = [&]() {
     if (qtile < C::unit / 16)
@@ -356,8 +341,8 @@ kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a) {
       __syncthreads();
 #pragma unroll
       for (int mt = 0; mt < kMt; ++mt) {
-        crow[mt][0] = row_c[wrow + 16 * mt + g];
-        crow[mt][1] = row_c[wrow + 16 * mt + g + 8];
+        crow[mt][0] = row_c[16 * mt + g];
+        crow[mt][1] = row_c[16 * mt + g + 8];
       }
     }
     // each row's token (rows that the unit does not have: its first row's), and the
@@ -368,7 +353,7 @@ kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a) {
     for (int mt = 0; mt < kMt; ++mt)
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        const int row = wrow + 16 * mt + g + 8 * r;
+        const int row = 16 * mt + g + 8 * r;
         rpos[mt][r] = w.d.len - w.d.n + i0 + over_g(a, row < nrow ? row : 0);
         if (a.causal) {
           all_hi = min(all_hi, rpos[mt][r] + 1);
@@ -393,9 +378,9 @@ kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a) {
 #pragma unroll 1
     for (int t = w.t0; t < w.t1; ++t) {
       copy_wait<C::stages - 2>();
-      // the group's copies of tile t are there, and it is done with tile t - 1,
-      // whose stage takes the next copies
-      group_sync<kRg>(kg);
+      // every lane's copies of tile t are there, and it is done with tile t - 1, whose
+      // stage takes the next copies
+      __syncwarp();
       request();
       const float4 bs = *reinterpret_cast<const float4*>(ring_scale + st * 4);
       const uint8_t* kt = ring + st * C::stage;
@@ -417,7 +402,7 @@ kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a) {
           for (int mt = 0; mt < kMt; ++mt)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-              qv[mt][i] = qs[((rq * kMt + mt) * (D / 16) + 4 * j + i) * 32 + lane];
+              qv[mt][i] = qs[(mt * (D / 16) + 4 * j + i) * 32 + lane];
         }
         uint4 b[4];
 #pragma unroll
@@ -553,7 +538,7 @@ kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a) {
       }
     }
     copy_wait<0>();
-    group_sync<kRg>(kg);  // the group is done with its ring
+    __syncwarp();  // the warp is done with its ring
 
     // ---- the next unit's first tiles, into the stages that the join leaves ----
     const bool whole = w.whole(), starts = w.t0 == 0;
@@ -569,18 +554,18 @@ kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a) {
       for (int i = 0; i < min(C::stages - kJoin, C::stages - 1); ++i) request();
     }
 
-    // ---- join the key groups ----
-    float* obuf = reinterpret_cast<float*>(ring);  // [row][D], of each key group
+    // ---- join the warps ----
+    float* obuf = reinterpret_cast<float*>(ring);  // [row][D], of each warp
 #pragma unroll
     for (int mt = 0; mt < kMt; ++mt)
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         lrow[mt][r] += __shfl_xor_sync(0xffffffffu, lrow[mt][r], 1);
         lrow[mt][r] += __shfl_xor_sync(0xffffffffu, lrow[mt][r], 2);
-        const int row = wrow + 16 * mt + g + 8 * r;
+        const int row = 16 * mt + g + 8 * r;
         if (c == 0) {
-          row_max[kg][row] = mrow[mt][r];
-          row_sum[kg][row] = lrow[mt][r];
+          row_max[warp][row] = mrow[mt][r];
+          row_sum[warp][row] = lrow[mt][r];
         }
         float* dst = obuf + (size_t)row * D + 2 * c;
 #pragma unroll
@@ -598,12 +583,12 @@ kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a) {
       if (row >= nrow) continue;
       float m = row_max[0][row];
 #pragma unroll
-      for (int q = 1; q < C::kgs; ++q) m = fmaxf(m, row_max[q][row]);
+      for (int q = 1; q < kWarps; ++q) m = fmaxf(m, row_max[q][row]);
       const float mz = m == -INFINITY ? 0.0f : m;
       float l = 0.0f;
       float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-      for (int q = 0; q < C::kgs; ++q) {
+      for (int q = 0; q < kWarps; ++q) {
         const float f = ex2(row_max[q][row] - mz);
         l = fmaf(row_sum[q][row], f, l);
         const float4 y = *reinterpret_cast<const float4*>(
@@ -636,38 +621,38 @@ kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a) {
   }
 }
 
-template <int D, int kMt, int kRg, bool kBf16>
+template <int D, int kMt, bool kBf16>
 __global__ void __launch_bounds__(kThreads)
 kv8_merge_kernel(const __grid_constant__ Kv8AttnArgs a, int workers) {
-  using C = Cfg<D, kMt, kRg>;
+  using C = Cfg<D, kMt>;
   merge_parts<typename C::Work, D, kBf16>(a, workers, kHeadroom);
 }
 
-template <int D, int kMt, int kRg, bool kBf16>
+template <int D, int kMt, bool kBf16>
 cudaError_t attn_t(const Kv8AttnArgs& args, cudaStream_t stream) {
-  using C = Cfg<D, kMt, kRg>;
+  using C = Cfg<D, kMt>;
   Kv8AttnArgs a = args;
   a.tpu = C::unit / a.G;
-  cudaError_t e = cudaFuncSetAttribute(kv8_attn_kernel<D, kMt, kRg, kBf16>,
+  cudaError_t e = cudaFuncSetAttribute(kv8_attn_kernel<D, kMt, kBf16>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, C::smem);
   if (e != cudaSuccess) return e;
   const int workers = device_sm_count() * C::ctas;
-  e = launch_kernel(kv8_attn_kernel<D, kMt, kRg, kBf16>, dim3(workers), dim3(kThreads), C::smem,
+  e = launch_kernel(kv8_attn_kernel<D, kMt, kBf16>, dim3(workers), dim3(kThreads), C::smem,
                     stream, /*pdl=*/false, a);
   if (e != cudaSuccess || a.uncut) return e;
-  return launch_kernel(kv8_merge_kernel<D, kMt, kRg, kBf16>, dim3(workers, merge_blocks<typename C::Work, D>(a)),
+  return launch_kernel(kv8_merge_kernel<D, kMt, kBf16>, dim3(workers, merge_blocks<typename C::Work, D>(a)),
                        dim3(kThreads), 0, stream, /*pdl=*/true, a, workers);
 }
 
-template <int D, bool kBf16>
-cudaError_t attn_rows(const Kv8AttnArgs& a, int64_t rows, cudaStream_t stream) {
-  if (rows <= 16) return attn_t<D, 1, 1, kBf16>(a, stream);
-  if (rows <= 32) return attn_t<D, 2, 1, kBf16>(a, stream);
-  return attn_t<D, 2, 2, kBf16>(a, stream);
-}
-
-// Units of up to so many keys are not cut.
-constexpr int64_t kUncut = 512, kUncutTc = 512;
+// Rows of a KV head (per sequence, on average) up to which the kernel of 16 rows
+// and that of 32 are taken.  At 64 rows a warp of 32 rows and its neighbour would
+// convert every tile twice (24 x 16K tokens, D = 128: 146 us); the tcgen05 kernel
+// takes 117 us there, and 114 us at 32 rows, where this one takes 88.
+constexpr int64_t kRows1 = 16, kRows2 = 32;
+// Units of up to so many keys are not cut: one CTA takes 3 to 4 us for 512 keys,
+// what the merge kernel would add (128 sequences of 1000 tokens: 58 us cut, 64 us
+// with units of 1024 keys left whole).
+constexpr int64_t kUncut = 512;
 
 // Query rows of a KV head per sequence, on average.
 int64_t mean_rows(int S, int T, int G) {
@@ -678,21 +663,21 @@ int64_t mean_rows(int S, int T, int G) {
 
 size_t kv8_attn_scratch_bytes(int S, int T, int H, int H_kv, int D) {
   if (D != 64 && D != 128) return 0;
-  if (mean_rows(S, T, H / H_kv) > 64) return kv8_attn_tc_scratch_bytes(D);
-  return align_up(scratch_bytes(device_sm_count() * 4, 64, D), 256);
+  if (mean_rows(S, T, H / H_kv) > kRows2) return kv8_attn_tc_scratch_bytes(D);
+  return align_up(scratch_bytes(device_sm_count() * 3, 32, D), 256);
 }
 
 cudaError_t launch_kv8_attn(const Kv8AttnArgs& args, int type, cudaStream_t stream) {
   Kv8AttnArgs a = args;
   const int64_t rows = mean_rows(a.c.S, a.c.T, a.G);
-  // cutting a unit of a few tiles gains less than the merge kernel takes
-  a.uncut = kv8_most_tokens(a) <= (rows > 64 ? kUncutTc : kUncut);
-  if (rows > 64) return launch_kv8_attn_tc(a, type, stream);
+  a.uncut = kv8_most_tokens(a) <= kUncut;
+  if (rows > kRows2) return launch_kv8_attn_tc(a, type, stream);
+  const bool one = rows <= kRows1, bf16 = type == CSA2_BF16;
   if (a.c.D == 128)
-    return type == CSA2_BF16 ? attn_rows<128, true>(a, rows, stream)
-                             : attn_rows<128, false>(a, rows, stream);
-  return type == CSA2_BF16 ? attn_rows<64, true>(a, rows, stream)
-                           : attn_rows<64, false>(a, rows, stream);
+    return one ? (bf16 ? attn_t<128, 1, true>(a, stream) : attn_t<128, 1, false>(a, stream))
+               : (bf16 ? attn_t<128, 2, true>(a, stream) : attn_t<128, 2, false>(a, stream));
+  return one ? (bf16 ? attn_t<64, 1, true>(a, stream) : attn_t<64, 1, false>(a, stream))
+             : (bf16 ? attn_t<64, 2, true>(a, stream) : attn_t<64, 2, false>(a, stream));
 }
 
 }  // namespace csa2
