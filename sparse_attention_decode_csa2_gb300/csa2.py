@@ -703,6 +703,8 @@ def kv8_attn(q: torch.Tensor, cache: Kv8Cache, batch: Kv8Batch, causal: bool = T
     allocated here)."""
     if q.dtype not in (torch.bfloat16, torch.float16):
         raise ValueError(f"q must be bf16 or fp16, got {q.dtype}")
+    if not 0 <= window < 1 << 31:
+        raise ValueError(f"window must be 0 or a count below 2^31, got {window}")
     qs = _kv8_rows(q, batch.n_rows, None, cache, "q")
     T, H, D = q.shape
     ws = _kv8_ws(cache, batch, H, ws)

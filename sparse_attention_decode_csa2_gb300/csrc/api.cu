@@ -528,7 +528,7 @@ csa2_status csa2_layer_group(const csa2_layer* layers, int n_layers, const csa2_
 }
 
 size_t csa2_kv8_workspace_size(const csa2_kv8_cache* c, const csa2_kv8_batch* b, int H) {
-  if (!c || !b || H < 1 || b->S < 1 || b->T < 1) return kStatusBytes;
+  if (!c || !b || c->H_kv < 1 || H < 1 || b->S < 1 || b->T < 1) return kStatusBytes;
   return kStatusBytes + kv8_attn_scratch_bytes(b->S, b->T, H, c->H_kv, c->D);
 }
 
@@ -574,7 +574,8 @@ csa2_status csa2_kv8_attn(const void* q, int type, int64_t q_stride, int H,
   if (type != CSA2_BF16 && type != CSA2_FP16) return CSA2_ERR_INVALID_ARG;
   if ((s = check_rows(q, type, q_stride, H, a.c.D)) != CSA2_OK) return s;
   if (window < 0 || (window > 0 && !causal)) return CSA2_ERR_INVALID_ARG;
-  if (!(softmax_scale > 0.0f) || !(softmax_scale < INFINITY)) return CSA2_ERR_INVALID_ARG;
+  a.scale_log2 = softmax_scale * 1.44269504088896340736f;
+  if (!(softmax_scale > 0.0f) || !(a.scale_log2 < INFINITY)) return CSA2_ERR_INVALID_ARG;
   if (a.c.T > 0 && (!q || !out)) return CSA2_ERR_INVALID_ARG;
   if (!aligned16(out)) return CSA2_ERR_INVALID_ARG;
   if (!ws || !aligned16(ws) || ws_bytes < csa2_kv8_workspace_size(cache, batch, H))
@@ -585,11 +586,10 @@ csa2_status csa2_kv8_attn(const void* q, int type, int64_t q_stride, int H,
   a.out = out;
   a.lse = lse;
   a.causal = causal ? 1 : 0;
-  a.window = window;
+  a.window = window < 3 << 29 ? window : 3 << 29;  // (past any length; token - window fits an int)
   a.uncut = 0;
   a.tpu = 0;
   a.g_inv = (65536 + a.G - 1) / a.G;
-  a.scale_log2 = softmax_scale * 1.44269504088896340736f;
   a.scratch = reinterpret_cast<uint8_t*>(ws) + kStatusBytes;
   return check_launch(launch_kv8_attn(a, type, stream));
 }

@@ -78,7 +78,8 @@ def test_row_arguments_are_refused(C):
     assert _attn(C, type=2) == 1                 # no fp32 queries
     assert _attn(C, H=0) == 1 and _attn(C, H=12) == 1
     assert _attn(C, window=-1) == 1 and _attn(C, causal=0, window=5) == 1
-    for scale in (0.0, -1.0, float("nan"), float("inf")):
+    assert _attn(C, H=8 * 257, q_stride=1 << 20) == 2
+    for scale in (0.0, -1.0, float("nan"), float("inf"), 3e38):
         assert _attn(C, scale=scale) == 1
     assert _attn(C, ws=FAKE + 4) == 3
 
@@ -97,6 +98,9 @@ def test_workspace_size(C):
     assert C.lib.csa2_kv8_workspace_size(c, b, 32) > 256
     n = C.lib.csa2_kv8_workspace_size(c, b, 32)
     assert _attn(C, ws_bytes=n - 1) == 3
+    for kw in (dict(H_kv=0), dict(S=0, T=0), dict(T=0)):  # nothing to attend with: the status alone
+        assert C.lib.csa2_kv8_workspace_size(*_structs(C, **kw), 32) == 256
+    assert C.lib.csa2_kv8_workspace_size(None, b, 32) == 256
 
 
 def test_binding_refuses_host_tensors(C):
