@@ -368,8 +368,8 @@ csa2_status csa2_sparse_attn_fp4_noalloc(const uint16_t* q_bf16, const uint8_t* 
  * of the step's T rows, or, with cu_rows NULL, an equal share (T % S == 0);
  * row i of its n rows is token kv_len[s] - n + i.  A row whose token would be
  * negative belongs to no token: it is not written to the cache, reads as
- * zeros, and sees nothing (so kv_len[s] = 0 makes s an idle slot of a fixed
- * batch).  Rows of no sequence (past cu_rows[S]) are left as they were.
+ * zeros, and sees nothing under a causal mask (kv_len[s] = 0 makes s an idle
+ * slot of a fixed batch).  Rows of no sequence (past cu_rows[S]) are left as they were.
  *   Entries that make no sense are skipped and set CSA2_ERR_BAD_INDEX in the
  * status: a block-table entry outside [0, n_pages) where a token is needed
  * (nothing is written; reads as zeros; not seen), kv_len[s] < 0 or past
@@ -434,12 +434,16 @@ csa2_status csa2_kv8_read(const csa2_kv8_cache* cache, const csa2_kv8_batch* bat
  * sequences' tokens in the cache (those of this step are appended before).
  *   q        [T][H][D], CSA2_BF16 or CSA2_FP16, tokens q_stride elements apart
  *            (as k_stride above); query head h reads KV head h / (H / H_kv)
- *   causal   non-zero: row i sees tokens up to its own; zero: all kv_len[s]
+ *   causal   non-zero: row i sees tokens up to its own; zero: every row sees all
+ *            kv_len[s] (rows need not be tokens then: queries over a text that
+ *            was stored before, any number of them)
  *   window   0, or (causal only) a row sees its own token and the window - 1
  *            before it
  *   out      [T][H][D] of q's type, dense, 16-byte aligned
  *   lse      fp32 [T][H] log-sum-exp of the scaled logits, or NULL
- *   A row that sees nothing yields out = 0 and lse = -inf.  The result of a
+ *   A row that sees nothing yields out = 0 and lse = -inf.  A NaN of a token
+ *   that a row sees makes its out NaN (in V: in that channel at least; lse is not
+ *   specified then); of one that it does not see it has no effect.  The result of a
  *   call depends on its inputs alone (no atomics).
  *   ws       at least csa2_kv8_workspace_size(cache, batch, H) bytes, 16-byte
  *            aligned.

@@ -386,8 +386,30 @@ kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a) {
       const uint8_t* kt = ring + st * C::stage;
       const uint32_t vt = ring_u + st * C::stage + C::tile;
       if (++st == C::stages) st = 0;
-      if (bs.z == 0.0f && bs.w == 0.0f) continue;
       const int key0 = key_first + t * C::granule;
+      const bool half0 = bs.z != 0.0f, half1 = bs.w != 0.0f;
+      const bool masked = !(half0 && half1 && key0 >= all_lo && key0 + kTileKeys <= all_hi);
+      if (masked) {
+        if (!half0 && !half1) continue;
+        // A weight of zero does not hide a NaN of V: where some rows see a key and
+        // others do not, its V codes become zeros and its K codes NaN, which the mask
+        // hides.  (Keys that no row sees are zeros.)
+        const int key = key0 + lane;
+        if (key < all_lo || key >= all_hi) {
+          uint8_t* codes = ring + (vt - C::tile - ring_u);
+          bool nan = false;
+#pragma unroll 1
+          for (int ch = 0; ch < D / 16; ++ch) {
+            uint4* x = reinterpret_cast<uint4*>(codes + C::tile + tile_off<D>(lane, ch));
+            if (has_nan(*x)) {
+              *x = make_uint4(0, 0, 0, 0);
+              nan = true;
+            }
+          }
+          if (nan) *reinterpret_cast<uint32_t*>(codes + tile_off<D>(lane, 0)) = 0x7F7F7F7Fu;
+        }
+        __syncwarp();
+      }
       // ---- S = Q K^T ----
       float sc[kMt][4][4];
 #pragma unroll
@@ -425,8 +447,7 @@ kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a) {
           }
       }
       // ---- masks ----
-      const bool half0 = bs.z != 0.0f, half1 = bs.w != 0.0f;
-      if (!(half0 && half1 && key0 >= all_lo && key0 + kTileKeys <= all_hi)) {
+      if (masked) {
 #pragma unroll
         for (int mt = 0; mt < kMt; ++mt)
 #pragma unroll

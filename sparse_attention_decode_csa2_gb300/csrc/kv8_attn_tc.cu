@@ -79,7 +79,7 @@ struct Ctl {
   // seen).  Four tiles: the loader is at most one ahead of the dequantisers, which
   // are at most two ahead of the slower softmax
   float4 sc[4][8];
-  int32_t clean[4];  // every key of the tile is seen by some row
+  int32_t marks[4];    // of a tile: kRagged, kEdge
   uint64_t rk_full, rk_empty, rv_full, rv_empty;  // the codes of a tile
   uint64_t q_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_full[2];
   uint64_t done;
@@ -182,6 +182,10 @@ __device__ __forceinline__ F2 add2(F2 a, F2 b) {
       : "f"(a.lo), "f"(a.hi), "f"(b.lo), "f"(b.hi));
   return r;
 }
+
+// Marks of a tile: keys that no row of the unit sees; keys that some rows see and
+// others do not.
+constexpr int kRagged = 1, kEdge = 2;
 
 // Columns key .. key + 31 of S that the row does not see become -infinity.
 __device__ __forceinline__ void mask32(uint32_t* s, int key, int rlo, int rhi) {
@@ -557,16 +561,33 @@ kv8_attn_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
           uint64_t* empty = kv ? ctl.v_empty : ctl.k_empty;
           alive = warp_wait(bars, it & 1u, status) && warp_wait(empty + st, par, status);
           if (!alive) break;
-          const bool clean = ctl.clean[it & 3] != 0;
+          const int marks = ctl.marks[it & 3];
+          if ((marks & kEdge) && !(alive = warp_wait(&ctl.rv_full, it & 1u, status))) break;
           const uint8_t* raw = smem + L::rk + kv * L::raw;
           uint8_t* to = smem + L::k + (2 * kv + st) * L::tile;
+          if (marks == 0) {
 #pragma unroll 4
-          for (int i = 0; i < 32 / kKeys; ++i) {
-            const int e = 32 * dw + kKeys * i + sub;
-            uint4 x = *reinterpret_cast<const uint4*>(raw + e * D + 16 * c);
-            if (!clean && (key0 + e < lo || key0 + e >= hi || ctl.sc[it & 3][e >> 4].z == 0.0f))
-              x = make_uint4(0, 0, 0, 0);
-            put16(to + (c >> 2) * kAtom, e, c & 3, x);
+            for (int i = 0; i < 32 / kKeys; ++i) {
+              const int e = 32 * dw + kKeys * i + sub;
+              put16(to + (c >> 2) * kAtom, e, c & 3,
+                    *reinterpret_cast<const uint4*>(raw + e * D + 16 * c));
+            }
+          } else {
+#pragma unroll 1
+            for (int i = 0; i < 32 / kKeys; ++i) {
+              const int e = 32 * dw + kKeys * i + sub;
+              uint4 x = *reinterpret_cast<const uint4*>(raw + e * D + 16 * c);
+              if (key0 + e < lo || key0 + e >= hi || ctl.sc[it & 3][e >> 4].z == 0.0f) {
+                x = make_uint4(0, 0, 0, 0);
+              } else if ((marks & kEdge) &&
+                         has_nan(*reinterpret_cast<const uint4*>(smem + L::rv + e * D + 16 * c))) {
+                // A weight of zero does not hide a NaN of V: where some rows see a key
+                // and others do not, its V codes become zeros and its K codes NaN,
+                // which the mask hides
+                x = kv ? make_uint4(0, 0, 0, 0) : make_uint4(0x7F7F7F7Fu, 0, 0, 0);
+              }
+              put16(to + (c >> 2) * kAtom, e, c & 3, x);
+            }
           }
           warp_arrive(full + st);
           if (lane == 0) mbar_arrive(su32(bars + 1));
@@ -590,6 +611,13 @@ kv8_attn_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
       if (w.t0 == 0 && w.t1 < w.u.ng && lane == 0) write_cut(a, w.cut(a, rg));
       const int t1 = w.t1, g0 = w.u.g0, lo = w.u.lo, hi = w.u.hi, h = w.h;
       const int32_t* table = a.c.table + (int64_t)w.s * a.c.max_pages;
+      // tokens that every row sees
+      int all_lo = lo, all_hi = hi;
+      if (a.causal) {
+        const int first = w.d.len - w.d.n + w.first_row();
+        all_hi = min(hi, first + 1);
+        if (a.window > 0) all_lo = max(lo, first + min(w.d.n - w.first_row(), w.d.tpu) - a.window);
+      }
       // page of the lane's group in tile j: -1 where no key of its run is seen or the
       // entry is outside the cache
       auto find = [&](int j) -> int {
@@ -623,7 +651,9 @@ kv8_attn_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
         }
         if (lane < 8) ctl.sc[it & 3][lane] = sc;
         if (lane == 0)
-          ctl.clean[it & 3] = all == 0xffffffffu && key0 >= lo && key0 + kTileE <= hi;
+          ctl.marks[it & 3] =
+              (all != 0xffffffffu || key0 < lo || key0 + kTileE > hi ? kRagged : 0) |
+              (max(key0, lo) < all_lo || min(key0 + kTileE, hi) > all_hi ? kEdge : 0);
         __syncwarp();
         if (lane == 0) mbar_expect_tx(su32(&ctl.rk_full), bytes);
         __syncwarp();

@@ -340,6 +340,12 @@ __device__ __forceinline__ float ex2(float x) {
   return r;
 }
 
+// Is one of 16 E4M3 codes a NaN (0x7F, 0xFF)?
+__device__ __forceinline__ bool has_nan(uint4 x) {
+  auto sevens = [](uint32_t w) { return (w & 0x7F7F7F7Fu) + 0x01010101u; };
+  return ((sevens(x.x) | sevens(x.y) | sevens(x.z) | sevens(x.w)) & 0x80808080u) != 0;
+}
+
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));

@@ -386,6 +386,92 @@ def test_attn_strided_queries_and_padded_rows(C):
     assert (out[60:] == 3).all() and (lse[60:] == 5).all()
 
 
+@pytest.mark.parametrize("D,page", [(128, 64), (64, 16)])
+@pytest.mark.parametrize("G,n,window", [(4, [4, 4, 4], 0), (4, [8, 8, 8], 0), (2, [6, 6, 6], 40), (3, [10, 10, 10], 33),
+                                        (4, [150, 60, 300], 0), (3, [150, 70, 300], 50), (16, [5, 9, 17], 0)])
+def test_attn_nan_of_a_token_stays_with_the_rows_that_see_it(C, D, page, G, n, window):
+    Hk, lens = 2, [150, 73, 409]
+    w = World(C, 48 + G, lens, Hk, D, page).fill()
+    cu = np.concatenate([[0], np.cumsum(n)]).tolist()
+    q = _q(w.rng, cu[-1], Hk * G, D, BF16)
+    # a NaN in V of head 0 of some tokens of this step (and one before it), in K of head 1 of another
+    k, v = w.k.copy(), w.v.copy()
+    vs_, ks_ = [], []
+    for s, L in enumerate(lens):
+        for j in (L - 2, L - n[s] + n[s] // 2, max(0, L - n[s] - 20)):
+            vs_.append((s, j, int(w.rng.integers(D))))
+        ks_.append((s, L - 1 - n[s] // 3))
+    for s, j, c in vs_:
+        v[w.table[s, j // page], 0, j % page, c] = 0x7F if j & 1 else 0xFF
+        w.v[w.table[s, j // page], 0, j % page, c] = 0
+    for s, j in ks_:
+        k[w.table[s, j // page], 1, j % page, 3] = 0x7F
+        w.k[w.table[s, j // page], 1, j % page, 3] = 0
+    f = lambda a: torch.from_numpy(a.copy()).cuda()
+    cache, batch = C.Kv8Cache(f(k), f(v), f(w.ks), f(w.vs)), w.batch(cu[-1], cu)
+    out, lse = C.kv8_attn(q.cuda(), cache, batch, True, window)
+    shares = R.rows_of(cu[-1], 3, cu)
+    ref = R.attention(q.double().numpy(), (w.k, w.v, w.ks, w.vs), w.table, lens, shares, page, True, window,
+                      1 / math.sqrt(D))
+    tol_o, tol_l = R.attention_bounds(*ref, D, max(lens), BF16)
+    got_o, got_l = out.double().cpu().numpy(), lse.double().cpu().numpy()
+    clean = np.ones((cu[-1], Hk * G), bool)
+    for s, (r0, m) in enumerate(shares):
+        pos = lens[s] - m + np.arange(m)
+        sees = lambda j: (pos >= j) & ((pos - j < window) if window else True)
+        for t, j, c in vs_:
+            if t == s:
+                rows = r0 + np.flatnonzero(sees(j))
+                assert np.isnan(got_o[rows, :G, c]).all()
+                clean[rows, :G] = False
+        for t, j in ks_:
+            if t == s:
+                rows = r0 + np.flatnonzero(sees(j))
+                assert np.isnan(got_o[rows, G:]).all() and np.isnan(got_l[rows, G:]).all()
+                clean[rows, G:] = False
+    assert clean.any() and not clean.all()
+    assert (np.abs(got_o - ref[0]) <= tol_o)[clean].all()
+    assert (np.abs(got_l - ref[1]) <= tol_l)[clean].all()
+
+
+def test_attn_without_a_causal_mask_takes_more_rows_than_tokens(C):
+    w = World(C, 49, [3, 0, 17], 2, 64, 16).fill()
+    _check_attn(C, w, _q(w.rng, 15, 4, 64, FP16), None, causal=False)
+    _check_attn(C, w, _q(w.rng, 165, 4, 64, FP16), None, causal=False)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n", [1, 6, 40])
+def test_attn_window_of_whole_units(C, D, n):
+    # up to 512 visible tokens a unit stays with one CTA, past it units are cut: the same sums either way
+    w = World(C, 50 + n, [1400, 30], 1, D, 32).fill()
+    for window in (512, 513, (1 << 31) - 1):
+        _check_attn(C, w, _q(w.rng, 2 * n, 4, D, BF16), None, True, window)
+
+
+@pytest.mark.parametrize("rows", [1, 70])
+def test_sequences_without_tokens_pages_or_rows(C, rows):
+    i = lambda a: torch.tensor(a, dtype=torch.int32).cuda()
+    for pages, width in ((4, 2), (4, 0), (0, 2), (0, 0)):
+        cache = C.Kv8Cache.empty(pages, 2, 16, 64)
+        table = torch.full((3, width), -1, dtype=torch.int32).cuda()
+        batch = C.Kv8Batch(table, i([0, 0, 0]), 3 * rows)
+        q, x = torch.ones((3 * rows, 4, 64), dtype=BF16).cuda(), torch.ones((3 * rows, 2, 64), dtype=BF16).cuda()
+        ws = C.make_kv8_workspace(cache, batch, 4)
+        before = cache.k.clone()
+        C.kv8_append(cache, batch, x, x, ws=ws)
+        assert torch.equal(cache.k, before)
+        for causal in (True, False):
+            out, lse = C.kv8_attn(q, cache, batch, causal, ws=ws)
+            assert (out == 0).all() and torch.isneginf(lse).all()
+        k, v = C.kv8_read(cache, batch, BF16, ws=ws)
+        assert (k == 0).all() and (v == 0).all() and C.read_status(ws) == (0, 0)
+    none = C.Kv8Batch(table, i([0, 0, 0]), 0)
+    out, lse = C.kv8_attn(q[:0], cache, none)
+    C.kv8_append(cache, none, x[:0], x[:0])
+    assert out.shape == (0, 4, 64) and lse.shape == (0, 4)
+
+
 def test_attn_window_never_reads_pages_behind_it(C):
     # pages behind every row's window have been given away: their table entries are -1
     w = World(C, 46, [1000, 513], 1, 128, 64).fill()
@@ -508,6 +594,69 @@ def test_a_captured_step_follows_the_batch_it_was_captured_with(C):
         want, want_lse = C.kv8_attn(q, fresh, b2)
         assert torch.equal(cache.k, fresh.k) and torch.equal(cache.v_scale[w.table[0]], fresh.v_scale[w.table[0]])
         assert torch.equal(out, want) and torch.equal(lse, want_lse)
+
+
+def test_two_graphs_that_share_a_workspace_replay_in_turn(C):
+    # few rows and many rows, both of them cut into parts: each replay leaves the other's results alone
+    w = World(C, 65, [3000, 1700], 2, 64, 64).fill()
+    cache = w.cache()
+    calls = []
+    for n, H in ((1, 8), (100, 4)):
+        q, batch = _q(w.rng, 2 * n, H, 64, BF16).cuda(), w.batch(2 * n)
+        calls.append((q, batch, C.kv8_attn(q, cache, batch)))
+    ws = max((C.make_kv8_workspace(cache, b, q.shape[1]) for q, b, _ in calls), key=lambda t: t.numel())
+    graphs = []
+    for q, batch, _ in calls:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            graphs.append((g, C.kv8_attn(q, cache, batch, ws=ws)))
+    for order in ((0, 1), (1, 0, 1), (0, 0, 1, 1)):
+        for k in order:
+            for t in graphs[k][1]:
+                t.fill_(7)
+            graphs[k][0].replay()
+    torch.cuda.synchronize()
+    for (_, got), (_, _, want) in zip(graphs, calls):
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert C.read_status(ws) == (0, 0)
+
+
+def test_binding_refusals(C):
+    cache = C.Kv8Cache.empty(4, 2, 16, 64)
+    i = lambda a: torch.tensor(a, dtype=torch.int32).cuda()
+    batch = C.Kv8Batch(i([[0, 1], [2, 3]]), i([20, 5]), 4)
+    q, x = torch.zeros((4, 4, 64), dtype=BF16).cuda(), torch.zeros((4, 2, 64), dtype=BF16).cuda()
+    ws = C.make_kv8_workspace(cache, batch, 4)
+    bad = [
+        lambda: C.kv8_append(cache, batch, x[:3], x), lambda: C.kv8_append(cache, batch, x, x.half()),
+        lambda: C.kv8_append(cache, batch, x.double(), x.double()), lambda: C.kv8_append(cache, batch, x.cpu(), x),
+        lambda: C.kv8_append(cache, batch, x, x[:, :1]), lambda: C.kv8_append(cache, batch, x[..., :32], x),
+        lambda: C.kv8_append(cache, batch, x[:1].expand(4, 2, 64), x),
+        lambda: C.kv8_append(cache, batch, x.transpose(1, 2).contiguous().transpose(1, 2), x),
+        lambda: C.kv8_append(cache, batch, x[0], x), lambda: C.kv8_append(cache, batch, x, x, ws=ws.cpu()),
+        lambda: C.kv8_read(cache, batch, torch.float64), lambda: C.kv8_read(cache, batch, BF16, out_k=x.float()),
+        lambda: C.kv8_read(cache, batch, BF16, out_v=x[:2]), lambda: C.kv8_attn(q.float(), cache, batch),
+        lambda: C.kv8_attn(q, cache, batch, window=-1), lambda: C.kv8_attn(q, cache, batch, window=1 << 32),
+        lambda: C.kv8_attn(q, cache, batch, out=q.half()), lambda: C.kv8_attn(q, cache, batch, lse=q[:, :, 0]),
+        lambda: C.kv8_attn(q.cpu(), cache, batch), lambda: C.kv8_attn(q[:, :, ::2], cache, batch),
+        lambda: C.Kv8Batch(i([[0, 1], [2, 3]]), i([20, 5]), 3), lambda: C.Kv8Batch(i([0, 1]), i([20, 5]), 2),
+        lambda: C.Kv8Batch(i([[0, 1], [2, 3]]), i([20]), 4), lambda: C.Kv8Batch(i([[0], [2]]), i([1, 1]), 4, i([0, 4])),
+        lambda: C.Kv8Batch(i([[0], [2]]).long(), i([1, 1]), 4), lambda: C.Kv8Batch(i([[0], [2]]), i([1, 1]), -2),
+        lambda: C.Kv8Cache(cache.k[0], cache.v[0], cache.k_scale, cache.v_scale),
+        lambda: C.Kv8Cache(cache.k, cache.v[:2], cache.k_scale, cache.v_scale),
+        lambda: C.Kv8Cache(cache.k, cache.v, cache.k_scale[:, :1], cache.v_scale),
+        lambda: C.Kv8Cache(cache.k, cache.v, cache.k_scale, cache.v_scale.double()),
+    ]
+    for call in bad:
+        with pytest.raises(ValueError):
+            call()
+    for call in (lambda: C.kv8_attn(q[:, :3], cache, batch), lambda: C.kv8_attn(q, cache, batch, ws=ws[:256]),
+                 lambda: C.kv8_attn(q, cache, batch, causal=False, window=3),
+                 lambda: C.kv8_attn(q, cache, batch, softmax_scale=0.0),
+                 lambda: C.kv8_append(cache, batch, x, x, ws=ws[:128]),
+                 lambda: C.kv8_append(C.Kv8Cache.empty(4, 2, 24, 64), batch, x, x)):
+        with pytest.raises(C.Csa2Error):
+            call()
 
 
 def test_calls_on_two_streams_with_their_own_workspaces(C):
