@@ -187,11 +187,24 @@ __device__ __forceinline__ F2 add2(F2 a, F2 b) {
 // others do not.
 constexpr int kRagged = 1, kEdge = 2;
 
-// Columns key .. key + 31 of S that the row does not see become -infinity.
-__device__ __forceinline__ void mask32(uint32_t* s, int key, int rlo, int rhi) {
+// Columns of S (a tile's, from address ts) outside the row's [lo, hi) become
+// -infinity.  Not inlined: the code of the roles shares the SM's instruction cache,
+// and the softmax keeps its registers.
+__device__ __noinline__ void mask_tile(uint32_t ts, int lo, int hi) {
+#pragma unroll 1
+  for (int i = 0; i < kTileE; i += 32) {
+    if (!__any_sync(0xffffffffu, lo > i || hi < i + 32)) continue;
+    const int l = max(0, min(32, lo - i)), h = max(0, min(32, hi - i));
+    const uint32_t seen = __funnelshift_lc(0xFFFFFFFFu, 0u, h) & __funnelshift_lc(0u, 0xFFFFFFFFu, l);
+    uint32_t x[32];
+    tmem_ld32(ts + i, x);
+    tmem_wait_ld32(x);
 #pragma unroll
-  for (int i = 0; i < 32; ++i)
-    if (key + i < rlo || key + i >= rhi) s[i] = 0xFF800000u;
+    for (int k = 0; k < 32; ++k)
+      if (!((seen >> k) & 1)) x[k] = 0xFF800000u;
+    tmem_st32(ts + i, x);
+  }
+  tmem_wait_st();
 }
 
 // `bytes` contiguous bytes of global memory into shared memory, completing on bar.
@@ -220,6 +233,58 @@ __device__ __forceinline__ void put16(uint8_t* atom, int e, int c4, uint4 w) {
   const uint2 c = e4m3x4_to_f16x4(w.z), d = e4m3x4_to_f16x4(w.w);
   *reinterpret_cast<uint4*>(row + (((2 * c4) ^ (e & 7)) << 4)) = make_uint4(a.x, a.y, b.x, b.y);
   *reinterpret_cast<uint4*>(row + (((2 * c4 + 1) ^ (e & 7)) << 4)) = make_uint4(c.x, c.y, d.x, d.y);
+}
+
+// 32 rows of a unit's Q (from row `first`), scaled to a largest magnitude in [1, 2),
+// into the warp's part of their row tile; returns the exponent of the lane's row.
+// D / 8 lanes take a row (a lane that takes a row of its own touches 32 lines an
+// instruction).  Not inlined: the softmax keeps its registers.
+template <int D, bool kBf16>
+__device__ __noinline__ int load_rows(const Kv8AttnArgs& a, uint8_t* qt, int first, int row0,
+                                      int head0, int nrow) {
+  constexpr int kLanes = D / 8, kAt = 32 / kLanes;  // lanes a row, rows an instruction
+  const int lane = threadIdx.x & 31;
+  int e = 0;
+#pragma unroll 1
+  for (int b = 0; b < 32; b += 8 * kAt) {
+    uint4 x[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int r = first + b + kAt * i + lane / kLanes, rt = over_g(a, r);
+      x[i] = r < nrow ? __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) +
+                                                            (int64_t)(row0 + rt) * a.q_stride +
+                                                            (int64_t)(head0 + r - rt * a.G) * D) +
+                              lane % kLanes)
+                      : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      uint32_t y[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+      if (kBf16) {
+        float mx = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 f = pair_to_float2<true>(y[j]);
+          mx = fmaxf(mx, fmaxf(fabsf(f.x), fabsf(f.y)));
+        }
+#pragma unroll
+        for (int o = 1; o < kLanes; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        const int E = row_exponent(mx);
+        const int mine = __shfl_sync(0xffffffffu, E, (lane % kAt) * kLanes);
+        if (lane / kAt == b / kAt + i) e = mine;
+        const float down = pow2f(-E);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 f = pair_to_float2<true>(y[j]);
+          y[j] = pack_f16(f.x * down, f.y * down);
+        }
+      }
+      *reinterpret_cast<uint4*>(qt + sw128_off((first & 127) + b + kAt * i + lane / kLanes,
+                                               8 * (lane % kLanes), kAtom)) =
+          make_uint4(y[0], y[1], y[2], y[3]);
+    }
+  }
+  return e;
 }
 
 template <int D, bool kBf16>
@@ -282,7 +347,6 @@ kv8_attn_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
     const uint32_t ts = tm_s + t * 128 + lane_base, to = tm_o + t * D + lane_base;
     const int row = t * 128 + quad * 32 + lane;
     uint8_t* qt = smem + L::q + t * L::tile;
-    const int qr = row & 127;
     uint32_t cnt = 0, units = 0;
     // the unit's row of this thread
     bool ok;
@@ -298,47 +362,12 @@ kv8_attn_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
         it += w.t1 - w.t0;
       }
     };
-    // The row of Q, scaled to a largest magnitude in [1, 2), into shared memory.
     auto load_q = [&]() {
-      const int i0 = w.first_row();
-      ok = row < w.rows(a.G);
+      const int i0 = w.first_row(), nrow = w.rows(a.G);
+      ok = row < nrow;
       const int tok = i0 + (ok ? row : 0) / a.G, head = w.h * a.G + (ok ? row % a.G : 0);
       orow = (int64_t)(w.d.row0 + tok) * a.H + head;
-      const uint4* src = reinterpret_cast<const uint4*>(
-          static_cast<const uint16_t*>(a.q) + (int64_t)(w.d.row0 + tok) * a.q_stride +
-          (int64_t)head * D);
-      float down = 1.0f;
-      crow = a.scale_log2;
-      if (kBf16) {
-        float mx = 0.0f;
-#pragma unroll 8
-        for (int i = 0; i < D / 8; ++i) {
-          const uint4 x = ok ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
-          const uint32_t y[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float2 f = pair_to_float2<true>(y[j]);
-            mx = fmaxf(mx, fmaxf(fabsf(f.x), fabsf(f.y)));
-          }
-        }
-        const int E = row_exponent(mx);
-        down = pow2f(-E);
-        crow *= pow2f(E);
-      }
-#pragma unroll 4
-      for (int i = 0; i < D / 8; ++i) {
-        const uint4 x = ok ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
-        uint32_t y[4] = {x.x, x.y, x.z, x.w};
-        if (kBf16) {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float2 f = pair_to_float2<true>(y[j]);
-            y[j] = pack_f16(f.x * down, f.y * down);
-          }
-        }
-        *reinterpret_cast<uint4*>(qt + sw128_off(qr, 8 * i, kAtom)) =
-            make_uint4(y[0], y[1], y[2], y[3]);
-      }
+      crow = a.scale_log2 * pow2f(load_rows<D, kBf16>(a, qt, row & ~31, w.d.row0 + i0, w.h * a.G, nrow));
       warp_arrive(&ctl.q_full[t]);
       rlo = w.u.lo;
       rhi = w.u.hi;
@@ -361,15 +390,7 @@ kv8_attn_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
         tc_fence_after();
         const float4* sc = ctl.sc[it & 3];
         if (__any_sync(0xffffffffu, key0 < rlo || key0 + kTileE > rhi)) {
-#pragma unroll 1
-          for (int i = 0; i < kTileE; i += 32) {  // (rolled: the code of the roles shares a cache)
-            uint32_t x[32];
-            tmem_ld32(ts + i, x);
-            tmem_wait_ld32(x);
-            mask32(x, key0 + i, rlo, rhi);
-            tmem_st32(ts + i, x);
-          }
-          tmem_wait_st();
+          mask_tile(ts, rlo - key0, rhi - key0);
         }
         // two halves of 64 keys (a loop: the code of all roles shares the SM's
         // instruction cache, and unrolled it misses)
@@ -573,14 +594,15 @@ kv8_attn_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
                     *reinterpret_cast<const uint4*>(raw + e * D + 16 * c));
             }
           } else {
-#pragma unroll 1
+            const uint8_t* raw_v = smem + L::rv;
+#pragma unroll 4
             for (int i = 0; i < 32 / kKeys; ++i) {
               const int e = 32 * dw + kKeys * i + sub;
               uint4 x = *reinterpret_cast<const uint4*>(raw + e * D + 16 * c);
+              const uint4 xv = *reinterpret_cast<const uint4*>(raw_v + e * D + 16 * c);
               if (key0 + e < lo || key0 + e >= hi || ctl.sc[it & 3][e >> 4].z == 0.0f) {
                 x = make_uint4(0, 0, 0, 0);
-              } else if ((marks & kEdge) &&
-                         has_nan(*reinterpret_cast<const uint4*>(smem + L::rv + e * D + 16 * c))) {
+              } else if ((marks & kEdge) && has_nan(xv)) {
                 // A weight of zero does not hide a NaN of V: where some rows see a key
                 // and others do not, its V codes become zeros and its K codes NaN,
                 // which the mask hides
@@ -637,6 +659,15 @@ kv8_attn_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
       };
       int pid = find(w.t0), next = find(w.t0 + 1);
       scales(pid);
+      // the unit's queries, for which the softmax would wait at the unit's start
+      for (int row = lane; row < w.rows(a.G); row += 32) {
+        const int tok = over_g(a, row);
+        const uint16_t* src = static_cast<const uint16_t*>(a.q) +
+                              (int64_t)(w.d.row0 + w.first_row() + tok) * a.q_stride +
+                              (int64_t)(h * a.G + row - tok * a.G) * D;
+#pragma unroll
+        for (int i = 0; i < D; i += 64) asm volatile("prefetch.global.L2 [%0];" ::"l"(src + i));
+      }
       for (int j = w.t0; j < t1; ++j, ++it) {
         const int key0 = (g0 + j) * kTileE, key = key0 + 16 * lane;
         const bool seen = pid >= 0 && key < hi && key + 16 > lo;
