@@ -25,15 +25,24 @@
 //   warps 12, 14    issue the MMAs of row tile 0, 1 (12: tensor memory too).  An
 //                   issuing warp is held until the tensor pipe has room, so that one
 //                   warp would come late to every barrier: the second issuer took
-//                   a chunk of 4096 rows over 16K tokens (32 heads over 8, D = 128) from 825 to 787 us
+//                   the chunk below from 825 to 787 us
 //   warp 13         loader: the block table and scales, and the codes of a tile's
 //                   pages into shared memory by bulk copies (through L2, where the
 //                   units of a sequence share them); a tile's K is requested while
 //                   its predecessor's V is converted and the reverse
 //   (warp 15 only completes its warpgroup, for the register split)
-// Measured before the loader had a warp of its own (the dequantisers looked up
-// pages and scales and loaded to registers): 6600 cycles a pair of tiles against
-// the 2048 of its MMAs, 3000 of them in those dependent loads.
+// Measured (GB300; cuBLAS bf16 1.89 PFLOP/s): a chunk of 4096 rows over 16K tokens
+// (32 heads over 8, D = 128) 769 us, 1.25 PFLOP/s of products that the mask leaves,
+// 66 %; tensor pipe 56 % busy, XU 28 %, 46 % of issue slots.  A tile of keys takes
+// 3300 to 3700 cycles, of which its MMAs 2048 (D = 128); each row tile goes through
+// softmax (1950 cycles, two warps a scheduler), P to O, S again, one after the other,
+// since P overwrites S.  Prompts of 10007 rows through a window of 1024 (16 heads
+// over 4, D = 64): 96 us.  There a unit has 8 clean tiles (softmax-bound as above:
+// D = 64 halves only the MMAs), 2 to 3 at the mask's edges with 1200 cycles more, and
+// 5000 cycles from its last tile to the next unit's first.
+// Before the loader had a warp of its own (the dequantisers looked up pages and
+// scales and loaded to registers): 6600 cycles a pair of tiles, 3000 of them in
+// those dependent loads.
 // Every wait is bounded (about 2 s): a role that gives up sets the timeout
 // status and leaves, the others follow, and tensor memory is freed.
 #include "kv8_sched.cuh"
