@@ -243,18 +243,24 @@ kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a) {
   int pids, pids_next;        // pages of the requested block of 16 tiles and of the next
   // page ids of tiles i .. i + 15 of the unit's: lane l has tile i + l % 16, its
   // 16-key half l / 16; -1: nothing of the half is seen, or the entry is outside the cache
-  auto pages = [&](const Walk<typename C::Work>& u, int i) -> int {
+  // (in two steps, the table's entry and its check, for what may run between them)
+  auto seen_key = [&](const Walk<typename C::Work>& u, int i) -> int {  // -1: nothing is seen
     const int t = u.t0 + i + (lane & 15);
     const int key = (u.u.g0 + t) * C::granule + warp * kTileKeys + (lane & 16);
-    int p = -1;
-    if (t < u.t1 && key < u.u.hi && key + 16 > u.u.lo) {
-      p = a.c.table[(int64_t)u.s * a.c.max_pages + (key >> a.c.page_shift)];
-      if (p < 0 || p >= a.c.n_pages) {
-        set_status(a.c.status, kStatusBadIndex);
-        p = -1;
-      }
-    }
-    return p;
+    return t < u.t1 && key < u.u.hi && key + 16 > u.u.lo ? key : -1;
+  };
+  auto entry = [&](const Walk<typename C::Work>& u, int key) -> int {
+    return key < 0 ? 0 : a.c.table[(int64_t)u.s * a.c.max_pages + (key >> a.c.page_shift)];
+  };
+  auto page_or_none = [&](int key, int p) -> int {
+    if (key < 0) return -1;
+    if (p >= 0 && p < a.c.n_pages) return p;
+    set_status(a.c.status, kStatusBadIndex);
+    return -1;
+  };
+  auto pages = [&](const Walk<typename C::Work>& u, int i) -> int {
+    const int key = seen_key(u, i);
+    return page_or_none(key, entry(u, key));
   };
   // Requests the unit's next tile (an empty group of copies past its last).  A half
   // is 16 * D contiguous bytes of a page.
@@ -320,10 +326,11 @@ kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a) {
       qrows = fetch_q<D>(a, w.d.row0 + w.first_row(), w.h * a.G, qtile * 16 + g, w.rows(a.G), c);
   };
 
-  // the unit's first loads, all in flight together: Q ahead of the copies, which
-  // fill the memory's queues
+  // the unit's first loads, all in flight together: the pages, which the copies wait
+  // for, then Q, ahead of the copies, which fill the memory's queues
+  const int key0 = seen_key(w, 0), entry0 = entry(w, key0);
   fetch();
-  open_unit(pages(w, 0));
+  open_unit(page_or_none(key0, entry0));
 #pragma unroll 1
   for (int i = 0; i < C::stages - 1; ++i) request();
   int st = 0;
@@ -611,7 +618,7 @@ kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a) {
     __syncthreads();
     float* pw = scratch_part(a, gridDim.x, blockIdx.x, starts, C::unit, D);
     constexpr int kTpr = D / 4;  // threads per row
-#pragma unroll 4
+#pragma unroll 1
     for (int i = 0; i < C::unit * kTpr / kThreads; ++i) {
       const int row = (i * kThreads + tid) / kTpr, ch = (tid % kTpr) * 4;
       if (row >= nrow) continue;

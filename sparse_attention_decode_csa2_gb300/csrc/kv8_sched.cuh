@@ -133,10 +133,9 @@ __device__ Range find_range(const Kv8AttnArgs& a, int worker, int workers,
     for (int m = lane; m < d.nm; m += 32) w += unit_places<Sh>(a, unit_span<Sh>(a, d, m));
     return warp_total(w) * a.c.H_kv;
   };
-  // work of sequence base + lane (0 past s1)
-  auto chunk = [&](int base) -> int64_t {
+  // work of sequence base + lane (0 past s1), and its dimensions
+  auto chunk = [&](int base, Dims& d) -> int64_t {
     const int s = base + lane;
-    Dims d;
     d.nm = 0;
     if (s < s1) {
       d = seq_dims<Sh>(a, s);
@@ -152,14 +151,18 @@ __device__ Range find_range(const Kv8AttnArgs& a, int worker, int workers,
     }
     return w;
   };
-  int64_t mine = 0, first = 0;
-  for (int b = s0; b < s1; b += 32) {
-    const int64_t w = chunk(b);
-    if (b == s0) first = w;
-    mine += w;
+  Dims d0;  // of the warp's first 32 sequences
+  const int64_t first = chunk(s0, d0), first_inc = warp_scan(first, lane);
+  int64_t mine = __shfl_sync(0xffffffffu, first_inc, 31);
+  if (s0 + 32 < s1) {
+    int64_t more = 0;
+    for (int b = s0 + 32; b < s1; b += 32) {
+      Dims d;
+      more += chunk(b, d);
+    }
+    mine += warp_total(more);
   }
   if (bad) set_status(a.c.status, kStatusBadIndex);
-  mine = warp_total(mine);
   if (lane == 0) sm.warp_sum[warp] = mine;
   if (tid == 0) sm.s = -1;
   __syncthreads();
@@ -177,12 +180,28 @@ __device__ Range find_range(const Kv8AttnArgs& a, int worker, int workers,
   if (r.w0 < r.w1 && r.w0 >= base && r.w0 < base + mine) {  // this warp's sequences hold w0
     int64_t at = base;
     for (int b = s0; b < s1; b += 32) {
-      const int64_t w = b == s0 ? first : chunk(b);
-      const int64_t inc = warp_scan(w, lane);
+      Dims db;
+      const int64_t w = b == s0 ? first : chunk(b, db);
+      const int64_t inc = b == s0 ? first_inc : warp_scan(w, lane);
       const uint32_t past = __ballot_sync(0xffffffffu, r.w0 < at + inc);
       if (past) {
         const int l = __ffs(past) - 1;
         const int s = b + l;
+        // (the short way takes 1000 cycles less before a CTA's first load)
+        if (b == s0 && __shfl_sync(0xffffffffu, d0.nm, l) == 1) {
+          if (lane == l) {
+            const int64_t rem = r.w0 - at - (inc - w);
+            const Span u = unit_span<Sh>(a, d0, 0);
+            const int n = unit_places<Sh>(a, u);
+            sm.s = s;
+            sm.m = 0;
+            sm.h = (int)quotient(rem, n);
+            sm.c0 = (int)(rem - (int64_t)sm.h * n);
+            sm.d = d0;
+            sm.u = u;
+          }
+          break;
+        }
         int64_t rem = r.w0 - at - __shfl_sync(0xffffffffu, inc - w, l);
         const Dims d = seq_dims<Sh>(a, s);
         // the block of rows: 32 at a time
