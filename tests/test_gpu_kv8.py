@@ -289,6 +289,27 @@ def test_attn_prompt_rows_with_growing_logits(C, D):
     _check_attn(C, w, q, None, scale=0.3)
 
 
+@pytest.mark.parametrize("wide", [None, 40])
+@pytest.mark.parametrize("S,G,choices", [(300, 1, [1]), (300, 4, [0, 1, 1, 1, 2, 5, 20]), (560, 16, [0, 1, 2, 3, 4, 30])])
+def test_attn_many_sequences(C, S, G, choices, wide):
+    # more sequences than the warps of a CTA look at in one step, some of several blocks of rows
+    rng = np.random.default_rng(S + G)
+    n = rng.choice(choices, S)
+    lens = [int(m + x) for m, x in zip(n, rng.integers(0, 60, S))]
+    w = World(C, 71, lens, 1, 64, 16, wide=wide).fill()
+    cu = np.concatenate([[0], np.cumsum(n)]).tolist()
+    _check_attn(C, w, _q(w.rng, cu[-1], G, 64, BF16), cu)
+
+
+@pytest.mark.parametrize("n", [1, 50])
+def test_attn_sequences_may_share_pages(C, n):
+    # a prefix that two sequences share, and a page that one of them has twice
+    w = World(C, 72, [160, 160, 100], 2, 64, 32).fill()
+    w.table[1, :3] = w.table[0, :3]
+    w.table[2, 1] = w.table[2, 0]
+    _check_attn(C, w, _q(w.rng, 3 * n, 4, 64, BF16), None)
+
+
 def test_attn_long_context_split_over_the_grid(C):
     # two sequences, one head: the tokens are split over every CTA and joined
     lens = [5000, 3001]
