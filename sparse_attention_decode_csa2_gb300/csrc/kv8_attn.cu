@@ -28,11 +28,11 @@
 //
 // A warp takes 32 keys at a time through its own ring of shared-memory stages
 // (16-byte asynchronous copies, swizzled); the warps of a CTA do not wait for one
-// another before they join their sums.  K fragments are plain 16-byte shared loads (the channel order of the
-// contraction is permuted so that a lane's 16 bytes are its four k-steps), V
-// fragments come from transposing matrix loads of bytes, whose four bytes are a
-// lane's keys of a k-step when S's columns are permuted to match; both are
-// converted in registers (E4M3 -> fp16 is one instruction for two values).
+// another before they join their sums.  K fragments are plain 16-byte shared loads
+// (the channel order of the contraction is permuted so that a lane's 16 bytes are
+// its four k-steps), V fragments come from transposing matrix loads of bytes, whose
+// four bytes are a lane's keys of a k-step when S's columns are permuted to match;
+// both are converted in registers (E4M3 -> fp16 is one instruction for two values).
 //
 // The running maximum is lazy: weights are formed with the old one, which gives
 // the key at the reference a weight of 2^7, and only where a sum of them leaves
@@ -42,12 +42,12 @@
 // Measured (GB300; the copy peak is 6.77 TB/s):
 //   one token of 32 sequences of up to 64K tokens (64 heads over 8, D = 128):
 //     465 us, 6.8 TB/s: the copy's rate
-//   17 sequences of up to 9K tokens (40 heads over 8, D = 64): 34.7 us (3.2 TB/s).
-//     Of them 5 us go before the first tile (ranges, pages, first loads) and 3 at
-//     the end; between, the warps wait for the results of their own instructions
+//   17 sequences of up to 9K tokens (40 heads over 8, D = 64): 34.5 us (3.2 TB/s).
+//     Of them 5 us go before the first tile (ranges, pages, first loads) and 4 to
+//     the merge; between, 5.9 TB/s: the warps wait for their own loads and results
 //     (12 warps an SM: the registers of O and of the codes in flight)
 //   4 drafted tokens of 24 sequences of up to 16K tokens (32 heads over 4, D = 128;
-//     32 rows a KV head): 89 us (3.3 TB/s), tensor pipe 40 % busy, 35 % of issue
+//     32 rows a KV head): 88 us (3.4 TB/s), tensor pipe 40 % busy, 35 % of issue
 //     slots: the same waits, with eight warps an SM
 #include "kv8_sched.cuh"
 
@@ -686,9 +686,11 @@ cudaError_t attn_t(const Kv8AttnArgs& args, cudaStream_t stream) {
 }
 
 // Rows of a KV head (per sequence, on average) up to which the kernel of 16 rows
-// and that of 32 are taken.  At 64 rows a warp of 32 rows and its neighbour would
-// convert every tile twice (24 x 16K tokens, D = 128: 146 us); the tcgen05 kernel
-// takes 117 us there, and 114 us at 32 rows, where this one takes 88.
+// and that of 32 are taken.  Measured: one token of 32 sequences of 64K (8 rows) 464
+// us with 16, 700 with 32; 17 sequences of 9K (5 rows, D = 64) 34.4 and 45.2; drafts
+// (32 rows, D = 128) 103 with 16, whose units read the cache twice, 88 with 32 and
+// 114 with the tcgen05 kernel.  At 64 rows the tcgen05 kernel takes 117 us, two
+// warps of 32 rows that share the keys took 146 (both convert every tile).
 constexpr int64_t kRows1 = 16, kRows2 = 32;
 // Units of up to so many keys are not cut: one CTA takes 3 to 4 us for 512 keys,
 // what the merge kernel would add (128 sequences of 1000 tokens: 58 us cut, 64 us
