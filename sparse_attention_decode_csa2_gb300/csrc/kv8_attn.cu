@@ -689,8 +689,9 @@ cudaError_t attn_t(const Kv8AttnArgs& args, cudaStream_t stream) {
 // and that of 32 are taken.  Measured: one token of 32 sequences of 64K (8 rows) 464
 // us with 16, 700 with 32; 17 sequences of 9K (5 rows, D = 64) 34.4 and 45.2; drafts
 // (32 rows, D = 128) 103 with 16, whose units read the cache twice, 88 with 32 and
-// 114 with the tcgen05 kernel.  At 64 rows the tcgen05 kernel takes 117 us, two
-// warps of 32 rows that share the keys took 146 (both convert every tile).
+// 114 with the tcgen05 kernel.  Of 40 to 64 rows there the tcgen05 kernel takes 122
+// us (D = 64: 97), units of 32 rows 152 (101); two warps of 32 rows that share the keys
+// took 146 (both convert every tile).
 constexpr int64_t kRows1 = 16, kRows2 = 32;
 // Units of up to so many keys are not cut: one CTA takes 3 to 4 us for 512 keys,
 // what the merge kernel would add (128 sequences of 1000 tokens: 58 us cut, 64 us
