@@ -41,13 +41,13 @@
 //
 // Measured (GB300; the copy peak is 6.77 TB/s):
 //   one token of 32 sequences of up to 64K tokens (64 heads over 8, D = 128):
-//     465 us, 6.8 TB/s: the copy's rate
-//   17 sequences of up to 9K tokens (40 heads over 8, D = 64): 34.5 us (3.2 TB/s).
+//     463 us, 6.9 TB/s: the copy's rate
+//   17 sequences of up to 9K tokens (40 heads over 8, D = 64): 32.8 us (3.4 TB/s).
 //     Of them 5 us go before the first tile (ranges, pages, first loads) and 4 to
 //     the merge; between, 5.9 TB/s: the warps wait for their own loads and results
 //     (12 warps an SM: the registers of O and of the codes in flight)
 //   4 drafted tokens of 24 sequences of up to 16K tokens (32 heads over 4, D = 128;
-//     32 rows a KV head): 88 us (3.4 TB/s), tensor pipe 40 % busy, 35 % of issue
+//     32 rows a KV head): 86 us (3.5 TB/s), tensor pipe 40 % busy, 35 % of issue
 //     slots: the same waits, with eight warps an SM
 #include "kv8_sched.cuh"
 
@@ -68,8 +68,9 @@ template <int D, int kMt>
 struct Cfg {
   static constexpr int unit = 16 * kMt;                    // query rows
   static constexpr int granule = kWarps * kTileKeys;       // keys
-  // a unit's queries and output take about as long as 128 keys
-  using Work = Shape<unit, granule, 1>;
+  // a unit's queries and output count as three granules (17 sequences of 9K tokens, D =
+  // 64, with none to four: 43.6, 34.3, 32.9, 32.8, 32.8 us; drafts 89, 88, 86.4, 86.0, 86.5)
+  using Work = Shape<unit, granule, 3>;
   static constexpr int stages = D == 128 ? 3 : 4;
   static constexpr int tile = kTileKeys * D;               // bytes of K (or V) of a stage
   static constexpr int stage = 2 * tile;

@@ -70,6 +70,8 @@ constexpr float kHeadroom = 7.0f, kMostSum = 57344.0f;
 // multiply-add: its rounding is then at most 2^-8 of a power of two, that of the
 // logits themselves.
 constexpr float kFused = 65536.0f;
+// (a unit's queries and output count as two granules: prompts of 10007 rows through a
+// window of 1024 with one to three 104.5, 96.6, 97.6 us)
 using Work = Shape<kUnit, kTileE, 2>;
 constexpr uint32_t kAtom = 128 * 128;            // bytes: 128 rows of 64 fp16 channels
 
