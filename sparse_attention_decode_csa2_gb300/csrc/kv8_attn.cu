@@ -682,8 +682,9 @@ cudaError_t attn_t(const Kv8AttnArgs& args, cudaStream_t stream) {
   e = launch_kernel(kv8_attn_kernel<D, kMt, kBf16>, dim3(workers), dim3(kThreads), C::smem,
                     stream, /*pdl=*/false, a);
   if (e != cudaSuccess || a.uncut) return e;
-  return launch_kernel(kv8_merge_kernel<D, kMt, kBf16>, dim3(workers, merge_blocks<typename C::Work, D>(a)),
-                       dim3(kThreads), 0, stream, /*pdl=*/true, a, workers);
+  const dim3 grid(workers, merge_blocks<typename C::Work, D>(a, workers));
+  return launch_kernel(kv8_merge_kernel<D, kMt, kBf16>, grid, dim3(kThreads), 0, stream,
+                       /*pdl=*/true, a, workers);
 }
 
 // Rows of a KV head (per sequence, on average) up to which the kernel of 16 rows

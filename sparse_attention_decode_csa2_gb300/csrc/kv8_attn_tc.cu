@@ -812,8 +812,9 @@ cudaError_t attn_tc_t(const Kv8AttnArgs& args, cudaStream_t stream) {
   e = launch_kernel(kv8_attn_tc_kernel<D, kBf16>, dim3(workers), dim3(kThreads), L::alloc, stream,
                     /*pdl=*/false, a);
   if (e != cudaSuccess || a.uncut) return e;
-  return launch_kernel(kv8_merge_tc_kernel<D, kBf16>, dim3(workers, merge_blocks<Work, D>(a)), dim3(128), 0, stream,
-                       /*pdl=*/true, a, workers);
+  const dim3 grid(workers, merge_blocks<Work, D>(a, workers));
+  return launch_kernel(kv8_merge_tc_kernel<D, kBf16>, grid, dim3(128), 0, stream, /*pdl=*/true, a,
+                       workers);
 }
 
 }  // namespace

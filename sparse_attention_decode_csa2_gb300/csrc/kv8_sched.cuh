@@ -413,12 +413,17 @@ template <class Sh, int D>
 constexpr int merge_rows() {  // rows of a block of four warps
   return 4 / (D / 32);
 }
-// Blocks for a worker's unit: a row group each for up to 16 rows.
+// Blocks for a worker's unit: a row group each for up to 16 rows, or, where the units
+// are few and so of many parts, up to 128.  (One token of 60000, 64 heads over 1, D =
+// 128: 31 us with 128, 42 with 16; two of 50000, 128 heads: 52 and 114.  Batches of
+// many units would start thousands of blocks for nothing.)
 template <class Sh, int D>
-int merge_blocks(const Kv8AttnArgs& a) {
+int merge_blocks(const Kv8AttnArgs& a, int workers) {
   const int64_t most = a.c.cu ? Sh::kUnit : (int64_t)(a.c.T / a.c.S) * a.G;
   const int rows = (int)(most < Sh::kUnit ? most : Sh::kUnit);
-  return ((rows < 16 ? rows : 16) + merge_rows<Sh, D>() - 1) / merge_rows<Sh, D>();
+  const int64_t units = ((int64_t)a.c.S + a.c.T / a.tpu) * a.c.H_kv;
+  const int cap = units * 4 <= workers ? 128 : 16;
+  return ((rows < cap ? rows : cap) + merge_rows<Sh, D>() - 1) / merge_rows<Sh, D>();
 }
 template <class Sh, int D, bool kBf16>
 __device__ __forceinline__ void merge_parts(const Kv8AttnArgs& a, int workers, float headroom) {
