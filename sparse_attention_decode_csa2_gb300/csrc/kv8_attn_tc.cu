@@ -448,6 +448,10 @@ kv8_attn_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
             }
           }
           if (slow) {  // the reference moves to the half's largest exponent where that is past it
+            // The first half's weights, and O as the first half left it, are read
+            // back below: their stores are waited for (loads from tensor memory are
+            // not ordered behind stores).
+            tmem_wait_st();
             float x = -INFINITY;
 #pragma unroll 1
             for (int i = 0; i < 2; ++i) {
