@@ -315,6 +315,7 @@ kv8_attn_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
   Walk<Work>& w = ctl.walk[min(warp, kMmaWarp1)];
   bool any = false;
   if (warp <= kMmaWarp1) any = warp_start(w, a, rg, rsm);
+  proxy_fence();  // (of the range's record, before the loader's copies land on it)
   if (!__syncthreads_or(any)) {  // no range, or one that ends within a unit's fixed cost
     if (tid == 0) write_cut(a, Cut{-1, 0, 0, 0});
     return;
@@ -614,10 +615,10 @@ kv8_attn_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
             for (int i = 0; i < 32 / kKeys; ++i) {
               const int e = 32 * dw + kKeys * i + sub;
               uint4 x = *reinterpret_cast<const uint4*>(raw + e * D + 16 * c);
-              const uint4 xv = *reinterpret_cast<const uint4*>(raw_v + e * D + 16 * c);
               if (key0 + e < lo || key0 + e >= hi || ctl.sc[it & 3][e >> 4].z == 0.0f) {
                 x = make_uint4(0, 0, 0, 0);
-              } else if ((marks & kEdge) && has_nan(xv)) {
+              } else if ((marks & kEdge) &&  // (only there have V's codes been waited for)
+                         has_nan(*reinterpret_cast<const uint4*>(raw_v + e * D + 16 * c))) {
                 // A weight of zero does not hide a NaN of V: where some rows see a key
                 // and others do not, its V codes become zeros and its K codes NaN,
                 // which the mask hides
