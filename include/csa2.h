@@ -374,8 +374,9 @@ csa2_status csa2_sparse_attn_fp4_noalloc(const uint16_t* q_bf16, const uint8_t* 
  * status: a block-table entry outside [0, n_pages) where a token is needed
  * (nothing is written; reads as zeros; not seen), kv_len[s] < 0 or past
  * max_pages * page (the tokens past it are skipped), cu_rows that decrease or
- * leave [0, T] (the sequence has no rows).  Entries for tokens outside a
- * sliding window are never read.
+ * leave [0, T] (the sequence has no rows; the others keep theirs, and a row of the
+ * step that two of them then claim reads back, or yields, what either has there).
+ * Entries for tokens outside a sliding window are never read.
  *   Sequences may share pages that the step does not write.
  * Supported: D in {64, 128}, page in {16, 32, 64, 128}, max_pages * page <= 2^30,
  * n_pages < 2^31, T <= 2^28, S <= 2^24, H_kv <= 2^14; else

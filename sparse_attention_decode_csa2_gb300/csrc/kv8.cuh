@@ -46,14 +46,6 @@ __device__ __forceinline__ Kv8Seq kv8_seq(const Kv8Args& a, int s) {
               : kv8_seq_of(a, s * n, s * n + n, a.kv_len[s]);
 }
 
-// Raises the bad-index bit if any sequence's entries make no sense (one
-// block's threads look at all of them).
-__device__ __forceinline__ void kv8_check_batch(const Kv8Args& a) {
-  bool bad = false;
-  for (int s = threadIdx.x; s < a.S; s += blockDim.x) bad |= kv8_seq(a, s).bad;
-  if (bad) set_status(a.status, kStatusBadIndex);
-}
-
 // Page id of column `col` (< max_pages) of sequence s, or -1 (and the
 // bad-index bit) for an entry outside the cache.
 __device__ __forceinline__ int64_t kv8_page(const Kv8Args& a, int s, int col) {

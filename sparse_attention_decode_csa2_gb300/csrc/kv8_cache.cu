@@ -123,62 +123,31 @@ __device__ __forceinline__ void decode16(uint4 c, float* x) {
 // pages its rows can touch: n rows touch at most (n + page - 2) / page + 1
 // pages.  With equal shares that is the count; with cu, sequence s owns slots
 // [cu[s] / page + 2 s, cu[s + 1] / page + 2 s + 2), which is at least as many
-// and needs no prefix sum, so a slot finds its sequence by bisection.
+// and needs no prefix sum, so a slot finds its sequence by bisection.  Offsets
+// that decrease or leave [0, T] break the order that the bisection goes by: the
+// slots that it then misses are the last block's (lost_slots).
+__host__ __device__ inline int64_t pages_of(int64_t n, int page_shift) {
+  return ((n + ((int64_t)1 << page_shift) - 2) >> page_shift) + 1;
+}
 __host__ __device__ inline int64_t slots_of(int S, int T, bool cu, int page_shift) {
-  const int64_t page = (int64_t)1 << page_shift;
   if (cu) return ((int64_t)T >> page_shift) + 2 * (int64_t)S;
-  const int64_t n = T / S;
-  return (int64_t)S * ((n + page - 2) / page + 1);
+  return (int64_t)S * pages_of(T / S, page_shift);
+}
+// Sequence s's first slot, from its entry of cu.
+__device__ __forceinline__ int64_t slot_base(const Kv8Args& a, int s, int cu) {
+  return (int64_t)(min(max(cu, 0), a.T) >> a.page_shift) + 2 * (int64_t)s;
 }
 
-// The rows of the step that a slot stands for: page column `col` of sequence
-// s, tokens [pos, pos + rows), the first of them row `row` of the step.
-// rows = 0: nothing to do.
+// The rows of the step that slot j of sequence s stands for: page column `col`,
+// tokens [pos, pos + rows), the first of them row `row` of the step.  rows = 0:
+// nothing to do.
 struct Slot {
   int s, j, col, pos, rows, row;
   Kv8Seq q;
 };
 
-__device__ __forceinline__ Slot find_slot(const Kv8Args& a, int64_t slot) {
-  Slot r;
-  if (a.cu) {
-    // last s with clamp(cu[s]) / page + 2 s <= slot, 32 candidates a round (every
-    // lane of a warp has the same slot); the last round has the sequence's entries
-    const int lane = threadIdx.x & 31;
-    int lo = 0, hi = a.S, step;
-    do {
-      step = (hi - lo + 31) / 32;
-      const int c = lo + lane * step;
-      int cu = 0, next = 0, len = 0;
-      bool le = false;
-      if (c < hi) {
-        cu = a.cu[c];
-        if (step == 1) {
-          next = a.cu[c + 1];
-          len = a.kv_len[c];
-        }
-        le = lane == 0 || ((int64_t)(min(max(cu, 0), a.T) >> a.page_shift) + 2 * (int64_t)c) <= slot;
-      }
-      const int k = 31 - __clz(__ballot_sync(0xffffffffu, le));  // the highest that is not past the slot
-      lo += k * step;
-      hi = min(hi, lo + step);
-      if (step == 1) {
-        cu = __shfl_sync(0xffffffffu, cu, k);
-        next = __shfl_sync(0xffffffffu, next, k);
-        len = __shfl_sync(0xffffffffu, len, k);
-        r.q = kv8_seq_of(a, cu, next, len);
-        const int64_t j = slot - ((int64_t)(min(max(cu, 0), a.T) >> a.page_shift) + 2 * (int64_t)lo);
-        r.j = j < 0 || j > INT32_MAX ? INT32_MAX : (int)j;
-      }
-    } while (step > 1);
-    r.s = lo;
-  } else {
-    const int64_t page = (int64_t)1 << a.page_shift;
-    const int64_t per = ((int64_t)(a.T / a.S) + page - 2) / page + 1;
-    r.s = (int)(slot / per);
-    r.j = (int)(slot % per);
-    r.q = kv8_seq(a, r.s);
-  }
+// r.s, r.j and r.q are set.
+__device__ __forceinline__ void slot_rows(const Kv8Args& a, Slot& r) {
   const int cap = (int)min((int64_t)r.q.len, (int64_t)a.max_pages << a.page_shift);
   const int64_t first = (int64_t)r.q.len - r.q.n;  // token of the sequence's row 0
   const int p0 = first < 0 ? 0 : (int)first;
@@ -189,7 +158,91 @@ __device__ __forceinline__ Slot find_slot(const Kv8Args& a, int64_t slot) {
   r.pos = (int)(lo < cap ? lo : cap);
   r.rows = r.q.n > 0 && r.col < a.max_pages && hi > lo ? (int)(hi - lo) : 0;
   r.row = r.q.row0 + (int)(lo - first);
+}
+
+// With cu: the last sequence s whose first slot is not past `slot`, 32 candidates a
+// round (every lane of a warp has the same slot); the last round has the
+// sequence's entries.
+__device__ __forceinline__ void search_slot(const Kv8Args& a, int64_t slot, Slot& r) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, hi = a.S, step;
+  do {
+    step = (hi - lo + 31) / 32;
+    const int c = lo + lane * step;
+    int cu = 0, next = 0, len = 0;
+    bool le = false;
+    if (c < hi) {
+      cu = a.cu[c];
+      if (step == 1) {
+        next = a.cu[c + 1];
+        len = a.kv_len[c];
+      }
+      le = lane == 0 || slot_base(a, c, cu) <= slot;
+    }
+    const int k = 31 - __clz(__ballot_sync(0xffffffffu, le));  // the highest that is not past the slot
+    lo += k * step;
+    hi = min(hi, lo + step);
+    if (step == 1) {
+      cu = __shfl_sync(0xffffffffu, cu, k);
+      next = __shfl_sync(0xffffffffu, next, k);
+      len = __shfl_sync(0xffffffffu, len, k);
+      r.q = kv8_seq_of(a, cu, next, len);
+      const int64_t j = slot - slot_base(a, lo, cu);
+      r.j = j < 0 || j > INT32_MAX ? INT32_MAX : (int)j;
+    }
+  } while (step > 1);
+  r.s = lo;
+}
+
+__device__ __forceinline__ Slot find_slot(const Kv8Args& a, int64_t slot) {
+  Slot r;
+  if (a.cu) {
+    search_slot(a, slot, r);
+  } else {
+    const int64_t per = pages_of(a.T / a.S, a.page_shift);
+    r.s = (int)(slot / per);
+    r.j = (int)(slot % per);
+    r.q = kv8_seq(a, r.s);
+  }
+  slot_rows(a, r);
   return r;
+}
+
+// The last block: raises the bad-index bit if any sequence's entries make no sense.
+// True (to all threads) if it is cu's, so that slots may be lost.
+__device__ __forceinline__ bool check_batch(const Kv8Args& a) {
+  bool bad = false, order = false;
+  for (int s = threadIdx.x; s < a.S; s += blockDim.x) {
+    bad |= kv8_seq(a, s).bad;
+    if (a.cu) order |= a.cu[s] < 0 || a.cu[s + 1] < a.cu[s] || a.cu[s + 1] > a.T;
+  }
+  if (bad) set_status(a.status, kStatusBadIndex);
+  return __syncthreads_or(order);
+}
+
+// The slots of sound sequences that the search gives to others, one after the other
+// (every thread of the block; `take` has the slot).  For a batch that should not be:
+// it may take its time.
+template <class Take>
+__device__ __forceinline__ void lost_slots(const Kv8Args& a, Take&& take) {
+  const int64_t slots = slots_of(a.S, a.T, true, a.page_shift);
+  for (int s = 0; s < a.S; ++s) {
+    Slot r;
+    r.s = s;
+    r.q = kv8_seq(a, s);
+    if (r.q.n == 0) continue;
+    const int64_t base = slot_base(a, s, a.cu[s]);
+    const int n = (int)pages_of(r.q.n, a.page_shift);
+    for (r.j = 0; r.j < n; ++r.j) {
+      if (base + r.j < slots) {
+        Slot at;
+        search_slot(a, base + r.j, at);
+        if (at.s == s) continue;  // a team has it
+      }
+      slot_rows(a, r);
+      take(r);
+    }
+  }
 }
 
 template <int kTeam>
@@ -210,20 +263,15 @@ __device__ __forceinline__ float team_max(float x, float* red) {
   return x;
 }
 
-template <typename T, int kTeam>
-__global__ void __launch_bounds__(block_of<kTeam>(), (kTeam == 32 ? 4 : 8) / (sizeof(T) / 2))
-kv8_append_kernel(const __grid_constant__ Kv8Args a, const T* __restrict__ k,
-                  const T* __restrict__ v, int64_t k_stride, int64_t v_stride, int64_t items) {
-  __shared__ float red[kTeam / 32];
-  const int64_t item = (int64_t)blockIdx.x * (block_of<kTeam>() / kTeam) + threadIdx.x / kTeam;
-  if (item >= items) {
-    kv8_check_batch(a);  // the threads behind the last item (there are some) look for bad entries
-    return;
-  }
+// Rows of the step into one block: (page of the slot, head, K or V), by one team.
+// One pass over the rows: the first kHold chunks of a thread stay in registers (four: a
+// page of 64 rows of 128 channels for a team of 128), the rest are read again.
+template <typename T, int kTeam, int kHold>
+__device__ __forceinline__ void append_block(const Kv8Args& a, const T* __restrict__ k,
+                                             const T* __restrict__ v, int64_t k_stride,
+                                             int64_t v_stride, const Slot& sl, int h, bool is_v,
+                                             float* red) {
   const int t = threadIdx.x % kTeam;
-  const bool is_v = item & 1;
-  const int h = (int)((item >> 1) % a.H_kv);
-  const Slot sl = find_slot(a, (item >> 1) / a.H_kv);
   if (sl.rows == 0) return;
   const int64_t page_id = kv8_page(a, sl.s, sl.col);
   if (page_id < 0) return;
@@ -234,11 +282,7 @@ kv8_append_kernel(const __grid_constant__ Kv8Args a, const T* __restrict__ k,
   uint8_t* blk = (is_v ? a.v : a.k) + ((page_id * a.H_kv + h) << a.page_shift) * D;
   float* scale = (is_v ? a.v_scale : a.k_scale) + page_id * a.H_kv + h;
 
-  // one pass over the rows: the first kHold chunks of a thread stay in
-  // registers (a page of 64 rows of 128 channels for a team of 128), the rest are
-  // read again
-  constexpr int kHold = 4;
-  Vec16<T> held[kHold];
+  Vec16<T> held[kHold > 0 ? kHold : 1];
   const int chunks = sl.rows * cpr;
   const int shift = D == 128 ? 3 : 2;
   auto at = [&](int c) { return src + (int64_t)(c >> shift) * stride + (c & (cpr - 1)) * 16; };
@@ -292,6 +336,32 @@ kv8_append_kernel(const __grid_constant__ Kv8Args a, const T* __restrict__ k,
   if (t == 0 && sc != old) *scale = sc;
 }
 
+template <typename T, int kTeam>
+__device__ __noinline__ void append_lost(const Kv8Args& a, const T* k, const T* v, int64_t k_stride,
+                                         int64_t v_stride, float* red) {
+  lost_slots(a, [&](const Slot& sl) {
+    for (int i = threadIdx.x / kTeam; i < 2 * a.H_kv; i += block_of<kTeam>() / kTeam) {
+      append_block<T, kTeam, 0>(a, k, v, k_stride, v_stride, sl, i >> 1, i & 1, red);
+      if (kTeam > 32) __syncthreads();  // the maxima of the next block
+    }
+  });
+}
+
+template <typename T, int kTeam>
+__global__ void __launch_bounds__(block_of<kTeam>(), (kTeam == 32 ? 4 : 8) / (sizeof(T) / 2))
+kv8_append_kernel(const __grid_constant__ Kv8Args a, const T* __restrict__ k,
+                  const T* __restrict__ v, int64_t k_stride, int64_t v_stride, int64_t items) {
+  __shared__ float red[kTeam / 32];
+  const int64_t item = (int64_t)blockIdx.x * (block_of<kTeam>() / kTeam) + threadIdx.x / kTeam;
+  if (blockIdx.x == gridDim.x - 1) {  // past the items
+    if (check_batch(a)) append_lost<T, kTeam>(a, k, v, k_stride, v_stride, red);
+    return;
+  }
+  if (item >= items) return;
+  append_block<T, kTeam, 4>(a, k, v, k_stride, v_stride, find_slot(a, (item >> 1) / a.H_kv),
+                            (int)((item >> 1) % a.H_kv), item & 1, red);
+}
+
 template <typename T>
 __device__ __forceinline__ void store16(T* p, const float* x);
 template <>
@@ -330,18 +400,9 @@ __device__ __forceinline__ void store16<__nv_bfloat16>(__nv_bfloat16* p, const f
 // tokens (8 heads x 128, bf16) 140 us, 5.7 TB/s in all, of which a plain fill of
 // the 537 MB written takes 136.
 template <typename T, int kTeam>
-__global__ void __launch_bounds__(block_of<kTeam>())
-kv8_read_kernel(const __grid_constant__ Kv8Args a, T* __restrict__ k, T* __restrict__ v,
-                int64_t items) {
-  const int64_t item = (int64_t)blockIdx.x * (block_of<kTeam>() / kTeam) + threadIdx.x / kTeam;
-  if (item >= items) {
-    kv8_check_batch(a);
-    return;
-  }
+__device__ __forceinline__ void read_block(const Kv8Args& a, T* __restrict__ k, T* __restrict__ v,
+                                           const Slot& sl, int h, bool is_v) {
   const int t = threadIdx.x % kTeam;
-  const bool is_v = item & 1;
-  const int h = (int)((item >> 1) % a.H_kv);
-  const Slot sl = find_slot(a, (item >> 1) / a.H_kv);
   const int D = a.D, cpr = D / 16, shift = D == 128 ? 3 : 2;
   const int64_t stride = (int64_t)a.H_kv * D;
   T* out = (is_v ? v : k) + (int64_t)h * D;
@@ -373,6 +434,28 @@ kv8_read_kernel(const __grid_constant__ Kv8Args a, T* __restrict__ k, T* __restr
   }
 }
 
+template <typename T, int kTeam>
+__device__ __noinline__ void read_lost(const Kv8Args& a, T* k, T* v) {
+  lost_slots(a, [&](const Slot& sl) {
+    for (int i = threadIdx.x / kTeam; i < 2 * a.H_kv; i += block_of<kTeam>() / kTeam)
+      read_block<T, kTeam>(a, k, v, sl, i >> 1, i & 1);
+  });
+}
+
+template <typename T, int kTeam>
+__global__ void __launch_bounds__(block_of<kTeam>(), kTeam == 32 ? 5 : 16)
+kv8_read_kernel(const __grid_constant__ Kv8Args a, T* __restrict__ k, T* __restrict__ v,
+                int64_t items) {
+  const int64_t item = (int64_t)blockIdx.x * (block_of<kTeam>() / kTeam) + threadIdx.x / kTeam;
+  if (blockIdx.x == gridDim.x - 1) {
+    if (check_batch(a)) read_lost<T, kTeam>(a, k, v);
+    return;
+  }
+  if (item >= items) return;
+  read_block<T, kTeam>(a, k, v, find_slot(a, (item >> 1) / a.H_kv), (int)((item >> 1) % a.H_kv),
+                       item & 1);
+}
+
 // A warp per item where a block's rows are few, or few of it are written: up to
 // four 16-value pieces a lane, as many as it holds.  Measured: one token of 256
 // sequences, a call by itself, 20 us with warps and 26 with teams of 128; the
@@ -381,7 +464,7 @@ inline bool small_items(const Kv8Args& a) {
   const int64_t rows = ((int64_t)a.T + a.S - 1) / a.S, page = (int64_t)1 << a.page_shift;
   return (rows < page ? rows : page) * (a.D / 16) <= 128;
 }
-// Blocks of a launch: the items', and one whose threads check the batch's entries.
+// Blocks of a launch: the items', and one that checks the batch's entries.
 inline int64_t blocks_of(int64_t items, bool small) {
   return (small ? (items + kBlockSmall / 32 - 1) / (kBlockSmall / 32) : items) + 1;
 }
