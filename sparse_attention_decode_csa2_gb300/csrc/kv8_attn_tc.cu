@@ -16,9 +16,12 @@
 //   warps 0-3, 4-7  softmax of row tile 0, 1: a thread owns a row (a tensor-memory
 //                   lane), so row maxima and sums need no exchange.  The reference
 //                   maximum is lazy: weights are formed in one pass with the old
-//                   reference, which gives the key at the reference a weight of 2^7;
+//                   reference, which gives a logit at the reference a weight of 2^7;
 //                   only where they grow past fp16's range (seen from their sums)
-//                   does it move, O is rescaled and the weights are formed again
+//                   does it move, O is rescaled and the weights are formed again.
+//                   It moves by whole powers of two, to the next one above the
+//                   largest logit: what was formed before is scaled exactly, the
+//                   fp16 weights of the tile's first half too
 //   warps 8-11      dequantisers: E4M3 codes to fp16, 128-byte swizzled, double
 //                   buffered; keys that no row of the unit may see, and those of
 //                   pages outside the cache, become zeros
@@ -63,8 +66,9 @@ constexpr int kSoftRegs = 184, kDeqRegs = 80, kMmaRegs = 64;
 static_assert(2 * kSoftRegs + kDeqRegs + kMmaRegs <= 512, "register split");
 constexpr int kUnit = 256;      // query rows of a unit
 constexpr int kTileE = 128;     // keys of a tile (and rows of a row tile)
-// log2 of the weight at the reference, and the largest sum of 16 weights: no
-// weight is above it, which fp16 holds (65504)
+// log2 of the weight at the reference (up to one less for the largest logit: the
+// reference is whole; with 8 the chunk below took 778 us, with 7 772), and the largest
+// sum of 16 weights: no weight is above it, which fp16 holds (65504)
 constexpr float kHeadroom = 7.0f, kMostSum = 57344.0f;
 // The largest reference with which exponents are formed by one fused
 // multiply-add: its rounding is then at most 2^-8 of a power of two, that of the
@@ -468,8 +472,10 @@ kv8_attn_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
                 x = fmaxf(x, fmaf(mx, fmaxf(crow * b.x, 1.17549435e-38f), b.y));
               }
             }
-            const float alpha = x > m_ref ? ex2(m_ref - x) : 1.0f;
-            m_ref = fmaxf(m_ref, x);
+            // by whole powers of two, so that what was formed with the old one keeps its bits
+            const float up = fmaxf(m_ref, ceilf(x)), down = m_ref - up;
+            const float alpha = !(up > m_ref) ? 1.0f : down < -126.0f ? 0.0f : pow2f((int)down);
+            m_ref = up;
             l *= alpha;
             // S_t(j) is done, so O_t(j - 1), issued before it, is too
             if (j > t0) {
@@ -484,19 +490,18 @@ kv8_attn_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
               }
             }
             if (half == 1) {  // the first half's weights had the old reference
-              const __half2 a2 = __float2half2_rn(alpha);
               uint32_t y[32];
               tmem_ld32(ts, y);
               tmem_wait_ld32(y);
 #pragma unroll
               for (int k = 0; k < 32; ++k) {
-                const __half2 z = __hmul2(*reinterpret_cast<const __half2*>(&y[k]), a2);
-                y[k] = *reinterpret_cast<const uint32_t*>(&z);
+                const float2 f = half2_bits_to_float2(y[k]);
+                y[k] = pack_f16(f.x * alpha, f.y * alpha);
               }
               tmem_st32(ts, y);
             }
-            // the weights, the reference subtracted from the rounded exponent: its own
-            // weight is exact however large the logits are.  P's columns are those of
+            // the weights, the reference subtracted from the rounded exponent: the largest
+            // logit's weight is exact however large it is.  P's columns are those of
             // keys that have been read
             const float base = (m_ref == -INFINITY ? 0.0f : m_ref) - kHeadroom;
 #pragma unroll 1

@@ -53,3 +53,22 @@ def test_attn_reference_that_moves_in_both_halves_of_every_tile(C, dtype, D, pag
     q = torch.zeros((rows, 1, D), dtype=dtype)
     q[:, 0, 0] = 1.0
     _check_attn(C, w, q, None, causal=False, scale=math.log(2.0))
+
+
+@pytest.mark.parametrize("D,page", [(128, 64), (64, 16)])
+@pytest.mark.parametrize("rows", [4, 40])
+def test_attn_weights_that_the_reference_leaves_behind_keep_their_bits(C, D, page, rows):
+    # the last token of a tile outgrows the others by 2^10 .. 2^20: their weights, formed before, are scaled down.
+    # They alone reach channel 0, where they keep the bound of weights rounded once (the least is 2^-13, normal)
+    w = World(C, 82, [128], 1, D, page)
+    k, v = np.zeros((128, 1, D)), np.zeros((128, 1, D))
+    k[:64, 0, 0] = np.arange(64) % 8 / 64
+    k[127, 0, 0] = 1.0
+    v[:64, 0, 0], v[64:, 0, 1] = 448.0, 1.0
+    _tokens(w, 0, k, v)
+    used = w.table[0]
+    w.ks[used], w.vs[used] = 1.0, 2.0 ** 6
+    q = torch.zeros((rows, 1, D), dtype=FP16)
+    q[:, 0, 0] = torch.linspace(10.0, 19.75, rows)
+    out, _ = _check_attn(C, w, q, None, causal=False, scale=math.log(2.0))
+    assert (out[:, 0, 0] > 0.5).all()
