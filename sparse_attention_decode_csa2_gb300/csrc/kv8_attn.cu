@@ -11,10 +11,11 @@
 // instructions (fp16 in, fp32 accumulate) therefore form q . codes with only
 // fp32 rounding.  The block scales enter in the exponent: with K scale ks and V
 // scale vs of key j's block,
-//   s_j = scale log2(e) ks (q . kcode_j) + log2(vs),   w_j = 2^(s_j - ref + 7),
-//   out = sum_j w_j vcode_j / sum_j (w_j / vs),
-// with a reference near the largest s, so the weights fit fp16 whatever the
-// scales, and applying both scales costs one fused multiply-add.  The weights are
+//   s_j = scale log2(e) ks (q . kcode_j) + log2(vs / 2^E),   w_j = 2^(s_j - ref + 7),
+//   out = 2^E sum_j w_j vcode_j / sum_j (w_j 2^E / vs),
+// with a reference near the largest s, and a unit 2^E near the blocks' V scales that
+// moves where they lie far apart (kv8_sched.cuh).  So the weights fit fp16, and
+// applying both scales costs one fused multiply-add.  The weights are
 // rounded to fp16 as the operand of the second product (2^-11 relative; the
 // factor 2^7 keeps those of 2^-21 and more of the reference normal, so that a long
 // tail of small ones is not lost); sums and maxima are fp32.
@@ -41,14 +42,19 @@
 //
 // Measured (GB300; the copy peak is 6.77 TB/s):
 //   one token of 32 sequences of up to 64K tokens (64 heads over 8, D = 128):
-//     463 us, 6.9 TB/s: the copy's rate
-//   17 sequences of up to 9K tokens (40 heads over 8, D = 64): 32.8 us (3.4 TB/s).
+//     468 us, 6.8 TB/s: the copy's rate
+//   17 sequences of up to 9K tokens (40 heads over 8, D = 64): 34.8 us (3.2 TB/s).
 //     Of them 5 us go before the first tile (ranges, pages, first loads) and 4 to
-//     the merge; between, 5.9 TB/s: the warps wait for their own loads and results
+//     the merge; between, the warps wait for their own loads and results
 //     (12 warps an SM: the registers of O and of the codes in flight)
 //   4 drafted tokens of 24 sequences of up to 16K tokens (32 heads over 4, D = 128;
-//     32 rows a KV head): 86 us (3.5 TB/s), tensor pipe 40 % busy, 35 % of issue
+//     32 rows a KV head): 90 us (3.3 TB/s), tensor pipe 40 % busy, 35 % of issue
 //     slots: the same waits, with eight warps an SM
+// Following the V scales costs 463 -> 468, 32.8 -> 34.8 and 86 -> 90 us of these: a
+// comparison a tile and the code of the rare case.  (Tiles whose second half came by
+// itself by going round the loop once more: 494, 35.8 and 94.)
+#include <type_traits>
+
 #include "kv8_sched.cuh"
 
 namespace csa2 {
@@ -84,7 +90,7 @@ struct Cfg {
   static constexpr int ctas = D == 64 && kMt == 1 ? 3 : 2;
   // the join of the warps uses kMt stages of each ring, the next unit's first tiles
   // the others
-  static_assert(kMt * stage == unit * D * 4 && kMt < stages, "join");
+  static_assert(kMt * stage == unit * D * 4 && kMt < stages && kWarps == 4, "join");
 };
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
@@ -221,6 +227,7 @@ kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ RangeSmem<kWarps> rsm;
   __shared__ float row_max[kWarps][C::unit], row_sum[kWarps][C::unit], row_c[C::unit];
+  __shared__ int v_exp[kWarps];  // of the warp's V scales: the largest exponent; at the join, E
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, c = lane & 3;
   pdl_trigger();
@@ -396,50 +403,20 @@ kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a) {
       lrow[mt][0] = lrow[mt][1] = 0.0f;
     }
 
-#pragma unroll 1
-    for (int t = w.t0; t < w.t1; ++t) {
-      copy_wait<C::stages - 2>();
-      // every lane's copies of tile t are there, and it is done with tile t - 1, whose
-      // stage takes the next copies
-      __syncwarp();
-      request();
-      const float4 bs = *reinterpret_cast<const float4*>(ring_scale + st * 4);
-      const uint8_t* kt = ring + st * C::stage;
-      const uint32_t vt = ring_u + st * C::stage + C::tile;
-      if (++st == C::stages) st = 0;
-      const int key0 = key_first + t * C::granule;
-      const bool half0 = bs.z != 0.0f, half1 = bs.w != 0.0f;
-      const bool masked = !(half0 && half1 && key0 >= all_lo && key0 + kTileKeys <= all_hi);
-      if (masked) {
-        if (!half0 && !half1) continue;
-        // A weight of zero does not hide a NaN of V: where some rows see a key and
-        // others do not, its V codes become zeros and its K codes NaN, which the mask
-        // hides.  (Keys that no row sees are zeros.)
-        const int key = key0 + lane;
-        if (key < all_lo || key >= all_hi) {
-          uint8_t* codes = ring + (vt - C::tile - ring_u);
-          bool nan = false;
-#pragma unroll 1
-          for (int ch = 0; ch < D / 16; ++ch) {
-            uint4* x = reinterpret_cast<uint4*>(codes + C::tile + tile_off<D>(lane, ch));
-            if (has_nan(*x)) {
-              *x = make_uint4(0, 0, 0, 0);
-              nan = true;
-            }
-          }
-          if (nan) *reinterpret_cast<uint32_t*>(codes + tile_off<D>(lane, 0)) = 0x7F7F7F7Fu;
-        }
-        __syncwarp();
-      }
+    // a tile's keys (kHalves = 1: its first half): V scales as ratios to 2^E; what O is to be
+    // multiplied by, where `moved`
+    auto attend = [&](auto halves, const uint8_t* kt, uint32_t vt, int key0, float2 ks, bool half0,
+                      bool half1, const float (&ratio)[2], bool masked, bool moved, float factor) {
+      constexpr int kHalves = decltype(halves)::value;
       // ---- S = Q K^T ----
-      float sc[kMt][4][4];
+      float sc[kMt][2 * kHalves][4];
 #pragma unroll
       for (int mt = 0; mt < kMt; ++mt)
 #pragma unroll
-        for (int nt = 0; nt < 4; ++nt) sc[mt][nt][0] = sc[mt][nt][1] = sc[mt][nt][2] = sc[mt][nt][3] = 0.0f;
+        for (int nt = 0; nt < 2 * kHalves; ++nt) sc[mt][nt][0] = sc[mt][nt][1] = sc[mt][nt][2] = sc[mt][nt][3] = 0.0f;
 #pragma unroll
       for (int j = 0; j < D / 64; ++j) {
-        uint4 qv[kMt][4];
+        [[maybe_unused]] uint4 qv[kMt][4];
         if constexpr (kMt > 1) {
 #pragma unroll
           for (int mt = 0; mt < kMt; ++mt)
@@ -447,14 +424,14 @@ kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a) {
             for (int i = 0; i < 4; ++i)
               qv[mt][i] = qs[(mt * (D / 16) + 4 * j + i) * 32 + lane];
         }
-        uint4 b[4];
+        uint4 b[2 * kHalves];
 #pragma unroll
-        for (int nt = 0; nt < 4; ++nt)
+        for (int nt = 0; nt < 2 * kHalves; ++nt)
           b[nt] = *reinterpret_cast<const uint4*>(kt + tile_off<D>(key_of(nt, g), 4 * j + c));
 #pragma unroll
         for (int i = 0; i < 4; ++i)  // (4 kMt independent products in a row)
 #pragma unroll
-          for (int nt = 0; nt < 4; ++nt) {
+          for (int nt = 0; nt < 2 * kHalves; ++nt) {
             const uint2 f = e4m3x4_to_f16x4(i == 0 ? b[nt].x : i == 1 ? b[nt].y : i == 2 ? b[nt].z : b[nt].w);
             if constexpr (kMt == 1) {
               mma16816(sc[0][nt], qf[4 * j + i], f.x, f.y);
@@ -472,7 +449,7 @@ kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a) {
 #pragma unroll
         for (int mt = 0; mt < kMt; ++mt)
 #pragma unroll
-          for (int nt = 0; nt < 4; ++nt)
+          for (int nt = 0; nt < 2 * kHalves; ++nt)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const int key = key0 + key_of(nt, 2 * c + (e & 1)), pos = rpos[mt][e >> 1];
@@ -482,26 +459,26 @@ kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a) {
             }
       }
       // ---- weights ----
-      const float lv[2] = {half0 ? __log2f(bs.z) : 0.0f, half1 ? __log2f(bs.w) : 0.0f};
-      const float rv[2] = {half0 ? 1.0f / bs.z : 0.0f, half1 ? 1.0f / bs.w : 0.0f};
-      // exponents: the logit in powers of two plus log2 of the V scale.  (Subtracting
+      const float lv[2] = {__log2f(ratio[0]), __log2f(ratio[1])};
+      const float rv[2] = {1.0f / ratio[0], 1.0f / ratio[1]};
+      // exponents: the logit in powers of two plus log2 of the V scale's ratio.  (Subtracting
       // the reference from the rounded exponent, not inside the fused multiply-add,
       // makes the reference's own weight exact however large the logits are.)
 #pragma unroll
       for (int mt = 0; mt < kMt; ++mt)
 #pragma unroll
-        for (int nt = 0; nt < 4; ++nt)
+        for (int nt = 0; nt < 2 * kHalves; ++nt)
 #pragma unroll
           for (int e = 0; e < 4; ++e)
             sc[mt][nt][e] = fmaf(sc[mt][nt][e],
-                                 fmaxf(crow[mt][e >> 1] * (nt < 2 ? bs.x : bs.y), 1.17549435e-38f),
+                                 fmaxf(crow[mt][e >> 1] * (nt < 2 ? ks.x : ks.y), 1.17549435e-38f),
                                  lv[nt >> 1]);
-      uint32_t pf[kMt][2][4];
-      float ls[kMt][2][2];  // sums [row][half]
+      uint32_t pf[kMt][kHalves][4];
+      float ls[kMt][2][kHalves];  // sums [row][half]
       bool fresh = false;
 #pragma unroll
       for (int mt = 0; mt < kMt; ++mt) fresh |= mrow[mt][0] == -INFINITY || mrow[mt][1] == -INFINITY;
-      bool move = __any_sync(0xffffffffu, fresh);
+      bool move = moved || __any_sync(0xffffffffu, fresh);
 #pragma unroll 1
       for (int pass = 0; pass < 2; ++pass) {
         if (move) {  // the reference moves to the tile's largest exponent where that is past it
@@ -512,13 +489,14 @@ kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a) {
             for (int r = 0; r < 2; ++r) {
               float x = -INFINITY;
 #pragma unroll
-              for (int nt = 0; nt < 4; ++nt)
+              for (int nt = 0; nt < 2 * kHalves; ++nt)
                 x = fmaxf(x, fmaxf(sc[mt][nt][2 * r], sc[mt][nt][2 * r + 1]));
               x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
               x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
               alpha[r] = x > mrow[mt][r] ? ex2(mrow[mt][r] - x) : 1.0f;
               mrow[mt][r] = fmaxf(mrow[mt][r], x);
               lrow[mt][r] *= alpha[r];
+              alpha[r] *= factor;  // (1 but where E moves, which is always a first pass)
             }
 #pragma unroll
             for (int i = 0; i < D / 8; ++i) {
@@ -536,7 +514,7 @@ kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a) {
           for (int r = 0; r < 2; ++r) {
             const float base = (mrow[mt][r] == -INFINITY ? 0.0f : mrow[mt][r]) - kHeadroom;
 #pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
+            for (int hf = 0; hf < kHalves; ++hf) {
               float p[4];
 #pragma unroll
               for (int i = 0; i < 4; ++i)
@@ -556,10 +534,12 @@ kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a) {
       for (int mt = 0; mt < kMt; ++mt)
 #pragma unroll
         for (int r = 0; r < 2; ++r)
-          lrow[mt][r] = fmaf(ls[mt][r][0], rv[0], fmaf(ls[mt][r][1], rv[1], lrow[mt][r]));
+#pragma unroll
+          for (int hf = kHalves - 1; hf >= 0; --hf)
+            lrow[mt][r] = fmaf(ls[mt][r][hf], rv[hf], lrow[mt][r]);
       // ---- O += P V ----
 #pragma unroll
-      for (int kk = 0; kk < 2; ++kk) {
+      for (int kk = 0; kk < kHalves; ++kk) {
         const int r = kk * 16 + (lane & 15);
 #pragma unroll
         for (int cb = 0; cb < D / 16; cb += 2) {
@@ -578,6 +558,88 @@ kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a) {
           }
         }
       }
+    };
+    // E from the first tile
+    copy_wait<C::stages - 2>();
+    __syncwarp();
+    float unit;  // 2^-E
+    {
+      const float2 vs = *reinterpret_cast<const float2*>(ring_scale + st * 4 + 2);
+      const float s = vs.x != 0.0f ? vs.x : vs.y;
+      const int e = s != 0.0f ? unit_exp(s) : kNoUnit;
+      unit = pow2f(-e);
+      if (lane == 0) v_exp[warp] = e;
+    }
+#pragma unroll 1
+    for (int t = w.t0; t < w.t1; ++t) {
+      copy_wait<C::stages - 2>();
+      // every lane's copies of tile t are there, and it is done with tile t - 1, whose
+      // stage takes the next copies
+      __syncwarp();
+      request();
+      const float4 bs = *reinterpret_cast<const float4*>(ring_scale + st * 4);
+      const uint8_t* kt = ring + st * C::stage;
+      const uint32_t vt = ring_u + st * C::stage + C::tile;
+      if (++st == C::stages) st = 0;
+      const int key0 = key_first + t * C::granule;
+      // the halves' V scales as ratios to 2^E
+      float ratio[2] = {bs.z * unit, bs.w * unit}, factor = 1.0f;
+      bool half0 = true, half1 = true, moved = false;
+      const bool masked = !(near_unit(ratio[0]) && near_unit(ratio[1]) && key0 >= all_lo &&
+                            key0 + kTileKeys <= all_hi);
+      if (masked) {
+        half0 = bs.z != 0.0f;
+        half1 = bs.w != 0.0f;
+        if (!half0 && !half1) continue;
+        // A weight of zero does not hide a NaN of V: where some rows see a key and
+        // others do not, its V codes become zeros and its K codes NaN, which the mask
+        // hides.  (Keys that no row sees are zeros.)
+        const int key = key0 + lane;
+        uint8_t* codes = ring + (vt - C::tile - ring_u);
+        if (key < all_lo || key >= all_hi) {
+          bool nan = false;
+#pragma unroll 1
+          for (int ch = 0; ch < D / 16; ++ch) {
+            uint4* x = reinterpret_cast<uint4*>(codes + C::tile + tile_off<D>(lane, ch));
+            if (has_nan(*x)) {
+              *x = make_uint4(0, 0, 0, 0);
+              nan = true;
+            }
+          }
+          if (nan) *reinterpret_cast<uint32_t*>(codes + tile_off<D>(lane, 0)) = 0x7F7F7F7Fu;
+        }
+        __syncwarp();
+        moved = (half0 && !near_unit(ratio[0])) || (half1 && !near_unit(ratio[1]));
+        if (moved) {
+          VUnit u = {unit_of(unit), v_exp[warp]};
+          float f1 = 1.0f;
+          bool far0 = false, far1 = false;
+          if (half0) ratio[0] = follow(u, bs.z, factor, far0);
+          if (half1) ratio[1] = follow(u, bs.w, f1, far1);
+          unit = pow2f(-u.e);
+          __syncwarp();
+          if (lane == 0) v_exp[warp] = u.top;
+          if (lane < 16 ? far0 : far1) {  // of values that are left out, the NaN stay
+#pragma unroll 1
+            for (int ch = 0; ch < D / 16; ++ch) {
+              uint4* x = reinterpret_cast<uint4*>(codes + C::tile + tile_off<D>(lane, ch));
+              *x = only_nan(*x);
+            }
+          }
+          __syncwarp();
+          if (half0 && half1 && f1 != 1.0f) {  // E moves between the halves (pages of 16 tokens)
+            attend(std::integral_constant<int, 1>{}, kt, vt, key0, make_float2(bs.x, bs.y), true,
+                   true, ratio, true, true, factor);
+            half0 = false;
+            factor = 1.0f;
+          }
+          factor *= f1;
+        }
+        if (!half0) ratio[0] = 1.0f;
+        if (!half1) ratio[1] = 1.0f;
+      }
+      attend(std::integral_constant<int, 2>{}, kt, vt, key0, make_float2(bs.x, bs.y), half0, half1,
+             ratio, masked, moved, factor);
     }
     copy_wait<0>();
     __syncwarp();  // the warp is done with its ring
@@ -609,6 +671,7 @@ kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a) {
           row_max[warp][row] = mrow[mt][r];
           row_sum[warp][row] = lrow[mt][r];
         }
+        if (lane == 0 && mt == 0 && r == 0) v_exp[warp] = max(-126, unit_of(unit));
         float* dst = obuf + (size_t)row * D + 2 * c;
 #pragma unroll
         for (int i = 0; i < D / 8; ++i)  // (8-channel blocks exclusive-or'ed with the row: other banks)
@@ -618,6 +681,9 @@ kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a) {
     if (more) fetch();
     __syncthreads();
     float* pw = scratch_part(a, gridDim.x, blockIdx.x, starts, C::unit, D);
+    // (a warp without keys has O = 0 and the least E)
+    const int e_top = max(max(v_exp[0], v_exp[1]), max(v_exp[2], v_exp[3]));
+    const float to_one = pow2f(e_top);
     constexpr int kTpr = D / 4;  // threads per row
 #pragma unroll 1
     for (int i = 0; i < C::unit * kTpr / kThreads; ++i) {
@@ -631,8 +697,9 @@ kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a) {
       float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
       for (int q = 0; q < kWarps; ++q) {
-        const float f = ex2(row_max[q][row] - mz);
+        float f = ex2(row_max[q][row] - mz);
         l = fmaf(row_sum[q][row], f, l);
+        f *= pow2_or_zero(v_exp[q] - e_top);
         const float4 y = *reinterpret_cast<const float4*>(
             smem + q * (C::stages * C::stage) + ((size_t)row * D + (ch ^ ((row & 3) * 8))) * 4);
         x.x = fmaf(y.x, f, x.x);
@@ -640,12 +707,15 @@ kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a) {
         x.z = fmaf(y.z, f, x.z);
         x.w = fmaf(y.w, f, x.w);
       }
+      const float inv = l == 0.0f ? 0.0f : 1.0f / l;  // no visible token: zeros
+      x.x = x.x * inv * to_one;
+      x.y = x.y * inv * to_one;
+      x.z = x.z * inv * to_one;
+      x.w = x.w * inv * to_one;
       if (whole) {
-        const float inv = l == 0.0f ? 0.0f : 1.0f / l;  // no visible token: zeros
         const int64_t orow = out_row(a, token0, head0, row);
         *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + orow * D + ch) =
-            make_uint2(pair_from_floats<kBf16>(x.x * inv, x.y * inv),
-                       pair_from_floats<kBf16>(x.z * inv, x.w * inv));
+            make_uint2(pair_from_floats<kBf16>(x.x, x.y), pair_from_floats<kBf16>(x.z, x.w));
         if (a.lse && ch == 0)
           a.lse[orow] = l == 0.0f ? -INFINITY : (mz - kHeadroom + __log2f(l)) * kLn2;
       } else {

@@ -545,7 +545,7 @@ kv8_attn_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
       ++units;
       tc_fence_after();
       // ---- output, or a part of it ----
-      const float inv = !whole ? 1.0f : l == 0.0f ? 0.0f : 1.0f / l;  // no visible token: zeros
+      const float inv = l == 0.0f ? 0.0f : 1.0f / l;  // no visible token: zeros
       float* part = scratch_part(a, gridDim.x, blockIdx.x, t0 == 0, kUnit, D);
 #pragma unroll 1
       for (int i = 0; i < D; i += 32) {
@@ -567,8 +567,13 @@ kv8_attn_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
         } else {
           uint4* dst = reinterpret_cast<uint4*>(part + (size_t)row * D + i);
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            dst[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+          for (int k = 0; k < 8; ++k) {
+            uint32_t y[4];
+#pragma unroll
+            for (int n = 0; n < 4; ++n)
+              y[n] = __float_as_uint(__uint_as_float(o[4 * k + n]) * inv);
+            dst[k] = make_uint4(y[0], y[1], y[2], y[3]);
+          }
         }
       }
       if (out_ok) {

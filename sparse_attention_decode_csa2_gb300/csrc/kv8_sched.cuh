@@ -238,10 +238,10 @@ __device__ Range find_range(const Kv8AttnArgs& a, int worker, int workers,
   return r;
 }
 
-// Scratch: a record for each worker, then its parts of cut units, O [kUnit][D],
-// max [kUnit], sum [kUnit]: [0] a part that continues a unit, [1] one that starts
-// it.  The record of the worker that starts a cut unit says how to join it, so
-// that the merge kernel need not find its way again.
+// Scratch: a record for each worker, then its parts of cut units, out [kUnit][D] (as if
+// the part's keys were all), max [kUnit], sum [kUnit]: [0] a part that continues a unit,
+// [1] one that starts it.  The record of the worker that starts a cut unit says how to
+// join it, so that the merge kernel need not find its way again.
 struct Cut {
   int last;  // the worker with the unit's last part; -1: this worker starts no cut unit
   int token, head, rows;  // the unit's first row in q and out, its KV head's first query head
@@ -365,6 +365,14 @@ __device__ __forceinline__ bool has_nan(uint4 x) {
   return ((sevens(x.x) | sevens(x.y) | sevens(x.z) | sevens(x.w)) & 0x80808080u) != 0;
 }
 
+// The NaN of 16 codes, the others zero.
+__device__ __forceinline__ uint4 only_nan(uint4 x) {
+  auto f = [](uint32_t w) {
+    return ((((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) >> 7) * 0x7Fu;
+  };
+  return make_uint4(f(x.x), f(x.y), f(x.z), f(x.w));
+}
+
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -389,6 +397,52 @@ __device__ __forceinline__ int row_exponent(float mx) {
   return mx > 0.0f ? max(-126, min(126, E)) : 0;
 }
 
+// V scales far apart.  O is held in units of 2^E, a V scale enters the weights as its
+// ratio to 2^E, and E follows the blocks as their keys come: it stays where the ratio is
+// in [2^-6, 4), so that fp16 weights lose no logits to a scale, and moves to the
+// block's exponent otherwise, O scaled by the (exact) power of two between.  Down it goes
+// to 2^60 below the largest only, so that O (2^55 and less, for 2^30 tokens) cannot
+// overflow.  Blocks that are smaller still count in the sum with a ratio of 1, and
+// their values (below 2^-51 of the largest scale) are left out, but for NaN.
+constexpr int kSpan = 60;
+__device__ __forceinline__ bool near_unit(float ratio) {
+  return __float_as_uint(ratio) - 0x3C800000u < 0x40800000u - 0x3C800000u;
+}
+// E for a block: its ratio is in [2^-2, 2^-1), so that blocks a few powers of two to either
+// side do not move it.
+__device__ __forceinline__ int unit_exp(float scale) {
+  return max(-126, min(126, (int)((__float_as_uint(scale) >> 23) & 0xFFu) - 125));
+}
+// E of 2^-E; kNoUnit for 2^127.
+__device__ __forceinline__ int unit_of(float unit) { return 127 - (int)(__float_as_uint(unit) >> 23); }
+// 2^e, zero below fp32's normal numbers.
+__device__ __forceinline__ float pow2_or_zero(int e) { return e < -126 ? 0.0f : pow2f(e); }
+// E and the largest exponent so far; a unit starts without.
+struct VUnit {
+  int e, top;
+};
+constexpr int kNoUnit = -127;
+// The block's ratio, and what O is to be multiplied by before it.  far: its values are
+// left out.
+__device__ __forceinline__ float follow(VUnit& u, float scale, float& factor, bool& far) {
+  const int e = unit_exp(scale);
+  factor = 1.0f;
+  far = false;
+  if (u.e == kNoUnit) {
+    u.e = u.top = e;
+  } else if (e > u.e + 3 || e < u.e - 4) {
+    u.top = max(u.top, e);
+    const int to = max(e, u.top - kSpan);
+    if (e < to - 4) {
+      far = true;
+      return 1.0f;
+    }
+    factor = pow2_or_zero(u.e - to);
+    u.e = to;
+  }
+  return scale * pow2f(-u.e);
+}
+
 // row / G for row < 256, by the host's reciprocal ceil(2^16 / G): row times its
 // excess (below G) stays below 2^16.
 __device__ __forceinline__ int over_g(const Kv8AttnArgs& a, int row) {
@@ -401,7 +455,9 @@ __device__ __forceinline__ int64_t out_row(const Kv8AttnArgs& a, int token, int 
 }
 
 // Joins the parts of the cut units: block (x, y) takes the unit that worker x
-// starts, every gridDim.y-th group of its rows.  Few parts: a thread has four
+// starts, every gridDim.y-th group of its rows.  A part counts by its share of the sum so
+// far, so the result stays a mean of the parts' outputs and cannot overflow, whatever
+// scales the parts' values have.  Few parts: a thread has four
 // channels of a row and goes through them.  Many (a long context with few units):
 // a warp has 32 channels of a row; its lanes share out the parts' maxima and sums,
 // 32 at a time, and four groups of eight lanes sum a quarter of the parts each, all
@@ -434,11 +490,9 @@ __device__ __forceinline__ void merge_parts(const Kv8AttnArgs& a, int workers, f
   const int4 cut = __ldcg(reinterpret_cast<const int4*>(a.scratch) + blockIdx.x);
   const int last = cut.x, nrow = last < 0 ? 0 : cut.w;
   auto write = [&](int row, int c4, float4 x, float m, float l) {
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;  // no visible token: zeros
     const int64_t orow = out_row(a, cut.y, cut.z, row);
     *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + orow * D + c4) =
-        make_uint2(pair_from_floats<kBf16>(x.x * inv, x.y * inv),
-                   pair_from_floats<kBf16>(x.z * inv, x.w * inv));
+        make_uint2(pair_from_floats<kBf16>(x.x, x.y), pair_from_floats<kBf16>(x.z, x.w));
     if (a.lse && c4 == 0)
       a.lse[orow] =
           l == 0.0f ? -INFINITY : ((m == -INFINITY ? 0.0f : m) - headroom + __log2f(l)) * kLn2;
@@ -455,9 +509,12 @@ __device__ __forceinline__ void merge_parts(const Kv8AttnArgs& a, int workers, f
         const float pm = __ldcg(src + kUnit * D + row), pl = __ldcg(src + kUnit * D + kUnit + row);
         const float4 y = __ldcg(reinterpret_cast<const float4*>(src + (size_t)row * D + c4));
         const float nm = fmaxf(m, pm), z = nm == -INFINITY ? 0.0f : nm;
-        const float f0 = ex2(m - z), f1 = ex2(pm - z);
+        float f0 = l * ex2(m - z), f1 = pl * ex2(pm - z);
         m = nm;
-        l = l * f0 + pl * f1;
+        l = f0 + f1;
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;  // no visible token: zeros
+        f0 *= inv;
+        f1 *= inv;
         x.x = x.x * f0 + y.x * f1;
         x.y = x.y * f0 + y.y * f1;
         x.z = x.z * f0 + y.z * f1;
@@ -490,23 +547,25 @@ __device__ __forceinline__ void merge_parts(const Kv8AttnArgs& a, int workers, f
       float top = fmaxf(m, pm);
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      const float z = top == -INFINITY ? 0.0f : top, old = ex2(m - z), f = ex2(pm - z);
-      float sum = f * pl;
+      const float z = top == -INFINITY ? 0.0f : top, g = pl * ex2(pm - z);
+      float old = l * ex2(m - z), sum = g;
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      l = fmaf(l, old, sum);
+      l = old + sum;
       m = top;
+      const float inv = l == 0.0f ? 0.0f : 1.0f / l, f = g * inv;
+      old *= inv;
       x.x *= old;
       x.y *= old;
       x.z *= old;
       x.w *= old;
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        const float g = __shfl_sync(0xffffffffu, f, group + 4 * k);
-        x.x = fmaf(y[k].x, g, x.x);
-        x.y = fmaf(y[k].y, g, x.y);
-        x.z = fmaf(y[k].z, g, x.z);
-        x.w = fmaf(y[k].w, g, x.w);
+        const float h = __shfl_sync(0xffffffffu, f, group + 4 * k);
+        x.x = fmaf(y[k].x, h, x.x);
+        x.y = fmaf(y[k].y, h, x.y);
+        x.z = fmaf(y[k].z, h, x.z);
+        x.w = fmaf(y[k].w, h, x.w);
       }
     }
 #pragma unroll

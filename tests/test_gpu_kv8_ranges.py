@@ -1,5 +1,5 @@
 """The 8-bit paged KV cache's attention where magnitudes lie far apart: logits that outgrow the running reference
-inside a tile of keys.  Every channel is held to its own bound (kv8_ref.py), so what a few tokens give to a channel
+inside a tile of keys, V scales of blocks that are far from one another.  Every channel is held to its own bound (kv8_ref.py), so what a few tokens give to a channel
 of their own counts, however small it is beside the others.  Needs a GPU."""
 import math
 
@@ -72,3 +72,154 @@ def test_attn_weights_that_the_reference_leaves_behind_keep_their_bits(C, D, pag
     q[:, 0, 0] = torch.linspace(10.0, 19.75, rows)
     out, _ = _check_attn(C, w, q, None, causal=False, scale=math.log(2.0))
     assert (out[:, 0, 0] > 0.5).all()
+
+
+# ------------------------------------------------------------------ V scales far apart
+
+def _fill(w, v_of, ks=2.0 ** -8):
+    """Codes and scales of every token: K at random, V and its block's scale from v_of(sequence, columns, codes):
+    columns [tokens] of the block table, random codes' values [tokens][H_kv][D] -> (values, scales [columns])."""
+    for s, L in enumerate(w.lens):
+        if L == 0:
+            continue
+        j = np.arange(L)
+        p, r = w.table[s, j // w.page], j % w.page
+        w.k[p, :, r] = R.encode(60.0 * w.rng.standard_normal((L, w.Hk, w.D)))
+        v, vs = v_of(s, j // w.page, 60.0 * w.rng.standard_normal((L, w.Hk, w.D)))
+        w.v[p, :, r] = R.encode(v)
+        used = w.table[s, :-(-L // w.page)]
+        w.ks[used] = ks
+        w.vs[used] = np.asarray(vs)[:, None]
+    return w
+
+
+def _queries(w, T, H, dtype):
+    return torch.tensor(w.rng.standard_normal((T, H, w.D)) * 1.5, dtype=torch.float32).to(dtype)
+
+
+FEW = [(1, 4), (6, 2), (13, 2)]   # rows of a sequence, query heads of a KV head: 4, 12 and 26 rows a unit
+
+
+@pytest.mark.parametrize("n,G", FEW)
+@pytest.mark.parametrize("D,page", [(128, 64), (64, 16), (128, 128), (64, 32)])
+@pytest.mark.parametrize("apart", [6, 10, 20, 24, 28, 32, 40, 54])
+@pytest.mark.parametrize("dtype,code", [(BF16, 100.0), (FP16, 0.0)])
+def test_attn_blocks_with_an_outlier_leave_the_others_their_output(C, n, G, D, page, apart, dtype, code):
+    _outlier_blocks(C, n, G, D, page, apart, dtype, code)
+
+
+def _outlier_blocks(C, n, G, D, page, apart, dtype, code):
+    # some blocks have a scale 2^apart times the others' and one channel (fp16: none) that is not zero there: the
+    # other channels come from the small blocks alone.  They are the first block, the last, one between, every other
+    last = lambda c: c == c.max()
+    where = [lambda c: c == 0, last, lambda c: c == c.max() // 2, lambda c: c % 2 == 1]
+
+    def v_of(s, col, v):
+        big = where[s](np.arange(col.max() + 1))
+        v[big[col]] = 0.0
+        v[big[col], :, 5] = code
+        return v, np.where(big, 2.0 ** (apart - 8), 2.0 ** -8)
+
+    w = _fill(World(C, 83 + apart, [300, 333, 290, 512], 2, D, page), v_of)
+    _check_attn(C, w, _queries(w, 4 * n, 2 * G, dtype), None)
+
+
+@pytest.mark.parametrize("n,G", FEW)
+@pytest.mark.parametrize("D", [64, 128])
+def test_attn_outlier_blocks_in_other_parts_of_a_long_context(C, n, G, D):
+    _outlier_parts(C, n, G, D)
+
+
+def _outlier_parts(C, n, G, D):
+    # a context that is split over the grid: runs of small blocks and runs with an outlier, 2^40 apart
+    def v_of(s, col, v):
+        big = np.arange(col.max() + 1) // 9 % 2 == 1
+        v[big[col]] = 0.0
+        v[big[col], :, 5] = 100.0
+        return v, np.where(big, 2.0 ** 32, 2.0 ** -8)
+
+    w = _fill(World(C, 84, [9001], 1, D, 64), v_of)
+    q = _queries(w, n, G, BF16)
+    a = _check_attn(C, w, q, None)
+    b = _check_attn(C, w, q, None)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+@pytest.mark.parametrize("n,G", FEW)
+@pytest.mark.parametrize("big", [2.0 ** -8, 2.0 ** 30, 2.0 ** 100])
+@pytest.mark.parametrize("lens,page", [([200, 130, 64, 333], 16), ([200, 130, 64, 333], 128), ([7001], 64)])
+def test_attn_blocks_of_zeros_count_in_the_sum(C, n, G, big, lens, page):
+    _zero_blocks(C, n, G, big, lens, page)
+
+
+def _zero_blocks(C, n, G, big, lens, page):
+    # blocks of zeros, which append gives the scale 2^-100, beside others up to 2^200 above: in a tile, in the tiles
+    # of other warps, in other parts
+    def v_of(s, col, v):
+        zero = (np.arange(col.max() + 1) + s) // 2 % 2 == 0
+        v[zero[col]] = 0.0
+        return v, np.where(zero, 2.0 ** -100, big)
+
+    w = _fill(World(C, 85, lens, 2, 64, page), v_of)
+    _check_attn(C, w, _queries(w, n * len(lens), 2 * G, BF16), None)
+
+
+@pytest.mark.parametrize("n,G", FEW)
+def test_attn_a_head_without_values_has_a_finite_lse(C, n, G):
+    _no_values(C, n, G)
+
+
+def _no_values(C, n, G):
+    # every block of V is zeros (scale 2^-100) and all logits are zero, over more than 2^22 tokens.  The sum of the
+    # weights, all one power of two, is exact
+    D, page, tokens = 64, 128, (1 << 22) + 333
+    P = -(-tokens // page)
+    z = lambda: torch.zeros((P, 1, page, D), dtype=torch.uint8, device="cuda")
+    cache = C.Kv8Cache(z(), z(), torch.ones((P, 1), device="cuda"), torch.full((P, 1), 2.0 ** -100, device="cuda"))
+    i = lambda a: torch.tensor(a, dtype=torch.int32).cuda()
+    batch = C.Kv8Batch(torch.randperm(P).to(torch.int32).cuda().reshape(1, P), i([tokens]), n)
+    out, lse = C.kv8_attn(torch.ones((n, G, D), dtype=BF16).cuda(), cache, batch)
+    assert (out == 0).all()
+    want = torch.log(torch.arange(tokens - n + 1, tokens + 1, dtype=torch.float64))[:, None]
+    assert (lse.cpu().double() - want).abs().max() <= 2.0 ** -20 * 16
+
+
+@pytest.mark.parametrize("n,G", FEW)
+@pytest.mark.parametrize("page", [16, 64])
+def test_attn_scales_past_2_to_60_apart_lose_only_what_is_that_small(C, n, G, page):
+    _past_range(C, n, G, page)
+
+
+def _past_range(C, n, G, page):
+    # scales from 2^-90 to 2^90, every channel of every block: lse as ever, out to 2^-51 of the largest scale
+    # that the sequence has, beside the bound
+    rng = np.random.default_rng(88)
+    w = _fill(World(C, 87, [400, 90, 250], 1, 64, page),
+              lambda s, col, v: (v, 2.0 ** rng.integers(-90, 91, col.max() + 1)))
+    q = _queries(w, 3 * n, G, BF16)
+    cache, batch = w.cache(), w.batch(3 * n)
+    out, lse = C.kv8_attn(q.cuda(), cache, batch)
+    ref = R.attention(q.double().numpy(), (w.k, w.v, w.ks, w.vs), w.table, w.lens, R.rows_of(3 * n, 3, None), page,
+                      True, 0, 1 / 8)
+    tol_o, tol_l = R.attention_bounds(*ref, 64, 400, BF16)
+    for s, L in enumerate(w.lens):
+        tol_o[s * n:s * n + n] += 2.0 ** -51 * w.vs[w.table[s, :-(-L // page)]].max()
+    assert (np.abs(out.double().cpu().numpy() - ref[0]) <= tol_o).all()
+    assert (np.abs(lse.double().cpu().numpy() - ref[1]) <= tol_l).all()
+
+
+
+@pytest.mark.parametrize("n,G", FEW)
+@pytest.mark.parametrize("page", [16, 128])
+def test_attn_a_block_of_nan_is_seen_beside_large_ones(C, n, G, page):
+    _nan_block(C, n, G, page)
+
+
+def _nan_block(C, n, G, page):
+    # append gives a block without a number the least scale; its NaN reach the rows that see it all the same
+    w = _fill(World(C, 89, [400, 300], 1, 64, page), lambda s, col, v: (v, np.full(col.max() + 1, 2.0 ** -8)))
+    p = w.table[0, 128 // page]
+    w.v[p, :, :, 3], w.vs[p] = 0x7F, 2.0 ** -100
+    q = _queries(w, 2 * n, G, BF16)
+    out, lse = C.kv8_attn(q.cuda(), w.cache(), w.batch(2 * n))
+    assert torch.isnan(out[:n, :, 3]).all() and torch.isfinite(out[n:]).all() and torch.isfinite(lse[n:]).all()
