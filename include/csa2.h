@@ -442,6 +442,15 @@ csa2_status csa2_kv8_read(const csa2_kv8_cache* cache, const csa2_kv8_batch* bat
  *            before it
  *   out      [T][H][D] of q's type, dense, 16-byte aligned
  *   lse      fp32 [T][H] log-sum-exp of the scaled logits, or NULL
+ *   Queries (a row brought to [1, 2) by a power of two; what is 2^-17 below its largest
+ *   value loses bits) and codes are exact operands of the products, sums are fp32.  The
+ *   softmax weights are rounded to fp16 for the product with V (2^-11 relative for
+ *   those above 2^-20 of the row's largest, 2^-31 of that one below), their sum
+ *   takes them in fp32.  Exponential and logarithm are the hardware's (2^-21).
+ *   The V scales of a head may lie as far apart as the cache allows.  Only what
+ *   blocks give to out whose scale is 2^60 or more below the largest of the head in
+ *   the sequence may be left out (less than 2^-51 of that largest scale); they count
+ *   in the softmax as others do.  Logits past fp32's range are not specified.
  *   A row that sees nothing yields out = 0 and lse = -inf.  A NaN of a token
  *   that a row sees makes its out NaN (in V: in that channel at least; lse is not
  *   specified then); of one that it does not see it has no effect.  The result of a

@@ -35,17 +35,20 @@
 //                   its predecessor's V is converted and the reverse
 //   (warp 15 only completes its warpgroup, for the register split)
 // Measured (GB300; cuBLAS bf16 1.89 PFLOP/s): a chunk of 4096 rows over 16K tokens
-// (32 heads over 8, D = 128) 769 us, 1.25 PFLOP/s of products that the mask leaves,
-// 66 %; tensor pipe 56 % busy, XU 28 %, 46 % of issue slots.  A tile of keys takes
+// (32 heads over 8, D = 128) 776 us, 1.24 PFLOP/s of products that the mask leaves,
+// 65 %; tensor pipe 56 % busy, XU 28 %, 46 % of issue slots.  A tile of keys takes
 // 3300 to 3700 cycles, of which its MMAs 2048 (D = 128); each row tile goes through
 // softmax (1950 cycles, two warps a scheduler), P to O, S again, one after the other,
 // since P overwrites S.  Prompts of 10007 rows through a window of 1024 (16 heads
-// over 4, D = 64): 96 us.  There a unit has 8 clean tiles (softmax-bound as above:
+// over 4, D = 64): 102 us.  There a unit has 8 clean tiles (softmax-bound as above:
 // D = 64 halves only the MMAs), 2 to 3 at the mask's edges with 1200 cycles more, and
 // 5000 cycles from its last tile to the next unit's first.
 // Before the loader had a warp of its own (the dequantisers looked up pages and
 // scales and loaded to registers): 6600 cycles a pair of tiles, 3000 of them in
 // those dependent loads.
+// V scales far apart (kv8_sched.cuh): the loader marks such a tile, the softmax scales O
+// and adds the groups of 16 keys by phases.  Ordinary tiles pay for the check: prompts
+// through the window 97 -> 102 us, the chunk nothing.
 // Every wait is bounded (about 2 s): a role that gives up sets the timeout
 // status and leaves, the others follow, and tensor memory is freed.
 #include "kv8_sched.cuh"
@@ -90,13 +93,17 @@ struct Lay {
 static_assert(Lay<128>::alloc <= 232448, "shared memory");
 
 struct Ctl {
-  // of a tile's 16-key groups: K scale, log2 V scale, 1 / V scale (0: nothing of it is
-  // seen).  Four tiles: the loader is at most one ahead of the dequantisers, which
+  // of a tile's 16-key groups: K scale, log2 of the V scale's ratio to the unit of O, the
+  // ratio's reciprocal (0: nothing of it is seen).  Four tiles: the loader is at most one ahead of the dequantisers, which
   // are at most two ahead of the slower softmax
   float4 sc[4][8];
-  int32_t marks[4];    // of a tile: kRagged, kEdge
+  int32_t marks[4];       // of a tile: kRagged, kEdge, kMoved; see there
+  uint16_t phase[4][8];   // of a tile with kMoved: groups, and the power of two of O before them
   uint64_t rk_full, rk_empty, rv_full, rv_empty;  // the codes of a tile
   uint64_t q_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_full[2];
+  uint64_t phase_ready[2], phase_done[2];
+  uint8_t phases[kSoftWarps];  // waits of each warp for phase_done so far
+  int32_t* status;
   uint64_t done;
   Walk<Work> walk[kMmaWarp1 + 1];  // each warp's own (kept out of registers)
   uint32_t tmem;
@@ -135,6 +142,8 @@ __device__ __forceinline__ bool elect_one() {
                : "=r"(p));
   return p != 0;
 }
+// Instruction descriptor of P to O: B (V) MN-major.
+__device__ __forceinline__ uint32_t idesc_o(int D) { return idesc_f16(D, false) | (1u << 16); }
 // MMA with A from tensor memory.
 __device__ __forceinline__ void mma_f16_ta(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
                                            uint32_t accumulate) {
@@ -199,8 +208,11 @@ __device__ __forceinline__ F2 add2(F2 a, F2 b) {
 }
 
 // Marks of a tile: keys that no row of the unit sees; keys that some rows see and
-// others do not.
-constexpr int kRagged = 1, kEdge = 2;
+// others do not; V scales that the unit 2^E of O has to follow.  From bit 16 on E + 128,
+// behind the tile; with kMoved also, from bit 4, the number of phases in which P to O runs
+// (the groups of a phase share an E; between two the softmax scales O) and, from bit 8, the
+// groups whose values are left out (their weights are zeros: a NaN among them is seen).
+constexpr int kRagged = 1, kEdge = 2, kMoved = 4;
 
 // Columns of S (a tile's, from address ts) outside the row's [lo, hi) become
 // -infinity.  Not inlined: the code of the roles shares the SM's instruction cache,
@@ -220,6 +232,33 @@ __device__ __noinline__ void mask_tile(uint32_t ts, int lo, int hi) {
     tmem_st32(ts + i, x);
   }
   tmem_wait_st();
+}
+
+// O's row (from address to) times f.
+template <int D>
+__device__ __noinline__ void scale_o(uint32_t to, float f) {
+#pragma unroll 1
+  for (int i = 0; i < D; i += 16) {
+    float o[16];
+    tmem_ld16(to + i, o);
+    tmem_wait_ld();
+#pragma unroll
+    for (int k = 0; k < 16; ++k) o[k] *= f;
+    tmem_st16(to + i, o);
+  }
+}
+// Zeros into 8, 32 columns of this thread's lane.
+__device__ __forceinline__ void tmem_zero8(uint32_t addr) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%1,%1,%1,%1,%1,%1,%1};" ::"r"(addr),
+               "r"(0)
+               : "memory");
+}
+__device__ __forceinline__ void tmem_zero32(uint32_t addr) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%1,%1,%1,%1,%1,%1,%1,%1,%1,%1,%1,%1,%1,%1,"
+      "%1,%1,%1,%1,%1,%1,%1,%1,%1,%1,%1,%1,%1,%1,%1,%1,%1};" ::"r"(addr),
+      "r"(0)
+      : "memory");
 }
 
 // `bytes` contiguous bytes of global memory into shared memory, completing on bar.
@@ -302,6 +341,93 @@ __device__ __noinline__ int load_rows(const Kv8AttnArgs& a, uint8_t* qt, int fir
   return e;
 }
 
+// The loader's warp, for a tile with V scales that are not near the unit of O (lane g < 8
+// has group g's; live: the groups that are seen): the lane's ratio, the lane's phase, and
+// what the tile's marks say of them.
+struct Phases {
+  VUnit u;
+  float ratio;
+  int phase, marks;
+};
+__device__ __noinline__ Phases phases_of(VUnit u, float vs, uint32_t live) {
+  const int lane = threadIdx.x & 31, e = unit_exp(vs);
+  float ratio = 1.0f;
+  int phase = 0;
+  uint32_t todo = live, far = 0;
+  int n = 0;
+  while (todo) {
+    auto near = [&]() {
+      return __ballot_sync(0xffffffffu, ((todo >> lane) & 1) && e >= u.e - 4 && e <= u.e + 3);
+    };
+    uint32_t now = near();
+    int by = 0;
+    if (!now) {  // to the first of them
+      const int l = __ffs(todo) - 1, was = u.e;
+      float factor;
+      bool left_out;
+      follow(u, __shfl_sync(0xffffffffu, vs, l), factor, left_out);
+      if (left_out) {
+        far |= 1u << l;
+        todo &= ~(1u << l);
+        continue;
+      }
+      by = max(-127, was - u.e);
+      now = near();
+    }
+    if (lane == n) phase = (int)now | ((by & 0xFF) << 8);
+    if ((now >> lane) & 1) ratio = vs * pow2f(-u.e);
+    todo &= ~now;
+    ++n;
+  }
+  return {u, ratio, phase, kMoved | (max(n, 1) << 4) | (int)(far << 8)};
+}
+
+// A tile with kMoved, its softmax warps with their weights written: P to O of all phases
+// but the last, and the weights of their groups zero after it, so that the issuer adds
+// the last one as it does any tile.  False: a wait gave up.  (Not inlined, with what it
+// needs in shared memory, and nothing of it in the issuers' loop: the roles share the SM's
+// instruction cache and the softmax has no register to spare.  A branch on the marks in
+// the issuers' loop cost the chunk below 3 %, more arguments here 2 %.)
+template <int D>
+__device__ __noinline__ bool add_phases(Ctl& ctl, uint32_t it) {
+  const int warp = threadIdx.x >> 5, t = warp >> 2;
+  const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+  const uint32_t ts = ctl.tmem + t * 128, to = ctl.tmem + 256 + t * D;
+  const int marks = ctl.marks[it & 3], n = (marks >> 4) & 15;
+  int zero = (marks >> 8) & 0xFF;  // groups without weight from here on
+  for (int i = 0;; ++i) {
+#pragma unroll 1
+    for (int g = 0; g < 8; ++g)
+      if ((zero >> g) & 1) tmem_zero8(ts + lane_base + 8 * g);
+    const int phase = ctl.phase[it & 3][i], by = (int8_t)(phase >> 8);
+    if (by != 0) scale_o<D>(to + lane_base, pow2_or_zero(by));
+    tmem_wait_st();
+    if (i + 1 == n) return true;
+    const uint32_t parity = ctl.phases[warp] & 1u;
+    warp_arrive(&ctl.phase_ready[t]);
+    if ((warp & 3) == 0) {
+      if (!warp_wait(&ctl.phase_ready[t], parity, ctl.status) ||
+          !warp_wait(&ctl.v_full[it & 1u], (it >> 1) & 1u, ctl.status))
+        return false;
+      tc_fence_after();
+      if (elect_one()) {
+        const uint32_t v = su32(&ctl) - Lay<D>::ctl + Lay<D>::v + (it & 1u) * Lay<D>::tile;
+        const uint64_t vb = sw128_desc(v, kAtom, 1024);
+#pragma unroll 1
+        for (int x = 0; x < 8; ++x)
+          if ((phase >> x) & 1) mma_f16_ta(to, ts + 8 * x, vb + x * (2048 >> 4), idesc_o(D), 1);
+        mma_commit(su32(&ctl.phase_done[t]));
+      }
+      __syncwarp();
+    }
+    if (!warp_wait(&ctl.phase_done[t], parity, ctl.status)) return false;
+    tc_fence_after();
+    if ((threadIdx.x & 31) == 0) ++ctl.phases[warp];
+    __syncwarp();
+    zero = phase & 0xFF;
+  }
+}
+
 template <int D, bool kBf16>
 __global__ void __launch_bounds__(kThreads, 1)
 kv8_attn_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
@@ -340,7 +466,11 @@ kv8_attn_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
       mbar_init(su32(&ctl.v_empty[i]), 2);
       mbar_init(su32(&ctl.s_full[i]), 1);
       mbar_init(su32(&ctl.o_full[i]), 1);
+      mbar_init(su32(&ctl.phase_ready[i]), 4);
+      mbar_init(su32(&ctl.phase_done[i]), 1);
     }
+    for (int i = 0; i < kSoftWarps; ++i) ctl.phases[i] = 0;
+    ctl.status = status;
     mbar_init(su32(&ctl.done), 2);
     mbar_init(su32(&ctl.rk_full), 1);
     mbar_init(su32(&ctl.rv_full), 1);
@@ -395,9 +525,12 @@ kv8_attn_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
     };
     bool have = advance(true);
     if (have) load_q();
+#pragma unroll 1
+    for (int i = 0; i < D; i += 32) tmem_zero32(to + i);
     while (have) {
       const int t0 = w.t0, t1 = w.t1;
       float m_ref = -INFINITY, l = 0.0f;
+      int marks = 0;
       for (int j = t0, key0 = (w.u.g0 + t0) * kTileE; j < t1; ++j, ++it, ++cnt, key0 += kTileE) {
         if (!warp_wait(&ctl.s_full[t], cnt & 1u, status)) {
           alive = false;
@@ -478,17 +611,7 @@ kv8_attn_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
             m_ref = up;
             l *= alpha;
             // S_t(j) is done, so O_t(j - 1), issued before it, is too
-            if (j > t0) {
-#pragma unroll 1
-              for (int i = 0; i < D; i += 16) {
-                float o[16];
-                tmem_ld16(to + i, o);
-                tmem_wait_ld();
-#pragma unroll
-                for (int k = 0; k < 16; ++k) o[k] *= alpha;
-                tmem_st16(to + i, o);
-              }
-            }
+            if (j > t0) scale_o<D>(to, alpha);
             if (half == 1) {  // the first half's weights had the old reference
               uint32_t y[32];
               tmem_ld32(ts, y);
@@ -528,7 +651,12 @@ kv8_attn_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
             }
           }
         }
+        marks = ctl.marks[it & 3];
         tmem_wait_st();
+        if (marks & kMoved) {
+          alive = add_phases<D>(ctl, it);
+          if (!alive) break;
+        }
         warp_arrive(&ctl.p_full[t]);
       }
       if (!alive) break;
@@ -546,12 +674,22 @@ kv8_attn_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
       tc_fence_after();
       // ---- output, or a part of it ----
       const float inv = l == 0.0f ? 0.0f : 1.0f / l;  // no visible token: zeros
+      float f = inv;
+      const int e = (marks >> 16) - 128;
+      if (abs(e) <= 60) {
+        f *= pow2f(e);
+      } else {  // (one number need not hold both)
+        scale_o<D>(to, inv);
+        tmem_wait_st();
+        f = pow2_or_zero(e);
+      }
       float* part = scratch_part(a, gridDim.x, blockIdx.x, t0 == 0, kUnit, D);
 #pragma unroll 1
       for (int i = 0; i < D; i += 32) {
         uint32_t o[32];
         tmem_ld32(to + i, o);
         tmem_wait_ld();
+        tmem_zero32(to + i);  // for the next unit
         if (!out_ok) continue;
         if (whole) {
           uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + out_row * D + i);
@@ -560,8 +698,8 @@ kv8_attn_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
             uint32_t y[4];
 #pragma unroll
             for (int n = 0; n < 4; ++n)
-              y[n] = pair_from_floats<kBf16>(__uint_as_float(o[8 * k + 2 * n]) * inv,
-                                             __uint_as_float(o[8 * k + 2 * n + 1]) * inv);
+              y[n] = pair_from_floats<kBf16>(__uint_as_float(o[8 * k + 2 * n]) * f,
+                                             __uint_as_float(o[8 * k + 2 * n + 1]) * f);
             dst[k] = make_uint4(y[0], y[1], y[2], y[3]);
           }
         } else {
@@ -571,7 +709,7 @@ kv8_attn_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
             uint32_t y[4];
 #pragma unroll
             for (int n = 0; n < 4; ++n)
-              y[n] = __float_as_uint(__uint_as_float(o[4 * k + n]) * inv);
+              y[n] = __float_as_uint(__uint_as_float(o[4 * k + n]) * f);
             dst[k] = make_uint4(y[0], y[1], y[2], y[3]);
           }
         }
@@ -608,7 +746,7 @@ kv8_attn_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
           uint64_t* empty = kv ? ctl.v_empty : ctl.k_empty;
           alive = warp_wait(bars, it & 1u, status) && warp_wait(empty + st, par, status);
           if (!alive) break;
-          const int marks = ctl.marks[it & 3];
+          const int marks = ctl.marks[it & 3] & (kRagged | kEdge);
           if ((marks & kEdge) && !(alive = warp_wait(&ctl.rv_full, it & 1u, status))) break;
           const uint8_t* raw = smem + L::rk + kv * L::raw;
           uint8_t* to = smem + L::k + (2 * kv + st) * L::tile;
@@ -676,6 +814,8 @@ kv8_attn_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
         set_status(status, kStatusBadIndex);
         return -1;
       };
+      VUnit vu = {kNoUnit, kNoUnit};
+      float unit = 0.0f;  // 2^-E
       float ks = 0.0f, vs = 0.0f;
       auto scales = [&](int p) {
         if (p >= 0) {
@@ -698,7 +838,23 @@ kv8_attn_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
         const int key0 = (g0 + j) * kTileE, key = key0 + 16 * lane;
         const bool seen = pid >= 0 && key < hi && key + 16 > lo;
         const uint32_t all = __ballot_sync(0xffffffffu, seen || lane >= 8);
-        const float4 sc = seen ? make_float4(ks, __log2f(vs), 1.0f / vs, 0.0f)
+        const uint32_t live = __ballot_sync(0xffffffffu, seen);
+        if (vu.e == kNoUnit && live) {
+          vu.e = vu.top = unit_exp(__shfl_sync(0xffffffffu, vs, __ffs(live) - 1));
+          unit = pow2f(-vu.e);
+        }
+        float ratio = vs * unit;
+        const bool moved = __any_sync(0xffffffffu, seen && !near_unit(ratio));
+        int how = 0, phase = 0;
+        if (moved) {
+          const Phases ph = phases_of(vu, vs, live);
+          vu = ph.u;
+          unit = pow2f(-vu.e);
+          ratio = ph.ratio;
+          how = ph.marks;
+          phase = ph.phase;
+        }
+        const float4 sc = seen ? make_float4(ks, __log2f(ratio), 1.0f / ratio, 0.0f)
                                : make_float4(1.0f, -INFINITY, 0.0f, 0.0f);
         const int64_t off = ((((int64_t)pid * a.c.H_kv + h) << a.c.page_shift) + (key & (page - 1))) * D;
         const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, leads && pid >= 0)) * run_bytes;
@@ -706,10 +862,13 @@ kv8_attn_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
           alive = false;
           break;
         }
-        if (lane < 8) ctl.sc[it & 3][lane] = sc;
+        if (lane < 8) {
+          ctl.sc[it & 3][lane] = sc;
+          if (moved) ctl.phase[it & 3][lane] = (uint16_t)phase;
+        }
         if (lane == 0)
           ctl.marks[it & 3] =
-              (all != 0xffffffffu || key0 < lo || key0 + kTileE > hi ? kRagged : 0) |
+              ((vu.e + 128) << 16) | how | (all != 0xffffffffu || key0 < lo || key0 + kTileE > hi ? kRagged : 0) |
               (max(key0, lo) < all_lo || min(key0 + kTileE, hi) > all_hi ? kEdge : 0);
         __syncwarp();
         if (lane == 0) mbar_expect_tx(su32(&ctl.rk_full), bytes);
@@ -738,7 +897,7 @@ kv8_attn_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
   if (warp == kMmaWarp || warp == kMmaWarp1) {
     // ================= MMA issuers =================
     const uint32_t id_s = idesc_f16(kTileE, false);
-    const uint32_t id_o = idesc_f16(D, false) | (1u << 16);  // B (V) MN-major
+    const uint32_t id_o = idesc_o(D);
     const int t = warp == kMmaWarp ? 0 : 1;                  // row tile
     const uint32_t sb = su32(smem), ts = tm_s + t * 128, to = tm_o + t * D;
     const uint64_t dq = sw128_desc(sb + L::q + t * L::tile, 16, 1024);
@@ -777,7 +936,7 @@ kv8_attn_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
             const uint64_t vb = dv + (o & 1u) * (L::tile >> 4);
 #pragma unroll
             for (int x = 0; x < kTileE / 16; ++x)  // 16 keys: 8 columns of P, 2048 bytes of V
-              mma_f16_ta(to, ts + 8 * x, vb + x * (2048 >> 4), id_o, x != 0 || j != 0);
+              mma_f16_ta(to, ts + 8 * x, vb + x * (2048 >> 4), id_o, 1);  // (O starts as zeros)
             mma_commit(su32(&ctl.v_empty[o & 1u]));
             if (j + 1 == n) mma_commit(su32(&ctl.o_full[t]));
           }
