@@ -664,11 +664,14 @@ def step_quantiles(step_ms) -> dict:
     return {"p10": pick(0.10), "p50": pick(0.50), "p90": pick(0.90)}
 
 
-def kernel_revision() -> str:
+def kernel_revision(d: str = os.path.join(ROOT, "sparse_attention_decode_csa2_gb300", "csrc")) -> str:
+    """Of the sources that the benchmark's path is built from: the kv8_* files (the 8-bit
+    paged cache, which nothing of it includes or launches) are left out."""
     import hashlib
     h = hashlib.sha1()
-    d = os.path.join(ROOT, "sparse_attention_decode_csa2_gb300", "csrc")
     for n in sorted(os.listdir(d)):
+        if n.startswith("kv8"):
+            continue
         with open(os.path.join(d, n), "rb") as f:
             h.update(f.read())
     return h.hexdigest()[:12]
