@@ -707,7 +707,8 @@ kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a) {
         x.z = fmaf(y.z, f, x.z);
         x.w = fmaf(y.w, f, x.w);
       }
-      const float inv = l == 0.0f ? 0.0f : 1.0f / l;  // no visible token: zeros
+      // no visible token: zeros
+      const float inv = l == 0.0f ? 0.0f : (whole ? 1.0f : kPartOut) / l;
       x.x = x.x * inv * to_one;
       x.y = x.y * inv * to_one;
       x.z = x.z * inv * to_one;

@@ -673,7 +673,8 @@ kv8_attn_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
       ++units;
       tc_fence_after();
       // ---- output, or a part of it ----
-      const float inv = l == 0.0f ? 0.0f : 1.0f / l;  // no visible token: zeros
+      // no visible token: zeros
+      const float inv = l == 0.0f ? 0.0f : (whole ? 1.0f : kPartOut) / l;
       float f = inv;
       const int e = (marks >> 16) - 128;
       if (abs(e) <= 60) {

@@ -240,8 +240,10 @@ __device__ Range find_range(const Kv8AttnArgs& a, int worker, int workers,
 
 // Scratch: a record for each worker, then its parts of cut units, out [kUnit][D] (as if
 // the part's keys were all), max [kUnit], sum [kUnit]: [0] a part that continues a unit,
-// [1] one that starts it.  The record of the worker that starts a cut unit says how to
+// [1] one that starts it.  (out is stored small: a value of 448 * 2^120, as append stores an
+// infinity, is past fp32 and would be NaN by a weight of zero.)  The record of the worker that starts a cut unit says how to
 // join it, so that the merge kernel need not find its way again.
+constexpr float kPartOut = 0.0625f;
 struct Cut {
   int last;  // the worker with the unit's last part; -1: this worker starts no cut unit
   int token, head, rows;  // the unit's first row in q and out, its KV head's first query head
@@ -492,7 +494,8 @@ __device__ __forceinline__ void merge_parts(const Kv8AttnArgs& a, int workers, f
   auto write = [&](int row, int c4, float4 x, float m, float l) {
     const int64_t orow = out_row(a, cut.y, cut.z, row);
     *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + orow * D + c4) =
-        make_uint2(pair_from_floats<kBf16>(x.x, x.y), pair_from_floats<kBf16>(x.z, x.w));
+        make_uint2(pair_from_floats<kBf16>(x.x / kPartOut, x.y / kPartOut),
+                   pair_from_floats<kBf16>(x.z / kPartOut, x.w / kPartOut));
     if (a.lse && c4 == 0)
       a.lse[orow] =
           l == 0.0f ? -INFINITY : ((m == -INFINITY ? 0.0f : m) - headroom + __log2f(l)) * kLn2;

@@ -282,3 +282,27 @@ def test_attn_scales_that_change_with_every_block(C, n, G, page):
     q = _queries(w, 2 * n, G, BF16)
     q[:, :, 0] = 4.0
     _check_attn(C, w, q, None, scale=0.3 / 8)
+
+
+@pytest.mark.parametrize("n,G", FEW + MANY)
+def test_attn_an_infinite_value_without_weight_stays_out_of_a_long_context(C, n, G):
+    # append stores infinities as 448 at a scale of 2^120, past fp32.  A run of them, which fills the parts of several
+    # CTAs, has logits 250 powers of two below the rest (softmax weights of zero): no NaN, and lse as ever
+    def v_of(s, col, v):
+        big = (np.arange(col.max() + 1) >= 40) & (np.arange(col.max() + 1) < 80)
+        v[big[col]] = 0.0
+        v[big[col], :, 5] = 448.0
+        return v, np.where(big, 2.0 ** 120, 2.0 ** -8)
+
+    w = _fill(World(C, 92, [9001], 1, 64, 64), v_of)
+    j = np.arange(9001)
+    w.k[w.table[0, j // 64], 0, j % 64, 0] = R.encode(np.where((j // 64 >= 40) & (j // 64 < 80), -448.0, 448.0))
+    q = _queries(w, n, G, BF16)
+    q[:, :, 0] = 400.0
+    cache, batch = w.cache(), w.batch(n)
+    out, lse = C.kv8_attn(q.cuda(), cache, batch, causal=False)
+    ref = R.attention(q.double().numpy(), (w.k, w.v, w.ks, w.vs), w.table, w.lens, R.rows_of(n, 1, None), 64, False,
+                      0, 1 / 8)
+    _, tol_l = R.attention_bounds(*ref, 64, 9001, BF16)
+    assert torch.isfinite(out).all()
+    assert (np.abs(lse.double().cpu().numpy() - ref[1]) <= tol_l).all()
