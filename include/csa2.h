@@ -378,6 +378,8 @@ csa2_status csa2_sparse_attn_fp4_noalloc(const uint16_t* q_bf16, const uint8_t* 
  * step that two of them then claim reads back, or yields, what either has there).
  * Entries for tokens outside a sliding window are never read.
  *   Sequences may share pages that the step does not write.
+ * Words (scales, tables, lengths, lse, the workspace's status) are 4-byte aligned, else
+ * CSA2_ERR_INVALID_ARG (the workspace: CSA2_ERR_WORKSPACE).
  * Supported: D in {64, 128}, page in {16, 32, 64, 128}, max_pages * page <= 2^30,
  * n_pages < 2^31, T <= 2^28, S <= 2^24, H_kv <= 2^14; else
  * CSA2_ERR_UNSUPPORTED.

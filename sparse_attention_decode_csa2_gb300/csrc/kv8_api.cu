@@ -6,7 +6,8 @@
 namespace csa2 {
 namespace {
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+bool aligned16(const void* p) { return aligned(p, 16); }
 
 // The 8-bit cache and the step's batch; fills the kernels' arguments.
 csa2_status check_kv8(const csa2_kv8_cache* c, const csa2_kv8_batch* b, void* ws, Kv8Args* a) {
@@ -28,6 +29,10 @@ csa2_status check_kv8(const csa2_kv8_cache* c, const csa2_kv8_batch* b, void* ws
       return CSA2_ERR_INVALID_ARG;
   }
   if (!aligned16(c->k) || !aligned16(c->v)) return CSA2_ERR_INVALID_ARG;
+  for (const void* p : {(const void*)c->k_scale, (const void*)c->v_scale,
+                        (const void*)b->block_table, (const void*)b->kv_len,
+                        (const void*)b->cu_rows})
+    if (!aligned(p, 4)) return CSA2_ERR_INVALID_ARG;
   a->k = c->k;
   a->v = c->v;
   a->k_scale = c->k_scale;
@@ -76,7 +81,7 @@ csa2_status csa2_kv8_append(const csa2_kv8_cache* cache, const csa2_kv8_batch* b
   if ((s = check_rows(k, type, k_stride, a.H_kv, a.D)) != CSA2_OK) return s;
   if ((s = check_rows(v, type, v_stride, a.H_kv, a.D)) != CSA2_OK) return s;
   if (a.T > 0 && (!k || !v)) return CSA2_ERR_INVALID_ARG;
-  if (!ws || ws_bytes < kStatusBytes) return CSA2_ERR_WORKSPACE;
+  if (!ws || !aligned(ws, 4) || ws_bytes < kStatusBytes) return CSA2_ERR_WORKSPACE;
   if (a.S == 0 || a.T == 0) return CSA2_OK;
   return check_launch(launch_kv8_append(a, k, v, type, k_stride, v_stride, stream));
 }
@@ -90,7 +95,7 @@ csa2_status csa2_kv8_read(const csa2_kv8_cache* cache, const csa2_kv8_batch* bat
   if ((s = check_rows(k, type, stride, a.H_kv, a.D)) != CSA2_OK) return s;
   if ((s = check_rows(v, type, stride, a.H_kv, a.D)) != CSA2_OK) return s;
   if (a.T > 0 && (!k || !v)) return CSA2_ERR_INVALID_ARG;
-  if (!ws || ws_bytes < kStatusBytes) return CSA2_ERR_WORKSPACE;
+  if (!ws || !aligned(ws, 4) || ws_bytes < kStatusBytes) return CSA2_ERR_WORKSPACE;
   if (a.S == 0 || a.T == 0) return CSA2_OK;
   return check_launch(launch_kv8_read(a, k, v, type, stream));
 }
@@ -112,7 +117,7 @@ csa2_status csa2_kv8_attn(const void* q, int type, int64_t q_stride, int H,
   a.scale_log2 = softmax_scale * 1.44269504088896340736f;
   if (!(softmax_scale > 0.0f) || !(a.scale_log2 < INFINITY)) return CSA2_ERR_INVALID_ARG;
   if (a.c.T > 0 && (!q || !out)) return CSA2_ERR_INVALID_ARG;
-  if (!aligned16(out)) return CSA2_ERR_INVALID_ARG;
+  if (!aligned16(out) || !aligned(lse, 4)) return CSA2_ERR_INVALID_ARG;
   if (!ws || !aligned16(ws) || ws_bytes < csa2_kv8_workspace_size(cache, batch, H))
     return CSA2_ERR_WORKSPACE;
   if (a.c.S == 0 || a.c.T == 0) return CSA2_OK;

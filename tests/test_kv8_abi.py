@@ -84,6 +84,18 @@ def test_row_arguments_are_refused(C):
     assert _attn(C, ws=FAKE + 4) == 3
 
 
+@pytest.mark.parametrize("name", ["ks", "vs", "table", "kv_len", "cu"])
+def test_words_off_their_alignment_are_refused(C, name):
+    for f in (_append, _read, _attn):
+        assert f(C, **{name: FAKE + 2}) == 1
+
+
+def test_a_workspace_or_lse_off_its_alignment_is_refused(C):
+    assert _append(C, ws=FAKE + 2) == 3 and _read(C, ws=FAKE + 2) == 3
+    c, b = _structs(C)
+    assert C.lib.csa2_kv8_attn(FAKE, 0, 4096, 32, c, b, 1, 0, 0.1, FAKE, FAKE + 2, FAKE, 1 << 40, None) == 1
+
+
 def test_empty_batches_do_nothing(C):
     none = dict(S=0, T=0, table=None, kv_len=None)
     for kw in (none, dict(T=0)):
