@@ -412,8 +412,10 @@ typedef struct csa2_kv8_batch {
  *   [-100, 120]; the scale becomes max(old scale, need), or need where a = 0 (the
  *   page starts).  If it grew, the rows [0, a) become E4M3(code * (old /
  *   new)); the new rows are E4M3(x * (1 / scale)), both to nearest even.
- *   Bit-exact.  Infinities saturate, a NaN is stored as the E4M3 NaN.  The
- *   rows of the page past b are left as they were.
+ *   Bit-exact.  A NaN is stored as the E4M3 NaN and does not count in absmax.  An
+ *   infinity does: it is stored as 448 * 2^120, beside which the block's finite values,
+ *   older rows included, become zeros, and the scale stays until the page starts
+ *   anew.  The rows of the page past b are left as they were.
  *   No two of the step's tokens may share a page row, and no two sequences a
  *   page that the step writes: the contents would depend on timing.
  *   ws       at least 256 bytes (the status word).
@@ -460,6 +462,10 @@ csa2_status csa2_kv8_read(const csa2_kv8_cache* cache, const csa2_kv8_batch* bat
  *   ws       at least csa2_kv8_workspace_size(cache, batch, H) bytes, 16-byte
  *            aligned.
  * H must be a multiple of H_kv, with H / H_kv <= 256 (else CSA2_ERR_UNSUPPORTED).
+ * A call takes one kernel for all its sequences, by T * H / (H_kv * S), the mean of the
+ * query rows that share a KV head (T with the rows of no sequence): up to 32 the one
+ * for few rows, past that the one for prompts.  A step that mixes single tokens with
+ * long chunks is faster as two calls.
  */
 csa2_status csa2_kv8_attn(const void* q, int type, int64_t q_stride, int H,
                           const csa2_kv8_cache* cache, const csa2_kv8_batch* batch, int causal,

@@ -640,7 +640,9 @@ def _kv8_call(index: int, where: str, fn, *args) -> None:
 
 
 def make_kv8_workspace(cache: Kv8Cache, batch: Kv8Batch, heads: int = 0) -> torch.Tensor:
-    """Workspace of the kv8 calls (heads > 0: of kv8_attn with that many query heads)."""
+    """Workspace of the kv8 calls (heads > 0: of kv8_attn with that many query heads).  A
+    call that is given none makes its own, whose status (bad entries, timeout) nobody
+    sees: pass one and read it with ``read_status``."""
     with torch.cuda.device(cache.device):
         n = int(lib.csa2_kv8_workspace_size(cache._ref, batch._ref, heads))
         ws = torch.empty(n, dtype=torch.uint8, device=cache.device)

@@ -8,7 +8,7 @@ import pytest
 import torch
 
 import kv8_ref as R
-from test_gpu_kv8 import BF16, FP16, World, _check_attn
+from test_gpu_kv8 import BF16, FP16, World, _check_attn, _rows
 
 pytestmark = pytest.mark.gpu
 
@@ -306,3 +306,21 @@ def test_attn_an_infinite_value_without_weight_stays_out_of_a_long_context(C, n,
     _, tol_l = R.attention_bounds(*ref, 64, 9001, BF16)
     assert torch.isfinite(out).all()
     assert (np.abs(lse.double().cpu().numpy() - ref[1]) <= tol_l).all()
+
+
+@pytest.mark.parametrize("D,page", [(64, 16), (128, 128)])
+def test_append_an_infinity_beside_finite_values(C, D, page):
+    # the whole block goes to the largest scale, older rows too, until its page starts anew
+    Hk, steps = 2, [page + 5, 1, 2, page, page]
+    w = World(C, 93, [sum(steps)], Hk, D, page)
+    cache, length = w.cache(), 0
+    for i, n in enumerate(steps):
+        length += n
+        k, v = (_rows(w.rng, n, Hk, D, FP16, 3.0) for _ in range(2))
+        if i == 1:
+            k[0, 0, 3], v[0, 1, 7], v[0, 1, 8] = math.inf, -math.inf, math.nan
+        C.kv8_append(cache, w.batch(n, None, [length]), k.cuda(), v.cuda())
+        for codes, sc, x in ((w.k, w.ks, k), (w.v, w.vs, v)):
+            R.append(codes, sc, x.double().numpy(), w.table, [length], [(0, n)], page)
+        w.same(cache)
+    assert w.ks[w.table[0, 1], 0] == 2.0 ** 120 and w.ks[w.table[0, 2], 0] < 1.0
