@@ -19,9 +19,9 @@
 //                   reference, which gives a logit at the reference a weight of 2^7;
 //                   only where they grow past fp16's range (seen from their sums)
 //                   does it move, O is rescaled and the weights are formed again.
-//                   It moves by whole powers of two, to the next one above the
-//                   largest logit: what was formed before is scaled exactly, the
-//                   fp16 weights of the tile's first half too
+//                   It moves to the largest logit, whose weight is exact then; in a
+//                   tile's second half by whole powers of two, so that the fp16 weights
+//                   of the first half are scaled without a second rounding
 //   warps 8-11      dequantisers: E4M3 codes to fp16, 128-byte swizzled, double
 //                   buffered; keys that no row of the unit may see, and those of
 //                   pages outside the cache, become zeros
@@ -69,9 +69,8 @@ constexpr int kSoftRegs = 184, kDeqRegs = 80, kMmaRegs = 64;
 static_assert(2 * kSoftRegs + kDeqRegs + kMmaRegs <= 512, "register split");
 constexpr int kUnit = 256;      // query rows of a unit
 constexpr int kTileE = 128;     // keys of a tile (and rows of a row tile)
-// log2 of the weight at the reference (up to one less for the largest logit: the
-// reference is whole; with 8 the chunk below took 778 us, with 7 772), and the largest
-// sum of 16 weights: no weight is above it, which fp16 holds (65504)
+// log2 of the weight at the reference, and the largest sum of 16 weights: no weight is
+// above it, which fp16 holds (65504)
 constexpr float kHeadroom = 7.0f, kMostSum = 57344.0f;
 // The largest reference with which exponents are formed by one fused
 // multiply-add: its rounding is then at most 2^-8 of a power of two, that of the
@@ -605,9 +604,11 @@ kv8_attn_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
                 x = fmaxf(x, fmaf(mx, fmaxf(crow * b.x, 1.17549435e-38f), b.y));
               }
             }
-            // by whole powers of two, so that what was formed with the old one keeps its bits
-            const float up = fmaxf(m_ref, ceilf(x)), down = m_ref - up;
-            const float alpha = !(up > m_ref) ? 1.0f : down < -126.0f ? 0.0f : pow2f((int)down);
+            // in the second half by whole powers of two, so that the first half's weights keep
+            // their bits (past 2^64 nothing of them is left)
+            float up = fmaxf(m_ref, x);
+            if (half == 1 && up - m_ref < 64.0f) up = m_ref + ceilf(up - m_ref);
+            const float alpha = up > m_ref ? ex2(m_ref - up) : 1.0f;
             m_ref = up;
             l *= alpha;
             // S_t(j) is done, so O_t(j - 1), issued before it, is too
