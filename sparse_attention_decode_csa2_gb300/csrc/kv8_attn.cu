@@ -42,7 +42,7 @@
 //
 // Measured (GB300; the copy peak is 6.77 TB/s):
 //   one token of 32 sequences of up to 64K tokens (64 heads over 8, D = 128):
-//     468 us, 6.8 TB/s: the copy's rate
+//     465 us, 6.8 TB/s: the copy's rate
 //   17 sequences of up to 9K tokens (40 heads over 8, D = 64): 34.8 us (3.2 TB/s).
 //     Of them 5 us go before the first tile (ranges, pages, first loads) and 4 to
 //     the merge; between, the warps wait for their own loads and results
@@ -50,7 +50,7 @@
 //   4 drafted tokens of 24 sequences of up to 16K tokens (32 heads over 4, D = 128;
 //     32 rows a KV head): 90 us (3.3 TB/s), tensor pipe 40 % busy, 35 % of issue
 //     slots: the same waits, with eight warps an SM
-// Following the V scales costs 463 -> 468, 32.8 -> 34.8 and 86 -> 90 us of these: a
+// Following the V scales costs 463 -> 465, 32.8 -> 34.8 and 86 -> 90 us of these: a
 // comparison a tile and the code of the rare case.  (Tiles whose second half came by
 // itself by going round the loop once more: 494, 35.8 and 94.)
 #include <type_traits>

@@ -36,7 +36,7 @@
 //   (warp 15 only completes its warpgroup, for the register split)
 // Measured (GB300; cuBLAS bf16 1.89 PFLOP/s): a chunk of 4096 rows over 16K tokens
 // (32 heads over 8, D = 128) 776 us, 1.24 PFLOP/s of products that the mask leaves,
-// 65 %; tensor pipe 56 % busy, XU 28 %, 46 % of issue slots.  A tile of keys takes
+// 65 %; tensor pipe 55 % busy, XU 28 %, 47 % of issue slots.  A tile of keys takes
 // 3300 to 3700 cycles, of which its MMAs 2048 (D = 128); each row tile goes through
 // softmax (1950 cycles, two warps a scheduler), P to O, S again, one after the other,
 // since P overwrites S.  Prompts of 10007 rows through a window of 1024 (16 heads
@@ -77,7 +77,7 @@ constexpr float kHeadroom = 7.0f, kMostSum = 57344.0f;
 // logits themselves.
 constexpr float kFused = 65536.0f;
 // (a unit's queries and output count as two granules: prompts of 10007 rows through a
-// window of 1024 with one to three 104.5, 96.6, 97.6 us)
+// window of 1024 with one to three 104.5, 96.6, 97.6 us when they took 97)
 using Work = Shape<kUnit, kTileE, 2>;
 constexpr uint32_t kAtom = 128 * 128;            // bytes: 128 rows of 64 fp16 channels
 

@@ -23,7 +23,8 @@
 // 128 channels, page 64, in 24.6 us, 5.0 TB/s of rows read and codes written (the
 // copy peak is 6.77; 18.2 us); with 256 threads a team 32.8 us.  Maxima by packed
 // 16-bit instructions, half as many, took 26.5 us: instructions do not bound it.
-// Steps of a few tokens take the call's own time (12 us through the binding).
+// Steps of a few tokens take the call's own time (12 us through the binding; 3 to 4 us
+// on the device).
 #include <cuda_bf16.h>
 
 #include "kv8.cuh"
