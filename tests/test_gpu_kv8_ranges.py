@@ -324,3 +324,19 @@ def test_append_an_infinity_beside_finite_values(C, D, page):
             R.append(codes, sc, x.double().numpy(), w.table, [length], [(0, n)], page)
         w.same(cache)
     assert w.ks[w.table[0, 1], 0] == 2.0 ** 120 and w.ks[w.table[0, 2], 0] < 1.0
+
+
+@pytest.mark.parametrize("n,G", FEW + MANY)
+@pytest.mark.parametrize("D,page", [(64, 16), (128, 64)])
+@pytest.mark.parametrize("causal,window", [(True, 90), (False, 0)])
+@pytest.mark.parametrize("apart", [30, 54])
+def test_attn_outlier_blocks_and_rows_that_do_not_see_them(C, n, G, D, page, causal, window, apart):
+    # every third block has an outlier; through the window some rows of a unit see it and others do not
+    def v_of(s, col, v):
+        big = np.arange(col.max() + 1) % 3 == s
+        v[big[col]] = 0.0
+        v[big[col], :, 5] = 100.0
+        return v, np.where(big, 2.0 ** (apart - 8), 2.0 ** -8)
+
+    w = _fill(World(C, 94, [600, 431, 150], 1, D, page), v_of)
+    _check_attn(C, w, _queries(w, 3 * n, G, BF16), None, causal, window)
